@@ -320,6 +320,248 @@ w4a16_status w4a16_pack_int4_kshuffle(const uint8_t* q, int64_t N, int64_t K,
 w4a16_status w4a16_unpack_int4_kshuffle(const int32_t* packed, int64_t N,
                                         int64_t K, uint8_t* q);
 
+/* ==========================================================================
+ * Between two weight products: rotary positions, the paged key/value cache,
+ * attention of drafted tokens over it, and the scores of given tokens.
+ *
+ * Each call takes one struct of arguments (every pointer a device pointer
+ * unless it says otherwise, owned by the caller) and a stream; it checks the
+ * arguments, enqueues its kernels and returns. What only the device knows
+ * (positions, slots, lengths, page numbers, token ids) is checked there: no
+ * value in those arrays makes a kernel read or write outside the buffers
+ * that the struct names; each call says what it does with such values.
+ * Strides count elements. The last dimension of every array is contiguous.
+ * ======================================================================== */
+
+/* How a cache holds its values. */
+typedef enum {
+  W4A16_KV_SAME = 0,        /* in the activation dtype, no scales */
+  W4A16_KV_E4M3 = 1,        /* 8-bit float (4 exponent, 3 mantissa bits, no infinities) */
+  W4A16_KV_INT8 = 2         /* -127..127 */
+} w4a16_kv_format;
+
+/* A paged cache. Slot s = page * page_size + offset holds one token. A page
+ * holds each head's tokens side by side, so that the tokens of one head that
+ * an attention workgroup reads are one contiguous run per page. */
+typedef struct {
+  void* k;                  /* [pages, heads, page_size, head_dim], 16-byte aligned */
+  void* v;                  /* the same */
+  float* k_scale;           /* [pages, heads, page_size]: value = code * scale; NULL for SAME */
+  float* v_scale;
+  int64_t pages;
+  int32_t page_size;        /* a power of two, 16..4096 */
+  int32_t heads;            /* key/value heads */
+  int32_t head_dim;         /* 8..256: a multiple of 8, of 16 above 128 and where quantised */
+  int32_t format;           /* w4a16_kv_format */
+} w4a16_kv_cache_t;
+
+/* How rotary frequencies are scaled for contexts longer than trained. With
+ * f_i = base^(-2i/r), i < r/2 (r = rotated dims):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     base replaced by base * factor^(r / (r - 2))
+ *   BANDS   by the number of turns t_i = original * f_i / 2 pi that the
+ *           trained context makes: f_i where t_i >= high, f_i / factor where
+ *           t_i <= low, in between linear in t_i
+ *   RAMP    as BANDS, but linear in i between the (fractional, then rounded
+ *           outwards) indices where t_i = high and t_i = low */
+typedef enum {
+  W4A16_ROPE_NONE = 0,
+  W4A16_ROPE_LINEAR = 1,
+  W4A16_ROPE_NTK = 2,
+  W4A16_ROPE_BANDS = 3,
+  W4A16_ROPE_RAMP = 4
+} w4a16_rope_scaling;
+
+typedef struct {
+  double base;              /* > 1 */
+  double factor;            /* >= 1 (ignored for NONE) */
+  double original;          /* trained context length, > 0 (BANDS, RAMP) */
+  double low, high;         /* turns, 0 < low < high (BANDS, RAMP) */
+  int32_t rot_dim;          /* r: even, 2..256 */
+  int32_t scaling;          /* w4a16_rope_scaling */
+} w4a16_rope_scale_t;
+
+/*
+ * w4a16_rope_frequencies - the r/2 frequencies above, in fp64, written to
+ * inv_freq (host memory). Host only. Errors: NULL, SHAPE, VALUE.
+ */
+w4a16_status w4a16_rope_frequencies(const w4a16_rope_scale_t* scale, double* inv_freq);
+
+/*
+ * w4a16_rope_table - table[p] = (amplitude cos(p f_i) for i < r/2, then
+ * amplitude sin(p f_i)), fp32 [positions, r], for p = 0..positions-1. Angles
+ * and their sine and cosine are formed in fp64 and rounded once: an fp32
+ * angle of position 100000 is off by up to 4e-3. inv_freq: host memory, r/2
+ * values. amplitude: 1, or the attention factor of a scaled context.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_rope_table(const double* inv_freq, int32_t rot_dim, double amplitude,
+                              int64_t positions, float* table, void* stream);
+
+/* Rotation of a head x by row p of a table, i < r/2, pair (a, b) = (i, i + r/2)
+ * or, interleaved, (2i, 2i + 1):
+ *   y[a] = x[a] cos_i - x[b] sin_i,  y[b] = x[b] cos_i + x[a] sin_i,
+ * dims from r on unchanged; fp32 arithmetic, one rounding to the dtype. */
+typedef struct {
+  const void* x;            /* [tokens, heads, head_dim], 16-byte aligned */
+  void* out;                /* the same shape; x itself is allowed (then with x's strides) */
+  const int64_t* positions; /* [tokens]; outside 0..table_rows-1: rotated dims become NaN */
+  const float* table;       /* [table_rows, rot_dim], 16-byte aligned */
+  int64_t tokens;
+  int64_t x_token, x_head;  /* strides, multiples of 8 */
+  int64_t out_token, out_head;
+  int64_t table_rows;
+  int32_t heads, head_dim;  /* head_dim: a multiple of 8, 8..256 */
+  int32_t rot_dim;          /* even, 2..head_dim */
+  int32_t interleaved;      /* 0: halves, 1: neighbours */
+  int32_t inverse;          /* 1: rotate back (the transpose) */
+  int32_t dtype;
+} w4a16_rope_t;
+
+/*
+ * w4a16_rope - the rotation of every head. Errors: NULL, SHAPE, DTYPE, ALIGN
+ * (a pointer, or a stride that is no multiple of 8), DEVICE, HIP.
+ */
+w4a16_status w4a16_rope(const w4a16_rope_t* args, void* stream);
+
+typedef struct {
+  w4a16_kv_cache_t cache;
+  const void* k;            /* [tokens, cache.heads, head_dim] */
+  const void* v;
+  const int64_t* slots;     /* [tokens]; outside 0..pages*page_size-1 (e.g. -1): not written */
+  const void* q;            /* [tokens, q_heads, head_dim] rotated into q_out, or NULL */
+  void* q_out;              /* q itself is allowed (then with q's strides) */
+  const int64_t* positions; /* [tokens], or NULL: nothing is rotated */
+  const float* table;       /* as for w4a16_rope */
+  int64_t tokens;
+  int64_t k_token, k_head, v_token, v_head, q_token, q_head, out_token, out_head;
+  int64_t table_rows;
+  int32_t q_heads;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t dtype;            /* of k, v, q, q_out */
+} w4a16_kv_write_t;
+
+/*
+ * w4a16_kv_write - rotates q and k, and writes k and v into their slots, one
+ * pass over the projection's output. Quantised formats hold, for each token
+ * and head, scale = amax / top (top = 448 or 127, amax the largest magnitude
+ * of the rotated fp32 head) and code = round-to-even(x * (top / amax)). A
+ * head with amax < 2^-100 is stored as scale 0 and codes 0; a head that
+ * holds an infinity or NaN as scale NaN and codes 0. Of two tokens with one
+ * slot either may stay.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_kv_write(const w4a16_kv_write_t* args, void* stream);
+
+typedef struct {
+  w4a16_kv_cache_t cache;
+  const int64_t* slots;     /* [tokens]; outside the cache: zeros are returned */
+  void* k_out;              /* [tokens, cache.heads, head_dim], contiguous, 16-byte aligned */
+  void* v_out;
+  int64_t tokens;
+  int32_t dtype;            /* of k_out and v_out (SAME: of the cache) */
+  int32_t reserved;         /* 0 */
+} w4a16_kv_read_t;
+
+/*
+ * w4a16_kv_read - code * scale of the tokens in the given slots, rounded once.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_kv_read(const w4a16_kv_read_t* args, void* stream);
+
+typedef struct {
+  w4a16_kv_cache_t cache;
+  const void* q;             /* [tokens, q_heads, head_dim]; sequence b has rows
+                                q_starts[b]..q_starts[b+1]-1 */
+  void* out;                 /* [tokens, q_heads, head_dim], contiguous */
+  float* lse;                /* [tokens, q_heads] natural log of the softmax denominator */
+  const int32_t* block_table;/* [sequences, table_pages]: token t of sequence b is in page
+                                block_table[b][t / page_size], offset t % page_size */
+  const int32_t* kv_lens;    /* [sequences]: cached tokens, the new ones (the last) included */
+  const int32_t* q_starts;   /* [sequences + 1], from 0 to tokens, not decreasing */
+  const uint64_t* mask;      /* [tokens, mask_words], or NULL */
+  int64_t tokens;
+  int64_t q_token, q_head;   /* strides, multiples of 8 */
+  int64_t table_stride;      /* of block_table */
+  int32_t sequences;
+  int32_t table_pages;
+  int32_t max_q;             /* most new tokens of a sequence; rows past it are not computed */
+  int32_t q_heads;           /* a multiple of cache.heads: query head h reads head h / (q_heads / heads) */
+  int32_t mask_words;
+  int32_t dtype;             /* of q, out, and of a SAME cache */
+  float scale;               /* of the scores, finite */
+  int32_t reserved;          /* 0 */
+} w4a16_tree_attention_t;
+
+/*
+ * w4a16_tree_attention - attention of each sequence's new tokens over its
+ * cached ones. With n new tokens and len cached ones (the new ones written
+ * before the call), new token i sees all of the first len - n, and of the new
+ * ones j (at cache position len - n + j) those whose bit is set: bit j % 64 of
+ * mask[q_starts[b] + i][j / 64] (a drafted token: its ancestors and itself).
+ * Without a mask j <= i: plain decoding (n = 1) and prompts in chunks.
+ *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t),  lse = ln sum_t p_t
+ * over the tokens t that i sees; where it sees none, out = 0 and lse = -inf.
+ * What a token does not see does not reach it, whatever its value (infinities
+ * and NaN included). Tokens past table_pages * page_size and tokens on pages
+ * outside 0..pages-1 are seen by none. Lengths below 0 count as 0.
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to 16 bits for the matrix cores (bf16 in front of 8-bit codes, else
+ * the dtype).
+ * Scratch: `workspace` as for w4a16_gemm_ws (counters first, zero before
+ * first use), of at least w4a16_tree_attention_workspace_bytes.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, VALUE (scale), WORKSPACE, DEVICE, HIP.
+ */
+w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* args, void* workspace,
+                                  int64_t ws_bytes, void* stream);
+
+/*
+ * w4a16_tree_attention_workspace_bytes - scratch that any call with these
+ * sizes needs (host only; num_cus as for w4a16_workspace_bytes).
+ * Errors: NULL, SHAPE.
+ */
+w4a16_status w4a16_tree_attention_workspace_bytes(int32_t sequences, int32_t max_q,
+                                                  int32_t q_heads, int32_t kv_heads,
+                                                  int32_t head_dim, int32_t num_cus,
+                                                  int64_t* bytes);
+
+typedef struct {
+  const void* logits;       /* [tokens, vocab], aligned to its elements */
+  const int64_t* ids;       /* [tokens]; outside 0..vocab-1: its log probability is NaN */
+  float* logprobs;          /* [tokens] */
+  float* entropy;           /* [tokens] */
+  float* top_logprobs;      /* [tokens, top_k], or NULL when top_k is 0 */
+  int64_t* top_ids;         /* the same */
+  int64_t tokens;
+  int64_t row_stride;       /* of logits */
+  int64_t vocab;            /* 1..2^30 */
+  int32_t top_k;            /* 0..64, at most vocab */
+  int32_t dtype;            /* w4a16_dtype, or W4A16_F32 */
+} w4a16_token_logprobs_t;
+#define W4A16_F32 2
+
+/*
+ * w4a16_token_logprobs - one pass over each row x of logits:
+ *   logprobs = x[id] - lse,  lse = ln sum_i exp(x_i),
+ *   entropy  = -sum_i p_i ln p_i,  p = softmax(x)  (terms with p_i = 0 are 0),
+ *   the top_k largest logits, descending, equal ones by lowest index: their
+ *   log probabilities and indices.
+ * fp32 throughout. A row that holds NaN or +infinity, or -infinity alone, has
+ * no softmax: its log probabilities and entropy are NaN (its top_ids are
+ * still top_k different indices, NaN ordered as -infinity).
+ * Scratch: as for w4a16_tree_attention, of at least
+ * w4a16_token_logprobs_workspace_bytes.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.
+ */
+w4a16_status w4a16_token_logprobs(const w4a16_token_logprobs_t* args, void* workspace,
+                                  int64_t ws_bytes, void* stream);
+
+/* Scratch of w4a16_token_logprobs (host only). Errors: NULL, SHAPE. */
+w4a16_status w4a16_token_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int32_t top_k,
+                                                  int32_t num_cus, int64_t* bytes);
+
 /*
  * Message of the calling thread's last failed call ("" if none): why the
  * problem was refused, as PR #43731's can_implement (Code section) returns

@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +23,10 @@ ARCH = "gfx950"
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wall", "-Wno-unused-function"]
-SOURCES = ["w4a16_host.cpp", "w4a16_kernels.hip", "w4a16_noalloc.hip"]
+SOURCES = ["w4a16_host.cpp", "w4a16_kernels.hip", "w4a16_noalloc.hip", "serve_host.cpp",
+           "rope_kv.hip", "token_logprobs.hip", "tree_attn_f16_same.hip", "tree_attn_f16_e4m3.hip",
+           "tree_attn_f16_int8.hip", "tree_attn_bf16_same.hip", "tree_attn_bf16_e4m3.hip",
+           "tree_attn_bf16_int8.hip"]
 
 
 def hipcc() -> str:
@@ -35,14 +39,15 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link the shared library."""
     cc = hipcc()
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(CSRC, src + ".o")
+    objs = [os.path.join(CSRC, src + ".o") for src in SOURCES]
+    cmds = []
+    for src, obj in zip(SOURCES, objs):
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [cc, *HIP_FLAGS, *lang, "-I", os.path.join(ROOT, "include"), "-c",
-               os.path.join(CSRC, src), "-o", obj]
-        _run(cmd, verbose)
-        objs.append(obj)
+        cmds.append([cc, *HIP_FLAGS, *lang, "-I", os.path.join(ROOT, "include"), "-c",
+                     os.path.join(CSRC, src), "-o", obj])
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        for _ in pool.map(lambda c: _run(c, verbose), cmds):
+            pass
     tmp = LIB + ".tmp"
     _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)

@@ -1,0 +1,141 @@
+// Internal interface between the host side (serve_host.cpp) and the gfx950
+// kernels of the operators around the weight products: rotary positions, the
+// paged key/value cache, attention of drafted tokens, token scores.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/w4a16.h"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+
+// Shared with w4a16_host.cpp: records the calling thread's message and
+// returns `st`; and the current device's CU count (DEVICE unless gfx950).
+w4a16_status report(w4a16_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+w4a16_status current_device(int* num_cus);
+
+// A paged cache as the kernels see it: page_size = 1 << page_shift.
+struct KvView {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int32_t page_shift, heads, dim;
+};
+
+// Lanes that hold one head, 8 dims each: the power of two that covers dim.
+inline int lanes_per_head(int dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
+
+struct RopeTableParams {
+  double inv_freq[128];
+  double amplitude;
+  float* table;
+  int64_t positions;
+  int32_t half;             // rotated dims / 2
+};
+
+// One kernel rotates (hkv = 0), writes the cache (hq = 0, table null) or
+// does both. Heads of a token are counted q, then k, then v.
+struct RopeKvParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  const int64_t* positions;
+  const int64_t* slots;
+  const float* table;       // null: nothing is rotated
+  KvView cache;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  int64_t table_rows;
+  int32_t tokens, hq, hkv, dim, rot;
+  int32_t interleaved, inverse;
+  int32_t per_unit;         // heads that one lane group takes in turn
+  int32_t units_per_token;
+};
+
+struct KvReadParams {
+  KvView cache;
+  const int64_t* slots;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int32_t tokens;
+  int32_t per_unit, units_per_token;
+};
+
+// ---- token scores
+constexpr int kScoreThreads = 256;
+constexpr int kScorePerThread = 32;                       // logits of a tile that a thread holds
+constexpr int kScoreTile = kScoreThreads * kScorePerThread;
+constexpr int kScoreMaxTop = 64;
+constexpr int kScoreMaxSplits = 64;                       // parts of a row: lanes of the last wave
+// What one part of a row hands over: max, sum, weighted sum, and top_k keys.
+__host__ __device__ constexpr int64_t score_part_bytes(int top_k) { return 16 + (int64_t)top_k * 8; }
+
+struct ScoreParams {
+  const void* logits;
+  const int64_t* ids;
+  float* logprobs;
+  float* entropy;
+  float* top_logprobs;
+  int64_t* top_ids;
+  int64_t row_stride;
+  char* parts;              // [tokens][splits] parts (splits > 1)
+  int32_t* counters;        // [tokens], zero between launches
+  int32_t tokens, vocab, top_k;
+  int32_t splits;           // parts of a row
+  int32_t part;             // logits of a part: a multiple of kScoreTile
+};
+
+// ---- attention over the paged cache
+constexpr int kAttnWaves = 4;
+constexpr int kAttnTile = 32;            // tokens that a wave multiplies at a time
+constexpr int kAttnStep = kAttnWaves * kAttnTile;  // tokens of a workgroup's step
+constexpr int kAttnMaxSplits = 256;      // parts of a sequence
+// Head dims a kernel is built for: the next of 64, 128, 256.
+inline int attn_dim_block(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+// Row blocks of 16 (row = new token and query head of one key/value head) that
+// a wave holds: the more, the fewer times keys and values are read.
+inline int attn_row_blocks(int64_t rows, int dim) {
+  const int most = dim > 128 ? 2 : 4;
+  const int need = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  return need < most ? need : most;
+}
+// Floats of one part: rows of sums, then each row's maximum and denominator.
+__host__ __device__ constexpr int64_t attn_part_floats(int rows, int dim_block) {
+  return (int64_t)rows * (dim_block + 2);
+}
+
+struct AttnParams {
+  KvView cache;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  const uint64_t* mask;     // null: causal
+  float* parts;             // [items][attn_part_floats]
+  int32_t* counters;        // one per (sequence, row block, head), zero between launches
+  int64_t q_token, q_head, table_stride;
+  int32_t tokens, sequences, table_pages, max_q, hq, group, mask_words;
+  int32_t target;           // work items aimed at; 0: never split a sequence
+  int32_t grid;
+  float scale_log2;         // scale * log2(e)
+};
+
+// One per dtype and format, each a source file of its own (build time).
+hipError_t attn_f16_same(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_f16_e4m3(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_f16_int8(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_bf16_same(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_bf16_e4m3(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_bf16_int8(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t launch_rope_table(const RopeTableParams& p, hipStream_t stream);
+hipError_t launch_rope_kv(const RopeKvParams& p, int dtype, int format, hipStream_t stream);
+hipError_t launch_kv_read(const KvReadParams& p, int dtype, int format, hipStream_t stream);
+hipError_t launch_token_logprobs(const ScoreParams& p, int dtype, hipStream_t stream);
+
+}  // namespace w4a16

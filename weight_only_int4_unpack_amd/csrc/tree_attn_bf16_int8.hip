@@ -1,0 +1,8 @@
+// Attention over a paged cache: bf16 activations, int8 cache.
+#include "tree_attn_kernel.h"
+
+namespace w4a16 {
+hipError_t attn_bf16_int8(const AttnParams& p, int row_blocks, hipStream_t stream) {
+  return serve::launch_attn_rows<serve::BF16, W4A16_KV_INT8>(p, row_blocks, stream);
+}
+}  // namespace w4a16

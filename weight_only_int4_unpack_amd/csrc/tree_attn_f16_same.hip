@@ -1,0 +1,8 @@
+// Attention over a paged cache: fp16 activations, 16-bit cache.
+#include "tree_attn_kernel.h"
+
+namespace w4a16 {
+hipError_t attn_f16_same(const AttnParams& p, int row_blocks, hipStream_t stream) {
+  return serve::launch_attn_rows<serve::F16, W4A16_KV_SAME>(p, row_blocks, stream);
+}
+}  // namespace w4a16

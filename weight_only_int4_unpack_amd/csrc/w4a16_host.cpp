@@ -732,6 +732,26 @@ w4a16_status gemm_common(const void* a, const int32_t* b_q, const void* scales,
 
 }  // namespace
 
+namespace w4a16 {
+
+w4a16_status report(w4a16_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+
+w4a16_status current_device(int* num_cus) {
+  DeviceState* ds = nullptr;
+  const w4a16_status st = device_state(&ds);
+  if (st == W4A16_OK) *num_cus = ds->num_cus;
+  return st;
+}
+
+}  // namespace w4a16
+
 extern "C" {
 
 w4a16_status w4a16_gemm(const void* a, const int32_t* b_q, const void* scales,

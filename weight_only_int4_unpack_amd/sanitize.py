@@ -1,10 +1,10 @@
 """Sanitizer build of the host side, and the C-ABI tests run against it.
 
-Builds ``libw4a16_asan.so`` from ``csrc/w4a16_host.cpp`` (argument checks,
-route/tile selector, workspace bookkeeping, host pack/unpack) with g++ under
+Builds ``libw4a16_asan.so`` from ``csrc/w4a16_host.cpp`` and ``csrc/serve_host.cpp``
+(argument checks, route/tile selector, workspace bookkeeping, host pack/unpack) with g++ under
 AddressSanitizer and UndefinedBehaviorSanitizer (every finding fatal), linked
 against host-only stand-ins for the kernels (``csrc/sanitize_stubs.cpp``),
-then runs ``tests/test_abi.py`` with that library in place of the real one
+then runs ``tests/test_abi.py`` and ``tests/test_serve_abi.py`` with that library in place of the real one
 (``W4A16_LIB``) and the sanitizer runtimes preloaded into Python. CPU only:
 no GPU code is built or run.
 
@@ -28,7 +28,8 @@ def build() -> str:
     cmd = ["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fPIC", "-shared",
            "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
            "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", f"-I{os.path.join(ROOT, 'include')}",
-           os.path.join(CSRC, "w4a16_host.cpp"), os.path.join(CSRC, "sanitize_stubs.cpp"),
+           os.path.join(CSRC, "w4a16_host.cpp"), os.path.join(CSRC, "serve_host.cpp"),
+           os.path.join(CSRC, "sanitize_stubs.cpp"),
            f"-L{ROCM}/lib", "-lamdhip64", f"-Wl,-rpath,{ROCM}/lib", "-o", OUT]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -52,7 +53,8 @@ def main() -> int:
     env["CUDA_VISIBLE_DEVICES"] = ""
     env["HIP_VISIBLE_DEVICES"] = ""
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider",
-                        os.path.join(ROOT, "tests", "test_abi.py")], cwd=ROOT, env=env)
+                        os.path.join(ROOT, "tests", "test_abi.py"),
+                        os.path.join(ROOT, "tests", "test_serve_abi.py")], cwd=ROOT, env=env)
     return r.returncode
 
 

@@ -84,10 +84,24 @@ def lib() -> ctypes.CDLL:
     L.w4a16_gemm_kpacked.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i64, i64, i64, i32, vp]
     L.w4a16_pack_int4_kshuffle.argtypes = [vp, i64, i64, vp]
     L.w4a16_unpack_int4_kshuffle.argtypes = [vp, i64, i64, vp]
+    f64, args = ctypes.c_double, ctypes.c_char_p   # args: a packed argument struct
+    L.w4a16_rope_frequencies.argtypes = [args, vp]
+    L.w4a16_rope_table.argtypes = [vp, i32, f64, i64, vp, vp]
+    L.w4a16_rope.argtypes = [args, vp]
+    L.w4a16_kv_write.argtypes = [args, vp]
+    L.w4a16_kv_read.argtypes = [args, vp]
+    L.w4a16_tree_attention.argtypes = [args, vp, i64, vp]
+    L.w4a16_tree_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32,
+                                                       ctypes.POINTER(i64)]
+    L.w4a16_token_logprobs.argtypes = [args, vp, i64, vp]
+    L.w4a16_token_logprobs_workspace_bytes.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
     for f in ("w4a16_gemm", "w4a16_gemm_bias", "w4a16_gemm_planned", "w4a16_gemm_ws",
               "w4a16_workspace_bytes", "w4a16_gemm_noalloc", "w4a16_plan", "w4a16_plan_route",
               "w4a16_dequant", "w4a16_pack_int4", "w4a16_unpack_int4", "w4a16_gemm_kpacked",
-              "w4a16_pack_int4_kshuffle", "w4a16_unpack_int4_kshuffle"):
+              "w4a16_pack_int4_kshuffle", "w4a16_unpack_int4_kshuffle",
+              "w4a16_rope_frequencies", "w4a16_rope_table", "w4a16_rope", "w4a16_kv_write",
+              "w4a16_kv_read", "w4a16_tree_attention", "w4a16_tree_attention_workspace_bytes",
+              "w4a16_token_logprobs", "w4a16_token_logprobs_workspace_bytes"):
         getattr(L, f).restype = ctypes.c_int
     L.w4a16_last_error.restype = ctypes.c_char_p
     L.w4a16_last_error.argtypes = []
