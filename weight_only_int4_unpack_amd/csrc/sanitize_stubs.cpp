@@ -31,10 +31,10 @@ hipError_t launch_rope_table(const RopeTableParams&, hipStream_t) { return hipEr
 hipError_t launch_rope_kv(const RopeKvParams&, int, int, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_kv_read(const KvReadParams&, int, int, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_token_logprobs(const ScoreParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_f16_same(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_f16_e4m3(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_f16_int8(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_bf16_same(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_bf16_e4m3(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
-hipError_t attn_bf16_int8(const AttnParams&, int, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_f16_same(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_f16_e4m3(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_f16_int8(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_bf16_same(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_bf16_e4m3(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
+hipError_t attn_bf16_int8(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
 }  // namespace w4a16

@@ -143,7 +143,8 @@ constexpr int64_t kAttnMaxSplitGroups = 4096;
 static_assert(kAttnMaxSplitGroups <= kCounterBytes / 4, "one counter per group");
 
 struct AttnShape {
-  int row_blocks, target;
+  AttnKind kind;
+  int rows, target;
   int64_t grid, workspace;
 };
 
@@ -158,15 +159,15 @@ w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64
   const int64_t rows = max_q * (q_heads / kv_heads);
   if (rows >= kMaxInt)
     return report(W4A16_ERR_SHAPE, "max_q times the heads of a group must be below 2^31");
-  s->row_blocks = attn_row_blocks(rows, (int)dim);
-  const int64_t block = 16 * s->row_blocks;
-  const int64_t groups = sequences * div_up(rows, block) * kv_heads;
-  s->target = groups <= kAttnMaxSplitGroups / s->row_blocks ? kAttnItemsPerCu * num_cus : 0;
+  s->kind = attn_kind(rows, (int)dim);
+  s->rows = attn_rows(s->kind);
+  const int64_t groups = sequences * div_up(rows, s->rows) * kv_heads;
+  s->target = groups <= kAttnMaxSplitGroups * 16 / s->rows ? kAttnItemsPerCu * num_cus : 0;
   s->grid = groups + s->target;
   if (s->grid >= kMaxInt)
     return report(W4A16_ERR_SHAPE, "too many sequences, tokens and heads for one launch");
   s->workspace =
-      s->target > 0 ? kCounterBytes + s->grid * attn_part_floats((int)block, attn_dim_block((int)dim)) * 4
+      s->target > 0 ? kCounterBytes + s->grid * attn_part_floats(s->rows, attn_dim_block((int)dim)) * 4
                     : 0;
   return W4A16_OK;
 }
@@ -402,7 +403,7 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
   // 32-bit counts of work: row blocks times steps of 128 tokens, over all heads
   const int64_t capacity = std::min<int64_t>((int64_t)a->table_pages * a->cache.page_size, kMaxInt - 1);
   const int64_t rows = (int64_t)a->max_q * (a->q_heads / view.heads);
-  const double work = (double)a->sequences * (double)div_up(rows, 16 * s.row_blocks) *
+  const double work = (double)a->sequences * (double)div_up(rows, s.rows) *
                       (double)view.heads * (double)(div_up(capacity, kAttnStep) + 1);
   if (work >= 2147483648.0)
     return report(W4A16_ERR_SHAPE, "sequences x new tokens x cached tokens too large for one launch");
@@ -451,10 +452,10 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
   p.target = s.target;
   p.grid = (int32_t)s.grid;
   p.scale_log2 = a->scale * 1.44269504088896340736f;
-  using Launch = hipError_t (*)(const AttnParams&, int, hipStream_t);
+  using Launch = hipError_t (*)(const AttnParams&, AttnKind, hipStream_t);
   static constexpr Launch kLaunch[2][3] = {{attn_f16_same, attn_f16_e4m3, attn_f16_int8},
                                            {attn_bf16_same, attn_bf16_e4m3, attn_bf16_int8}};
-  return launched(kLaunch[a->dtype][a->cache.format](p, s.row_blocks, (hipStream_t)stream));
+  return launched(kLaunch[a->dtype][a->cache.format](p, s.kind, (hipStream_t)stream));
 }
 
 w4a16_status w4a16_token_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int32_t top_k,

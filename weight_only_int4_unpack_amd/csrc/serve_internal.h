@@ -96,13 +96,19 @@ constexpr int kAttnStep = kAttnWaves * kAttnTile;  // tokens of a workgroup's st
 constexpr int kAttnMaxSplits = 256;      // parts of a sequence
 // Head dims a kernel is built for: the next of 64, 128, 256.
 inline int attn_dim_block(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-// Row blocks of 16 (row = new token and query head of one key/value head) that
-// a wave holds: the more, the fewer times keys and values are read.
-inline int attn_row_blocks(int64_t rows, int dim) {
-  const int most = dim > 128 ? 2 : 4;
-  const int need = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return need < most ? need : most;
+// Kernels by the rows (new token x query head) of a key/value head: up to 16 or
+// 32, the waves of a workgroup share the rows and take turns at the tokens;
+// above, each wave has 16 or 32 rows and they share the tokens through LDS.
+enum class AttnKind { kNarrow1, kNarrow2, kWide1, kWide2 };
+inline AttnKind attn_kind(int64_t rows, int dim) {
+  if (rows <= 16) return AttnKind::kNarrow1;
+  if (attn_dim_block(dim) == 256) return AttnKind::kWide1;
+  return rows <= 32 ? AttnKind::kNarrow2 : rows <= 64 ? AttnKind::kWide1 : AttnKind::kWide2;
 }
+inline int attn_rows(AttnKind k) {
+  return k == AttnKind::kNarrow1 ? 16 : k == AttnKind::kNarrow2 ? 32 : k == AttnKind::kWide1 ? 64 : 128;
+}
+constexpr int kAttnStage = 64;           // tokens that the wide kernels stage at a time
 // Floats of one part: rows of sums, then each row's maximum and denominator.
 __host__ __device__ constexpr int64_t attn_part_floats(int rows, int dim_block) {
   return (int64_t)rows * (dim_block + 2);
@@ -127,12 +133,12 @@ struct AttnParams {
 };
 
 // One per dtype and format, each a source file of its own (build time).
-hipError_t attn_f16_same(const AttnParams& p, int row_blocks, hipStream_t stream);
-hipError_t attn_f16_e4m3(const AttnParams& p, int row_blocks, hipStream_t stream);
-hipError_t attn_f16_int8(const AttnParams& p, int row_blocks, hipStream_t stream);
-hipError_t attn_bf16_same(const AttnParams& p, int row_blocks, hipStream_t stream);
-hipError_t attn_bf16_e4m3(const AttnParams& p, int row_blocks, hipStream_t stream);
-hipError_t attn_bf16_int8(const AttnParams& p, int row_blocks, hipStream_t stream);
+hipError_t attn_f16_same(const AttnParams& p, AttnKind kind, hipStream_t stream);
+hipError_t attn_f16_e4m3(const AttnParams& p, AttnKind kind, hipStream_t stream);
+hipError_t attn_f16_int8(const AttnParams& p, AttnKind kind, hipStream_t stream);
+hipError_t attn_bf16_same(const AttnParams& p, AttnKind kind, hipStream_t stream);
+hipError_t attn_bf16_e4m3(const AttnParams& p, AttnKind kind, hipStream_t stream);
+hipError_t attn_bf16_int8(const AttnParams& p, AttnKind kind, hipStream_t stream);
 hipError_t launch_rope_table(const RopeTableParams& p, hipStream_t stream);
 hipError_t launch_rope_kv(const RopeKvParams& p, int dtype, int format, hipStream_t stream);
 hipError_t launch_kv_read(const KvReadParams& p, int dtype, int format, hipStream_t stream);

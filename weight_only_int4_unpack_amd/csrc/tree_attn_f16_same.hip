@@ -2,7 +2,7 @@
 #include "tree_attn_kernel.h"
 
 namespace w4a16 {
-hipError_t attn_f16_same(const AttnParams& p, int row_blocks, hipStream_t stream) {
-  return serve::launch_attn_rows<serve::F16, W4A16_KV_SAME>(p, row_blocks, stream);
+hipError_t attn_f16_same(const AttnParams& p, AttnKind kind, hipStream_t stream) {
+  return serve::launch_attn_shape<serve::F16, W4A16_KV_SAME>(p, kind, stream);
 }
 }  // namespace w4a16

@@ -18,8 +18,14 @@
 // contiguous run over 16 lanes); one byte permute joins two tokens' values of
 // a dim into an operand word, and tile j of O^T holds dims c * DB/16 + j.
 //
-// 8-bit codes are widened (exactly) in registers; a token's scales multiply
-// its scores and its weights, which are one value per lane and token.
+// 8-bit codes are widened exactly to 16 bits; a token's scales multiply its
+// scores and its weights, which are one value per lane and token.
+//
+// Two kernels share this. Few rows (narrow): the four waves of a workgroup
+// hold the same rows and take turns at the tokens, operands go from memory
+// into registers, and the waves' sums are joined at the end. Many rows (wide):
+// each wave holds rows of its own, and the workgroup stages 64 tokens at a
+// time through LDS, widened and laid out as operands once for all four.
 #pragma once
 
 #include <type_traits>
@@ -53,7 +59,8 @@ __device__ __forceinline__ uint32_t pair(float lo, float hi) {
   }
 }
 
-// Codes in the low (HI = false) or high half of a word as a 16-bit pair.
+// Codes in the low (HI = false) or high half of a word as a 16-bit pair, exactly.
+// int8 (fp16 only): u = code + 128 in the mantissa of 1024, then 1152 off.
 template <typename T, int FMT, bool HI>
 __device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
   if constexpr (FMT == W4A16_KV_E4M3) {
@@ -62,7 +69,12 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w) {
     else
       return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
   } else {
-    return pair<T>((float)(int8_t)(w >> (HI ? 16 : 0)), (float)(int8_t)(w >> (HI ? 24 : 8)));
+    static_assert(T::kCode == W4A16_F16, "int8 codes are widened to fp16");
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w ^ 0x80808080u,
+                                             HI ? 0x04030402u : 0x04010400u);
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, u) -
+                                            f16x2{(_Float16)1152.0f, (_Float16)1152.0f});
   }
 }
 
@@ -107,6 +119,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   }
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) steps += (uint32_t)__shfl_xor((int)steps, s);
+  steps = (uint32_t)__builtin_amdgcn_readfirstlane((int)steps);
   uint32_t per = 0x7FFFFFFF / kAttnStep;   // steps of a split
   if (p.target > 0)
     per = max((steps * (uint32_t)p.cache.heads + p.target - 1) / (uint32_t)p.target, 1u);
@@ -128,26 +141,28 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
     const uint64_t past = __ballot(items_before + upto > index);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
+      // into scalar registers: everything below is the same for all lanes
+      auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
       it->seq = b0 + l;
-      it->splits = __shfl(splits, l);
-      it->blocks = __shfl(blocks, l);
-      it->chunk = (int)min(__shfl((int)own, l), 0x7FFFFF00 / kAttnStep) * kAttnStep;
-      it->len = __shfl(len, l);
-      it->news = __shfl(news, l);
-      it->start = __shfl(start, l);
-      const int local = index - (items_before + __shfl(upto - items, l));
+      it->splits = of(splits);
+      it->blocks = of(blocks);
+      it->chunk = min(of((int)own), 0x7FFFFF00 / kAttnStep) * kAttnStep;
+      it->len = of(len);
+      it->news = of(news);
+      it->start = of(start);
+      const int local = index - (items_before + of(upto - items));
       // heads innermost: workgroups go round the 8 XCDs, so with 8 heads the
       // row blocks that share a head's keys and values share an L2
       it->head = local % p.cache.heads;
       const int rest = local / p.cache.heads;
-      it->block = rest % it->blocks;
+      it->block = it->blocks - 1 - rest % it->blocks;  // causal: the longest first
       it->split = rest / it->blocks;
-      it->group = groups_before + __shfl(gupto - groups, l) + it->block * p.cache.heads + it->head;
-      it->first = index - it->split * it->blocks * p.cache.heads;
+      it->group = groups_before + of(gupto - groups) + it->block * p.cache.heads + it->head;
+      it->first = index - it->split * it->blocks * p.cache.heads;  // + split * blocks * heads
       return true;
     }
-    items_before += __shfl(upto, 63);
-    groups_before += __shfl(gupto, 63);
+    items_before += __builtin_amdgcn_readlane(upto, 63);
+    groups_before += __builtin_amdgcn_readlane(gupto, 63);
   }
   return false;
 }
@@ -170,22 +185,446 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Item& it, int 
     p.lse[at] = z == 0.0f ? kNegInf : 0.69314718055994530942f * (m - lift + __log2f(z));
 }
 
+// Types of the two products. 8-bit codes are multiplied by fp16 weights
+// whatever the activations are (2^-11 instead of bf16's 2^-8 per weight), and
+// int8 ones by fp16 queries (bf16 queries are scaled by a power of two per row
+// into fp16's range first: what that drops is below 2^-39 of the row's largest).
+template <typename T, int FMT>
+struct Types {
+  using K = typename std::conditional<FMT == W4A16_KV_INT8, F16, T>::type;
+  using P = typename std::conditional<FMT == W4A16_KV_SAME, T, F16>::type;
+  static constexpr bool kSame = FMT == W4A16_KV_SAME;
+  static constexpr bool kRescaleQ = FMT == W4A16_KV_INT8 && T::kCode == W4A16_BF16;
+  // fp16 weights are held 2^6 above 1, at most 2^14, so that the small ones
+  // stay above fp16's subnormals (2^-14) down to 2^-20 of the largest.
+  static constexpr float kLift = P::kCode == W4A16_F16 ? 6.0f : 0.0f;
+};
+
+constexpr float kSlack = 8.0f;  // how far (log2) a score may exceed the held maximum
+
+// A wave's rows: R blocks of 16, lane (g, c) holding row c of each.
+template <typename T, int FMT, int DB, int R>
+struct Rows {
+  using TY = Types<T, FMT>;
+  static constexpr int kSteps = DB / 32;  // contraction steps of S^T
+  static constexpr int kVD = DB / 16;     // tiles of O^T, and dims of V per lane
+  u32x4 q[R][kSteps];
+  f32x4 acc[R][kVD];
+  float factor[R];                        // of the scores: scale, log2(e), the row's rescaling
+  float top[R], total[R];                 // held maximum (log2) and this lane's sum of weights
+  int query[R];                           // new token of the row
+  float vref;                             // power of two that weights x scales are held against
+  int start, prefix, len;
+
+  // `row0`: the wave's first row. `dim_of(s)`: dims of contraction step s.
+  template <typename DimOf>
+  __device__ __forceinline__ void init(const AttnParams& p, const Item& it, int row0, int dim,
+                                       DimOf dim_of) {
+    const int c = threadIdx.x & 15;
+    start = it.start;
+    prefix = it.len - it.news;            // may be negative
+    len = it.len;
+    vref = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = min(row0 + 16 * r + c, it.news * p.group - 1);
+      query[r] = row / p.group;
+      const uint16_t* src = p.q + (int64_t)(it.start + query[r]) * p.q_token +
+                            (int64_t)(it.head * p.group + row - query[r] * p.group) * p.q_head;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = dim_of(s);
+        q[r][s] = u32x4{0, 0, 0, 0};
+        if (d < dim) q[r][s] = load16(src + d);
+      }
+      factor[r] = p.scale_log2;
+      top[r] = kNegInf;
+      total[r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVD; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+      if constexpr (TY::kRescaleQ) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const f32x8 x = widen8<T>(q[r][s]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        }
+        big = max(big, (uint32_t)__shfl_xor((int)big, 16));
+        big = max(big, (uint32_t)__shfl_xor((int)big, 32));
+        // largest magnitude into [2^14, 2^15); zero, subnormal and non-finite rows as they are
+        const int e = (int)(big >> 23) - 127;
+        const bool some = big >= 0x00800000u && big < 0x7F800000u;
+        const int by = some ? min(14 - e, 126) : 0;
+        const float up = ldexpf(1.0f, by);
+        factor[r] = ldexpf(p.scale_log2, -by);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[r][s] = narrow8<F16>(widen8<T>(q[r][s]) * up);
+      }
+    }
+  }
+
+  // Waits for the loads of init(): left to the compiler, that wait would sit in
+  // the token loop and hold up each pass for the loads of the next one.
+  __device__ __forceinline__ void settle() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  }
+
+  // Whether this lane's row r sees token t (which has to exist).
+  __device__ __forceinline__ bool sees(const AttnParams& p, int r, int t) const {
+    const int j = t - prefix;
+    if (j < 0) return true;
+    if (p.mask == nullptr) return j <= query[r];
+    return j < 64 * p.mask_words &&
+           ((p.mask[(int64_t)(start + query[r]) * p.mask_words + (j >> 6)] >> (j & 63)) & 1);
+  }
+
+  // One tile of 32 tokens from t0. k_op(u, i): operand of half tile u and step
+  // i; k_scale(u), v_scale(u): scales of this lane's 4 tokens; after(): called
+  // once the K operands are consumed; v_op(j, 0): operand of O^T's tile j. `edge`
+  // (uniform): some token may be unseen by some row; exists[u]: half tile u lies
+  // on a page. v_edge(in): lets the caller clear V of tokens that do not exist
+  // (bit 4u + i of `in`: this lane's token does) and say (uniform) whether V
+  // holds an infinity or NaN.
+  template <typename KOp, typename KScale, typename After, typename VEdge, typename VScale,
+            typename VOp>
+  __device__ __forceinline__ void tile(const AttnParams& p, int t0, bool edge, const bool* exists,
+                                       KOp k_op, KScale k_scale, After after, VEdge v_edge,
+                                       VScale v_scale, VOp v_op) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    // ---- S^T, in units of log2
+    f32x4 s[R][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const u32x4 a = k_op(u, i);
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r][u] = mfma16<typename TY::K>(a, q[r][i], s[r][u]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if constexpr (TY::kSame)
+          s[r][u] *= factor[r];
+        else
+          s[r][u] *= k_scale(u) * factor[r];
+      }
+    }
+    after();
+
+    // ---- what a row does not see: score -inf (and, below, weight 0)
+    uint32_t seen[R], in_all = 0xFF;      // bit 4u + i: this lane's token (u, i)
+    bool apart = false;
+    if (edge) {
+      in_all = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          in_all |= exists[u] && t0 + 16 * u + 4 * g + i < len ? 1u << (4 * u + i) : 0u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        seen[r] = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t bit = 1u << (4 * u + i);
+            const bool in = (in_all & bit) && sees(p, r, t0 + 16 * u + 4 * g + i);
+            seen[r] |= in ? bit : 0u;
+            s[r][u][i] = in ? s[r][u][i] : kNegInf;
+          }
+      }
+      apart = v_edge(in_all);
+    }
+
+    // ---- the held maximum rises only when a score exceeds it by 2^8
+    f32x4 vs[2];
+    bool rise = false;
+    float vhigh = 0.0f, high[R];
+    if constexpr (!TY::kSame) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        vs[u] = v_scale(u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // tokens that do not exist, infinities and NaN set no reference
+          const bool use = (in_all >> (4 * u + i) & 1) && vs[u][i] < __builtin_inff();
+          vhigh = use ? fmaxf(vhigh, vs[u][i]) : vhigh;
+        }
+      }
+      rise = vhigh > vref;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float m = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3]));
+      m = fmaxf(m, fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+      high[r] = m;
+      rise |= m > top[r] + kSlack;
+    }
+    if (__any(rise)) {
+      float down = 1.0f;
+      if constexpr (!TY::kSame) {
+        vhigh = fmaxf(vhigh, __shfl_xor(vhigh, 16));
+        vhigh = fmaxf(vhigh, __shfl_xor(vhigh, 32));
+        if (vhigh > vref) {               // the next power of two above
+          const float to = __uint_as_float(
+              min((__float_as_uint(vhigh) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
+          down = vref == to ? 1.0f : vref / to;
+          vref = to;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float m = fmaxf(high[r], __shfl_xor(high[r], 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        m = fmaxf(m, top[r]);
+        const float f = top[r] == m ? 1.0f : __builtin_amdgcn_exp2f(top[r] - m);
+        top[r] = m;
+        total[r] *= f;
+#pragma unroll
+        for (int j = 0; j < kVD; ++j) acc[r][j] *= f * down;
+      }
+    }
+
+    // ---- weights
+    if constexpr (!TY::kSame) {
+      const float inv = vref > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) vs[u] *= inv;
+    }
+    u32x4 w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float ref = (top[r] == kNegInf ? 0.0f : top[r]) - TY::kLift;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = __builtin_amdgcn_exp2f(s[r][u][i] - ref);
+          total[r] += x[i];
+          if constexpr (!TY::kSame) x[i] *= vs[u][i];
+        }
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = (seen[r] >> (4 * u + i)) & 1 ? x[i] : 0.0f;
+        }
+        w[r][2 * u] = pair<typename TY::P>(x[0], x[1]);
+        w[r][2 * u + 1] = pair<typename TY::P>(x[2], x[3]);
+      }
+    }
+
+    // ---- O^T
+    if (!apart) {
+#pragma unroll
+      for (int j = 0; j < kVD; ++j) {
+        const u32x4 a = v_op(j, 0u);
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r][j] = mfma16<typename TY::P>(a, w[r], acc[r][j]);
+      }
+    } else {
+      // An infinity or NaN among values that some rows may not see: token by
+      // token, and a row that does not see the token keeps its sums.
+#pragma unroll 1
+      for (int t = 0; t < kAttnTile; ++t) {
+        const int tu = t >> 4, tg = (t >> 2) & 3, ti = t & 3;
+        u32x4 only = {0, 0, 0, 0};
+        const uint32_t bits = tg == g ? (ti & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) only[e] = e == 2 * tu + (ti >> 1) ? bits : 0u;
+        uint32_t zero = 0;                // opaque: operands are formed anew for each token,
+        asm volatile("" : "+v"(zero));    // not kept in registers over the loop
+#pragma unroll
+        for (int j = 0; j < kVD; ++j) {
+          const u32x4 a = v_op(j, zero) & only;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const bool in = (__shfl((int)seen[r], tg * 16 + c) >> (4 * tu + ti)) & 1;
+            const f32x4 y = mfma16<typename TY::P>(a, w[r] & only, acc[r][j]);
+            acc[r][j] = in ? y : acc[r][j];
+          }
+        }
+      }
+    }
+  }
+
+  // This row's sum of weights over all lane groups.
+  __device__ __forceinline__ float denominator(int r) const {
+    float z = total[r] + __shfl_xor(total[r], 16);
+    return z + __shfl_xor(z, 32);
+  }
+  // Four of this lane's sums, V's reference put back: dims (4g + i) kVD + j..j+3 of row c.
+  __device__ __forceinline__ f32x4 sums(int r, int i, int j) const {
+    const f32x4 x = {acc[r][j][i], acc[r][j + 1][i], acc[r][j + 2][i], acc[r][j + 3][i]};
+    if constexpr (TY::kSame) return x;
+    return x * vref;
+  }
+};
+
+// Word x (two 16-bit values) or code word y holds an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ bool non_finite_pair(uint32_t x) {
+  constexpr uint32_t kExp = T::kCode == W4A16_F16 ? 0x7C00u : 0x7F80u;
+  return (x & kExp) == kExp || ((x >> 16) & kExp) == kExp;
+}
+__device__ __forceinline__ bool nan_codes(uint32_t y) {  // e4m3: seven ones
+  return (((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
+// Tokens [begin, end) of an item, and the first that some row of it may not see.
+struct Range {
+  int begin, end, see_all;
+};
+__device__ __forceinline__ Range range_of(const AttnParams& p, const Item& it, int row0, int rows) {
+  const int prefix = it.len - it.news;
+  const int last = (min(row0 + rows, it.news * p.group) - 1) / p.group;
+  const int block_end = p.mask ? it.len : min(it.len, prefix + last + 1);
+  Range r;
+  r.see_all = p.mask ? prefix : prefix + row0 / p.group + 1;
+  r.begin = it.split * it.chunk;
+  r.end = (int)min((int64_t)r.begin + it.chunk, (int64_t)max(block_end, 0));
+  return r;
+}
+
+// The page of token t (uniform): its first row (of head_dim values, or scales)
+// for the item's head, and whether there is one; row 0 where there is not.
+__device__ __forceinline__ int64_t page_row(const AttnParams& p, const Item& it, int t, bool* ok) {
+  const int page = t < it.len ? p.block_table[it.seq * p.table_stride + (t >> p.cache.page_shift)] : -1;
+  *ok = page >= 0 && page < p.cache.pages;
+  return (((int64_t)(*ok ? page : 0) * p.cache.heads + it.head) << p.cache.page_shift) +
+         (t & ((1 << p.cache.page_shift) - 1));
+}
+
+// Stores of a part, and the loads that join parts, go to the device's point
+// of coherence; the wait and the counter in arrive() order them.
+__device__ __forceinline__ void put2(float* at, float a, float b) {
+  __hip_atomic_store((uint64_t*)at, (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 get2(const float* at) {
+  const uint64_t x = __hip_atomic_load((const uint64_t*)at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return f32x2{__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))};
+}
+
+// Whether this workgroup is the last of its group's splits to arrive.
+__device__ __forceinline__ bool arrive(const AttnParams& p, const Item& it, int* flag) {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0F70);     // vmcnt(0): this wave's stores are complete
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int before = __hip_atomic_fetch_add(p.counters + it.group, 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+    *flag = before == it.splits - 1;
+    if (before == it.splits - 1)
+      __hip_atomic_store(p.counters + it.group, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool last = *flag != 0;
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  return last;
+}
+
+// The last workgroup of a group joins its parts, in an order that does not
+// depend on who arrived when. 16 lanes hold a row (VD dims each); with fewer
+// than 16 rows several such lane rows share a row's splits, and are joined
+// through `lds` (16 rows of DB + 4 floats).
+template <typename T, int DB, int ROWS>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, int rows, int dim,
+                                           float lift, float* lds) {
+  constexpr int kVD = DB / 16, kPad = DB + 4;
+  constexpr int64_t kPart = attn_part_floats(ROWS, DB);
+  const int slot = threadIdx.x >> 4, chunk = threadIdx.x & 15;
+  const int64_t stride = (int64_t)it.blocks * p.cache.heads * kPart;
+  const float* parts = p.parts + (int64_t)it.first * kPart;
+  rows = min(rows, ROWS);
+  int held = 16;                          // rows at a time: 1, 2, 4, 8 or 16
+  while (held / 2 >= rows) held /= 2;
+  const int share = 16 / held, lead = slot / held;
+  for (int at0 = 0; at0 < rows; at0 += held) {
+    const int at = at0 + slot % held;
+    const float* base = parts + (int64_t)at * DB + chunk * kVD;
+    const float* stats = parts + ROWS * DB + 2 * at;
+    float m = kNegInf, z = 0.0f, o[kVD];
+#pragma unroll
+    for (int j = 0; j < kVD; ++j) o[j] = 0.0f;
+    if (at < rows) {
+      for (int sp = lead + share * chunk; sp < it.splits; sp += 16 * share)
+        m = fmaxf(m, get2(stats + sp * stride).x);
+#pragma unroll
+      for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
+      constexpr int kDeep = 48 / kVD;     // parts in flight
+#pragma unroll 1
+      for (int s0 = lead; s0 < it.splits; s0 += share * kDeep) {
+        f32x2 st[kDeep], x[kDeep][kVD / 2];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+          const int sp = s0 + d * share;
+          if (sp < it.splits) {
+            st[d] = get2(stats + sp * stride);
+#pragma unroll
+            for (int j = 0; j < kVD; j += 2) x[d][j / 2] = get2(base + sp * stride + j);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+          if (s0 + d * share < it.splits) {
+            const float f = st[d].x == m ? 1.0f : __builtin_amdgcn_exp2f(st[d].x - m);
+            z = fmaf(f, st[d].y, z);
+#pragma unroll
+            for (int j = 0; j < kVD; j += 2) {
+              o[j] = fmaf(f, x[d][j / 2].x, o[j]);
+              o[j + 1] = fmaf(f, x[d][j / 2].y, o[j + 1]);
+            }
+          }
+      }
+    }
+    if (share > 1) {                      // the same in the whole workgroup; rows <= 8
+      __syncthreads();
+      float* mine = lds + slot * kPad;
+#pragma unroll
+      for (int j = 0; j < kVD; ++j) mine[chunk * kVD + j] = o[j];
+      if (chunk == 0) {
+        mine[DB] = m;
+        mine[DB + 1] = z;
+      }
+      __syncthreads();
+      if (lead == 0) {
+        float big = m;
+        for (int s = 1; s < share; ++s) big = fmaxf(big, lds[(slot + s * held) * kPad + DB]);
+        const float f0 = m == big ? 1.0f : __builtin_amdgcn_exp2f(m - big);
+        z *= f0;
+#pragma unroll
+        for (int j = 0; j < kVD; ++j) o[j] *= f0;
+        for (int s = 1; s < share; ++s) {
+          const float* other = lds + (slot + s * held) * kPad;
+          const float f = other[DB] == big ? 1.0f : __builtin_amdgcn_exp2f(other[DB] - big);
+          z = fmaf(f, other[DB + 1], z);
+#pragma unroll
+          for (int j = 0; j < kVD; ++j) o[j] = fmaf(f, other[chunk * kVD + j], o[j]);
+        }
+        m = big;
+      }
+    }
+    if (lead == 0 && at < rows) finish<T, kVD>(p, it, it.block * ROWS + at, chunk * kVD, dim, m, z, lift, o);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
 template <typename T, int FMT, int DB, int R, bool FULL>
-__global__ __launch_bounds__(64 * kAttnWaves) void tree_attn_kernel(AttnParams p) {
-  constexpr bool kSame = FMT == W4A16_KV_SAME;
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnParams p) {
+  using TY = Types<T, FMT>;
+  constexpr bool kSame = TY::kSame;
   constexpr int kRows = 16 * R;
-  constexpr int kSteps = DB / 32;              // contraction steps of S^T
-  constexpr int kVD = DB / 16;                 // dims of V per lane, and tiles of O^T
+  constexpr int kVD = DB / 16;
   constexpr int kBytes = kSame ? 2 : 1;
   constexpr int kVWords = kVD * kBytes / 4;    // words of a token's V per lane
   constexpr int kKLoads = DB * kBytes / 64;    // 16-byte loads of K per half tile
   constexpr int kPad = DB + 4;
-  // Weights against 8-bit codes carry the token's scale and are rounded to
-  // bf16, whose range holds any scale (fp16 would lose them below 6e-5).
-  using PT = typename std::conditional<kSame, T, BF16>::type;
-  // fp16 weights are kept 2^6 above 1 for the same reason: at most 2^14.
-  constexpr float kLift = PT::kCode == W4A16_F16 ? 6.0f : 0.0f;
-  constexpr float kSlack = 8.0f;               // how far scores may exceed the held maximum
 
   __shared__ float l_sum[kAttnWaves][16][kPad];
   __shared__ f32x2 l_stat[kAttnWaves][16];
@@ -197,59 +636,30 @@ __global__ __launch_bounds__(64 * kAttnWaves) void tree_attn_kernel(AttnParams p
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int dim = FULL ? DB : p.cache.dim;
-  const int rows = it.news * p.group - it.block * kRows;  // of this block, may exceed kRows
   const int row0 = it.block * kRows;
-  const int prefix = it.len - it.news;                    // may be negative
+  const int rows = it.news * p.group - row0;   // of this block, may exceed kRows
+  const Range range = range_of(p, it, row0, kRows);
+  const int tiles = range.end > range.begin ? (range.end - range.begin + kAttnTile - 1) / kAttnTile : 0;
 
-  // New token of this lane's row in row block r (clamped to the last one).
-  int query[R];
-  u32x4 qreg[R][kSteps];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = min(row0 + 16 * r + c, it.news * p.group - 1);
-    query[r] = row / p.group;
-    const uint16_t* src = p.q + (int64_t)(it.start + query[r]) * p.q_token +
-                          (int64_t)(it.head * p.group + row - query[r] * p.group) * p.q_head;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int d = kSame ? 32 * s + 8 * g : 64 * (s / 2) + 16 * g + 8 * (s & 1);
-      u32x4 x = {0, 0, 0, 0};
-      if (FULL || d < dim) x = load16(src + d);
-      qreg[r][s] = x;
-    }
-  }
-
-  // Tokens [begin, end) of this split; the block's rows see none past `end`.
-  const int last_query = min(row0 + kRows, it.news * p.group) - 1;
-  const int see_all = p.mask ? prefix : prefix + row0 / p.group + 1;  // every row sees below
-  const int block_end = p.mask ? it.len : min(it.len, prefix + last_query / p.group + 1);
-  const int begin = it.split * it.chunk;
-  const int end = (int)min((int64_t)begin + it.chunk, (int64_t)max(block_end, 0));
-  const int tiles = end > begin ? (end - begin + kAttnTile - 1) / kAttnTile : 0;
-
-  const int32_t* table = p.block_table + it.seq * p.table_stride;
-  const int shift = p.cache.page_shift;
   const char* kbase = (const char*)p.cache.k;
   const char* vbase = (const char*)p.cache.v;
-  const int64_t row_bytes = (int64_t)dim * kBytes;
+  const int row_bytes = dim * kBytes;
 
   u32x4 kreg[2][kKLoads];
   uint32_t vreg[2][4][kVWords];
   f32x4 kscale[2], vscale[2];
-  bool page_ok[2] = {true, true};
+  int64_t at[2];                               // rows of the next tile's half tiles
+  bool ok[2] = {false, false};
 
-  // First token row of half tile u of tile n (uniform), and whether its page exists.
-  auto place = [&](int n, int u, bool* ok) -> int64_t {
-    const int t = begin + n * kAttnTile + 16 * u;
-    const int page = t < it.len ? table[t >> shift] : -1;
-    *ok = page >= 0 && page < p.cache.pages;
-    return (((int64_t)(*ok ? page : 0) * p.cache.heads + it.head) << shift) + (t & ((1 << shift) - 1));
+  auto look_up = [&](int n) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      at[u] = page_row(p, it, range.begin + n * kAttnTile + 16 * u, &ok[u]);
   };
-  auto load_k = [&](int n) {
+  auto load_k = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t at = place(n, u, &page_ok[u]);
-      const char* src = kbase + (at + c) * row_bytes;
+      const char* src = kbase + at[u] * row_bytes + c * row_bytes;
 #pragma unroll
       for (int i = 0; i < kKLoads; ++i) {
         const int d = i * (64 / kBytes) + g * (16 / kBytes);
@@ -261,16 +671,14 @@ __global__ __launch_bounds__(64 * kAttnWaves) void tree_attn_kernel(AttnParams p
           kreg[u][i] = in ? x : u32x4{0, 0, 0, 0};
         }
       }
-      if constexpr (!kSame) kscale[u] = *(const f32x4*)(p.cache.k_scale + at + 4 * g);
+      if constexpr (!kSame) kscale[u] = *(const f32x4*)(p.cache.k_scale + at[u] + 4 * g);
     }
   };
-  auto load_v = [&](int n) {
+  auto load_v = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      bool ok;
-      const int64_t at = place(n, u, &ok);
       const int d = FULL ? c * kVD : min(c * kVD, dim - kVD);  // dims past the head's: not stored
-      const char* src = vbase + (at + 4 * g) * row_bytes + d * kBytes;
+      const char* src = vbase + at[u] * row_bytes + 4 * g * row_bytes + d * kBytes;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -287,221 +695,94 @@ __global__ __launch_bounds__(64 * kAttnWaves) void tree_attn_kernel(AttnParams p
             vreg[u][i][0] = *(const uint32_t*)(src + i * row_bytes);
           }
         }
-      if constexpr (!kSame) vscale[u] = *(const f32x4*)(p.cache.v_scale + at + 4 * g);
+      if constexpr (!kSame) vscale[u] = *(const f32x4*)(p.cache.v_scale + at[u] + 4 * g);
     }
   };
 
-  f32x4 acc[R][kVD];
-  float top[R], total[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    top[r] = kNegInf;
-    total[r] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kVD; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
-  }
-
   if (wave < tiles) {
-    load_k(wave);
-    load_v(wave);
+    look_up(wave);
+    load_k();
+    load_v();
   }
+  Rows<T, FMT, DB, R> rw;
+  rw.init(p, it, row0, dim, [&](int s) {
+    return kSame ? 32 * s + 8 * g : 64 * (s / 2) + 16 * g + 8 * (s & 1);
+  });
+
+  rw.settle();
   for (int n = wave; n < tiles; n += kAttnWaves) {
-    const int t0 = begin + n * kAttnTile;
-    // ---- S^T, in units of log2
-    f32x4 s[R][2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      u32x4 a[kSteps];
-      if constexpr (kSame) {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) a[i] = kreg[u][i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w = kreg[u][i / 2][2 * (i & 1) + e];
-            a[i][2 * e] = widen_pair<T, FMT, false>(w);
-            a[i][2 * e + 1] = widen_pair<T, FMT, true>(w);
-          }
-      }
-      f32x4 factor = f32x4{p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2};
-      if constexpr (!kSame) factor *= kscale[u];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) x = mfma16<T>(a[i], qreg[r][i], x);
-        s[r][u] = x * factor;
-      }
-    }
-    const bool edge = t0 + kAttnTile > see_all || t0 + kAttnTile > it.len || !page_ok[0] ||
-                      !page_ok[1];
-    const bool ok0 = page_ok[0], ok1 = page_ok[1];
-    if (n + kAttnWaves < tiles) load_k(n + kAttnWaves);
-
-    // ---- what a row does not see: score -inf (and, below, weight 0)
-    uint32_t seen[R];                          // bit 4u + i: this lane's token (u, i)
-    if (edge) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        seen[r] = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 16 * u + 4 * g + i;
-            const int j = t - prefix;
-            bool in = t < it.len && (u == 0 ? ok0 : ok1);
-            if (in && j >= 0) {
-              if (p.mask == nullptr)
-                in = j <= query[r];
-              else
-                in = j < 64 * p.mask_words &&
-                     ((p.mask[(int64_t)(it.start + query[r]) * p.mask_words + (j >> 6)] >> (j & 63)) & 1);
-            }
-            seen[r] |= in ? 1u << (4 * u + i) : 0u;
-            s[r][u][i] = in ? s[r][u][i] : kNegInf;
-          }
-      }
-    }
-
-    // ---- the held maximum rises only when a score exceeds it by 2^8
-    bool rise = false;
-    float high[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float m = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3]));
-      m = fmaxf(m, fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      high[r] = m;
-      rise |= m > top[r] + kSlack;
-    }
-    if (__any(rise)) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float m = fmaxf(high[r], __shfl_xor(high[r], 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
-        m = fmaxf(m, top[r]);
-        const float f = top[r] == m ? 1.0f : __builtin_amdgcn_exp2f(top[r] - m);
-        top[r] = m;
-        total[r] *= f;
-#pragma unroll
-        for (int j = 0; j < kVD; ++j) acc[r][j] *= f;
-      }
-    }
-
-    // ---- weights
-    u32x4 w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float ref = (top[r] == kNegInf ? 0.0f : top[r]) - kLift;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(s[r][u][i] - ref);
-          total[r] += x[i];
-          if constexpr (!kSame) x[i] *= vscale[u][i];
-        }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = (seen[r] >> (4 * u + i)) & 1 ? x[i] : 0.0f;
-        }
-        w[r][2 * u] = pair<PT>(x[0], x[1]);
-        w[r][2 * u + 1] = pair<PT>(x[2], x[3]);
-      }
-    }
-
-    // ---- O^T
-    bool apart = false;                        // a value that must not meet weight 0
-    if (edge) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 16 * u + 4 * g + i;
-          const bool in = t < it.len && (u == 0 ? ok0 : ok1);
-#pragma unroll
-          for (int x = 0; x < kVWords; ++x) {
-            vreg[u][i][x] = in ? vreg[u][i][x] : 0u;
-            const uint32_t y = vreg[u][i][x];
-            if constexpr (kSame) {
-              constexpr uint32_t kExp = T::kCode == W4A16_F16 ? 0x7C00u : 0x7F80u;
-              apart |= (y & kExp) == kExp || ((y >> 16) & kExp) == kExp;
-            } else if constexpr (FMT == W4A16_KV_E4M3) {
-              const uint32_t z = (y & 0x7F7F7F7Fu) + 0x01010101u;  // NaN codes: 0x80
-              apart |= (z & 0x80808080u) != 0;
-            }
-          }
-        }
-      apart = __any(apart);
-    }
-    // Operand words of tile j: tokens (i, i + 1) of dim j, joined by one permute.
-    auto operand = [&](int j) -> u32x4 {
-      u32x4 a;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+    const int t0 = range.begin + n * kAttnTile;
+    const bool exists[2] = {ok[0], ok[1]};
+    const bool edge = t0 + kAttnTile > min(range.see_all, it.len) || !exists[0] || !exists[1];
+    const bool more = n + kAttnWaves < tiles;
+    if (more) look_up(n + kAttnWaves);         // scalar loads, back before they are needed
+    rw.tile(
+        p, t0, edge, exists,
+        [&](int u, int i) -> u32x4 {
           if constexpr (kSame) {
-            a[2 * u + h] = __builtin_amdgcn_perm(vreg[u][2 * h + 1][j / 2], vreg[u][2 * h][j / 2],
-                                                 j & 1 ? 0x07060302u : 0x05040100u);
+            return kreg[u][i];
           } else {
-            // bytes j, j+1 of both tokens: {a_j, b_j, a_j+1, b_j+1}
-            const uint32_t y = __builtin_amdgcn_perm(vreg[u][2 * h + 1][j / 4], vreg[u][2 * h][j / 4],
-                                                     j & 2 ? 0x07030602u : 0x05010400u);
-            a[2 * u + h] = j & 1 ? widen_pair<PT, FMT, true>(y) : widen_pair<PT, FMT, false>(y);
+            const uint32_t x = kreg[u][i / 2][2 * (i & 1)], y = kreg[u][i / 2][2 * (i & 1) + 1];
+            using K = typename TY::K;
+            return u32x4{widen_pair<K, FMT, false>(x), widen_pair<K, FMT, true>(x),
+                         widen_pair<K, FMT, false>(y), widen_pair<K, FMT, true>(y)};
           }
-        }
-      return a;
-    };
-    if (!apart) {
+        },
+        [&](int u) { return kscale[u]; },
+        [&]() {
+          if (more) load_k();
+        },
+        [&](uint32_t in) -> bool {
+          bool odd = false;
 #pragma unroll
-      for (int j = 0; j < kVD; ++j) {
-        const u32x4 a = operand(j);
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][j] = mfma16<PT>(a, w[r], acc[r][j]);
-      }
-    } else {
-      // An infinity or NaN among values that some rows may not see: token by
-      // token, and a row that does not see the token keeps its sums.
-      for (int t = 0; t < kAttnTile; ++t) {
-        const int tu = t >> 4, tg = (t >> 2) & 3, ti = t & 3;
-        u32x4 only = {0, 0, 0, 0};
-        const uint32_t bits = tg == g ? (ti & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) only[e] = e == 2 * tu + (ti >> 1) ? bits : 0u;
+              for (int x = 0; x < kVWords; ++x) {
+                const uint32_t y = (in >> (4 * u + i)) & 1 ? vreg[u][i][x] : 0u;
+                vreg[u][i][x] = y;
+                if constexpr (kSame) odd |= non_finite_pair<T>(y);
+                if constexpr (FMT == W4A16_KV_E4M3) odd |= nan_codes(y);
+              }
+          return __any(odd);
+        },
+        [&](int u) { return vscale[u]; },
+        // tokens (i, i + 1) of dim j side by side: one permute per word
+        [&](int j, uint32_t zero) -> u32x4 {
+          u32x4 a;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const bool in = (__shfl((int)seen[r], tg * 16 + c) >> (4 * tu + ti)) & 1;
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int j = 0; j < kVD; ++j) {
-            const f32x4 y = mfma16<PT>(operand(j) & only, w[r] & only, acc[r][j]);
-            acc[r][j] = in ? y : acc[r][j];
-          }
-        }
-      }
-    }
-    if (n + kAttnWaves < tiles) load_v(n + kAttnWaves);
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (kSame) {
+                a[2 * u + h] = __builtin_amdgcn_perm(vreg[u][2 * h + 1][j / 2], vreg[u][2 * h][j / 2] | zero,
+                                                     j & 1 ? 0x07060302u : 0x05040100u);
+              } else {
+                const uint32_t y = __builtin_amdgcn_perm(
+                    vreg[u][2 * h + 1][j / 4], vreg[u][2 * h][j / 4] | zero,
+                    j & 2 ? 0x07030602u : 0x05010400u);
+                using P = typename TY::P;
+                a[2 * u + h] = j & 1 ? widen_pair<P, FMT, true>(y) : widen_pair<P, FMT, false>(y);
+              }
+            }
+          return a;
+        });
+    if (more) load_v();
   }
 
-  // ---- join the lane groups' sums and the four waves, a row block at a time
+  // ---- join the four waves, a row block at a time
   const int row = tid >> 4, chunk = tid & 15;
-  const int64_t part_floats = attn_part_floats(kRows, DB);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float sum = total[r];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
+    const float sum = rw.denominator(r);
     if (r > 0) __syncthreads();
-    if (g == 0) l_stat[wave][c] = f32x2{top[r], sum};
+    if (g == 0) l_stat[wave][c] = f32x2{rw.top[r], sum};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < kVD; j += 4)
-        *(f32x4*)&l_sum[wave][c][(4 * g + i) * kVD + j] =
-            f32x4{acc[r][j][i], acc[r][j + 1][i], acc[r][j + 2][i], acc[r][j + 3][i]};
+        *(f32x4*)&l_sum[wave][c][(4 * g + i) * kVD + j] = rw.sums(r, i, j);
     __syncthreads();
     float m = kNegInf;
 #pragma unroll
@@ -518,98 +799,283 @@ __global__ __launch_bounds__(64 * kAttnWaves) void tree_attn_kernel(AttnParams p
       for (int j = 0; j < kVD; ++j) o[j] = fmaf(f, l_sum[v][row][chunk * kVD + j], o[j]);
     }
     const int at = 16 * r + row;
-    if (at >= rows) continue;
-    if (it.splits == 1) {
-      finish<T, kVD>(p, it, row0 + at, chunk * kVD, dim, m, z, kLift, o);
-    } else {
-      // device-scope stores; the wait and the counter below order them
-      float* part = p.parts + blockIdx.x * part_floats;
-      uint64_t* dst = (uint64_t*)(part + at * DB + chunk * kVD);
+    if (at < rows) {
+      if (it.splits == 1) {
+        finish<T, kVD>(p, it, row0 + at, chunk * kVD, dim, m, z, TY::kLift, o);
+      } else {
+        float* part = p.parts + blockIdx.x * attn_part_floats(kRows, DB);
 #pragma unroll
-      for (int j = 0; j < kVD; j += 2)
-        __hip_atomic_store(dst + j / 2, __builtin_bit_cast(uint64_t, f32x2{o[j], o[j + 1]}),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (chunk == 0)
-        __hip_atomic_store((uint64_t*)(part + kRows * DB) + at,
-                           __builtin_bit_cast(uint64_t, f32x2{m, z}), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
-  if (it.splits == 1) return;
-
-  // ---- hand-off: the last of a group's splits to arrive joins them all, in
-  // split order (results do not depend on the order of arrival)
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are complete
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __syncthreads();
-  if (tid == 0) {
-    const int arrived = __hip_atomic_fetch_add(p.counters + it.group, 1, __ATOMIC_RELAXED,
-                                               __HIP_MEMORY_SCOPE_AGENT);
-    l_last = arrived == it.splits - 1;
-  }
-  __syncthreads();
-  if (!l_last) return;
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  if (tid == 0)
-    __hip_atomic_store(p.counters + it.group, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int64_t stride = (int64_t)it.blocks * p.cache.heads * part_floats;
-  const float* parts = p.parts + (int64_t)it.first * part_floats;
-  auto stat = [&](int split, int at) -> f32x2 {
-    const uint64_t x = __hip_atomic_load((const uint64_t*)(parts + split * stride + kRows * DB) + at,
-                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return __builtin_bit_cast(f32x2, x);
-  };
-  for (int at = row; at < min(rows, kRows); at += 16) {
-    float m = kNegInf;
-    for (int sp = chunk; sp < it.splits; sp += 16) m = fmaxf(m, stat(sp, at).x);
-#pragma unroll
-    for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
-    float z = 0.0f, o[kVD];
-#pragma unroll
-    for (int j = 0; j < kVD; ++j) o[j] = 0.0f;
-#pragma unroll 4
-    for (int sp = 0; sp < it.splits; ++sp) {
-      const f32x2 st = stat(sp, at);
-      const float f = st.x == m ? 1.0f : __builtin_amdgcn_exp2f(st.x - m);
-      z = fmaf(f, st.y, z);
-      const uint64_t* src = (const uint64_t*)(parts + sp * stride + at * DB + chunk * kVD);
-#pragma unroll
-      for (int j = 0; j < kVD; j += 2) {
-        const f32x2 x = __builtin_bit_cast(
-            f32x2, __hip_atomic_load(src + j / 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        o[j] = fmaf(f, x.x, o[j]);
-        o[j + 1] = fmaf(f, x.y, o[j + 1]);
+        for (int j = 0; j < kVD; j += 2) put2(part + at * DB + chunk * kVD + j, o[j], o[j + 1]);
+        if (chunk == 0) put2(part + kRows * DB + 2 * at, m, z);
       }
     }
-    finish<T, kVD>(p, it, row0 + at, chunk * kVD, dim, m, z, kLift, o);
   }
+  if (it.splits > 1 && arrive(p, it, &l_last))
+    join_parts<T, DB, kRows>(p, it, rows, dim, TY::kLift, &l_sum[0][0][0]);
 }
 
-template <typename T, int FMT, int DB, int R>
+// ---------------------------------------------------------------- many rows
+// LDS of a stage: K rows as they are read (16-byte pieces of a row permuted by
+// the row's low 3 bits, so that 8 rows' same piece lies in 8 bank groups), and
+// V as operands: for each half stage of 32 tokens, each of DB dims has a 64-byte
+// row of four pieces (lane groups g), a piece being the 8 slots of lane (g, .);
+// pieces permuted by two bits of the dim's index for the same reason.
+template <int DB>
+struct Stage {
+  u32x4 k[kAttnStage * DB / 8];
+  u32x4 v[2 * DB * 4];
+  float k_scale[kAttnStage], v_scale[kAttnStage];
+  int odd;                               // V holds an infinity or NaN
+};
+
+template <typename T, int FMT, int DB, int R, bool FULL>
+__global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_kernel(AttnParams p) {
+  using TY = Types<T, FMT>;
+  using KT = typename TY::K;
+  using PT = typename TY::P;
+  constexpr bool kSame = TY::kSame;
+  constexpr int kWaveRows = 16 * R, kRows = kAttnWaves * kWaveRows;
+  constexpr int kVD = DB / 16;
+  constexpr int kBytes = kSame ? 2 : 1;
+  constexpr int kPieces = DB / 8;                      // 8-dim pieces of a K row
+  constexpr int kPass = 64 * kAttnWaves / kPieces;     // K rows that the workgroup loads at once
+  constexpr int kPasses = kAttnStage / kPass;
+  constexpr int kVWords = kVD * kBytes / 4;
+  extern __shared__ __align__(16) char l_raw[];
+  Stage<DB>* stage = (Stage<DB>*)l_raw;                // two of them
+
+  Item it;
+  if (!find_item<kRows>(p, blockIdx.x, &it)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int dim = FULL ? DB : p.cache.dim;
+  const int row0 = it.block * kRows;
+  const int rows = it.news * p.group - row0;
+  const Range range = range_of(p, it, row0, kRows);
+  const int stages = range.end > range.begin ? (range.end - range.begin + kAttnStage - 1) / kAttnStage : 0;
+  const bool busy = wave * kWaveRows < rows;           // this wave has rows
+
+  const char* kbase = (const char*)p.cache.k;
+  const char* vbase = (const char*)p.cache.v;
+  const int row_bytes = dim * kBytes;
+  const int piece = tid % kPieces, krow = tid / kPieces;  // of K: row krow + pass * kPass
+  const int quad = tid >> 4, chunk = tid & 15;            // of V: tokens 4 quad.., dims chunk * kVD..
+
+  u32x4 kreg[kPasses];                                 // 8-bit: the low two words
+  uint32_t vreg[4][kVWords];
+  float sreg = 0.0f;                                   // a token's scale: K's, then V's threads
+  bool exists[4];                                      // of the stage in registers, by 16 tokens
+
+  auto load = [&](int n) {
+    const int t0 = range.begin + n * kAttnStage;
+    int64_t at[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) at[u] = page_row(p, it, t0 + 16 * u, &exists[u]);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      // rows of this wave in this pass: all in one group of 16 tokens
+      const int u = (i * kPass + wave * (kPass / kAttnWaves)) / 16;
+      const int64_t first = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
+      const char* src = kbase + (first + ((krow + i * kPass) & 15)) * row_bytes;
+      const int d = 8 * piece;
+      const bool in = FULL || d < dim;
+      if constexpr (kSame) {
+        const u32x4 x = load16(src + (in ? d : 0) * kBytes);
+        kreg[i] = in ? x : u32x4{0, 0, 0, 0};
+      } else {
+        const u32x2 x = load8(src + (in ? d : 0) * kBytes);
+        kreg[i] = in ? u32x4{x.x, x.y, 0, 0} : u32x4{0, 0, 0, 0};
+      }
+    }
+    const int64_t first = wave == 0 ? at[0] : wave == 1 ? at[1] : wave == 2 ? at[2] : at[3];
+    const int d = FULL ? chunk * kVD : min(chunk * kVD, dim - kVD);
+    const char* src = vbase + (first + 4 * g) * row_bytes + d * kBytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < kVWords; w += 4) {
+        if constexpr (kVWords >= 4) {
+          const u32x4 x = load16(src + i * row_bytes + 4 * w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vreg[i][w + e] = x[e];
+        } else if constexpr (kVWords == 2) {
+          const u32x2 x = load8(src + i * row_bytes);
+          vreg[i][0] = x.x;
+          vreg[i][1] = x.y;
+        } else {
+          vreg[i][0] = *(const uint32_t*)(src + i * row_bytes);
+        }
+      }
+    // scales: wave u brings those of tokens 16 u..; lanes 0..15 K's, 16..31 V's
+    if constexpr (!kSame)
+      if (lane < 32) sreg = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[first + c];
+  };
+  auto store = [&](int n) {
+    Stage<DB>& st = stage[n & 1];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = krow + i * kPass;
+      u32x4 x = kreg[i];
+      if constexpr (!kSame)
+        x = u32x4{widen_pair<KT, FMT, false>(kreg[i].x), widen_pair<KT, FMT, true>(kreg[i].x),
+                  widen_pair<KT, FMT, false>(kreg[i].y), widen_pair<KT, FMT, true>(kreg[i].y)};
+      st.k[r * kPieces + (piece ^ (r & 7))] = x;
+    }
+    // tokens that do not exist are zeros: a weight of 0 must not meet a NaN
+    const int t = range.begin + n * kAttnStage + 4 * quad;
+    const bool page = wave == 0 ? exists[0] : wave == 1 ? exists[1] : wave == 2 ? exists[2] : exists[3];
+    bool odd = false;
+    if (t + 4 > min(range.see_all, it.len) || !page) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          const uint32_t y = page && t + i < it.len ? vreg[i][w] : 0u;
+          vreg[i][w] = y;
+          if constexpr (kSame) odd |= non_finite_pair<T>(y);
+          if constexpr (FMT == W4A16_KV_E4M3) odd |= nan_codes(y);
+        }
+    }
+    // quad = 8 half + 4 u + lane group
+    uint32_t* base = (uint32_t*)(st.v + (quad >> 3) * (DB * 4));
+    const int u = (quad >> 2) & 1;
+#pragma unroll
+    for (int j = 0; j < kVD; ++j) {
+      const int line = j * 16 + chunk;
+      uint32_t x[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (kSame) {
+          x[h] = __builtin_amdgcn_perm(vreg[2 * h + 1][j / 2], vreg[2 * h][j / 2],
+                                       j & 1 ? 0x07060302u : 0x05040100u);
+        } else {
+          const uint32_t y = __builtin_amdgcn_perm(vreg[2 * h + 1][j / 4], vreg[2 * h][j / 4],
+                                                   j & 2 ? 0x07030602u : 0x05010400u);
+          x[h] = j & 1 ? widen_pair<PT, FMT, true>(y) : widen_pair<PT, FMT, false>(y);
+        }
+      }
+      *(u32x2*)(base + line * 16 + ((g ^ ((line >> 1) & 3)) * 4) + u * 2) = u32x2{x[0], x[1]};
+    }
+    if constexpr (!kSame)
+      if (lane < 32) (lane < 16 ? st.k_scale : st.v_scale)[16 * wave + c] = sreg;
+    if (odd) st.odd = 1;
+  };
+
+  Rows<T, FMT, DB, R> rw;
+  rw.init(p, it, row0 + wave * kWaveRows, dim, [&](int s) { return 32 * s + 8 * g; });
+
+  if (stages > 0) load(0);
+  if (tid < 2) stage[tid].odd = 0;
+  __syncthreads();
+  bool held[4] = {false, false, false, false};         // pages of the stage in LDS
+  if (stages > 0) {
+    store(0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) held[u] = exists[u];
+  }
+  rw.settle();
+  __syncthreads();
+  for (int n = 0; n < stages; ++n) {
+    if (n + 1 < stages) load(n + 1);
+    Stage<DB>& st = stage[n & 1];
+    if (busy) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int t0 = range.begin + n * kAttnStage + 32 * half;
+        if (t0 >= range.end) break;
+        const bool* on = held + 2 * half;
+        const bool edge = t0 + 32 > min(range.see_all, it.len) || !on[0] || !on[1];
+        rw.tile(
+            p, t0, edge, on,
+            [&](int u, int i) -> u32x4 {
+              const int r = 32 * half + 16 * u + c;
+              return st.k[r * kPieces + ((4 * i + g) ^ (r & 7))];
+            },
+            [&](int u) { return *(const f32x4*)&st.k_scale[32 * half + 16 * u + 4 * g]; },
+            []() {},
+            [&](uint32_t) -> bool { return __builtin_amdgcn_readfirstlane(st.odd) != 0; },
+            [&](int u) { return *(const f32x4*)&st.v_scale[32 * half + 16 * u + 4 * g]; },
+            [&](int j, uint32_t zero) -> u32x4 {
+              const int line = j * 16 + c + (int)zero;
+              return st.v[half * (DB * 4) + line * 4 + (g ^ ((line >> 1) & 3))];
+            });
+      }
+    }
+    if (n + 1 < stages) {
+      // the other stage was last read before the previous barrier
+      store(n + 1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) held[u] = exists[u];
+    }
+    __syncthreads();
+  }
+
+  // ---- a wave's rows are its own: straight to the output, or to the part
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float z = rw.denominator(r);
+    const int at = wave * kWaveRows + 16 * r + c;
+    if (at >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d0 = (4 * g + i) * kVD;
+      float o[kVD];
+#pragma unroll
+      for (int j = 0; j < kVD; j += 4) {
+        const f32x4 x = rw.sums(r, i, j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j + e] = x[e];
+      }
+      if (it.splits == 1) {
+        finish<T, kVD>(p, it, row0 + at, d0, dim, rw.top[r], z, TY::kLift, o);
+      } else {
+        float* part = p.parts + blockIdx.x * attn_part_floats(kRows, DB);
+#pragma unroll
+        for (int j = 0; j < kVD; j += 2) put2(part + at * DB + d0 + j, o[j], o[j + 1]);
+        if (d0 == 0) put2(part + kRows * DB + 2 * at, rw.top[r], z);
+      }
+    }
+  }
+  if (it.splits > 1 && arrive(p, it, &stage[0].odd))
+    join_parts<T, DB, kRows>(p, it, rows, dim, TY::kLift, (float*)l_raw);
+}
+
+template <typename T, int FMT, int DB, int R, bool WIDE>
 hipError_t launch_attn(const AttnParams& p, hipStream_t stream) {
   const dim3 grid((uint32_t)p.grid), block(64 * kAttnWaves);
-  if (p.cache.dim == DB)
-    hipLaunchKernelGGL((tree_attn_kernel<T, FMT, DB, R, true>), grid, block, 0, stream, p);
+  constexpr int kLds = WIDE ? 2 * (int)sizeof(Stage<DB>) : 0;
+  const bool full = p.cache.dim == DB;
+  void (*kernel)(AttnParams);
+  if constexpr (WIDE)
+    kernel = full ? attn_wide_kernel<T, FMT, DB, R, true> : attn_wide_kernel<T, FMT, DB, R, false>;
   else
-    hipLaunchKernelGGL((tree_attn_kernel<T, FMT, DB, R, false>), grid, block, 0, stream, p);
+    kernel = full ? attn_narrow_kernel<T, FMT, DB, R, true> : attn_narrow_kernel<T, FMT, DB, R, false>;
+  if (kLds > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, grid, block, kLds, stream, p);
   return hipGetLastError();
 }
 
-// One (dtype, format): row_blocks and the head dim pick the kernel.
+// One (dtype, format): the shape and the head dim pick the kernel.
 template <typename T, int FMT>
-hipError_t launch_attn_rows(const AttnParams& p, int row_blocks, hipStream_t stream) {
+hipError_t launch_attn_shape(const AttnParams& p, AttnKind kind, hipStream_t stream) {
   const int db = attn_dim_block(p.cache.dim);
   if (db == 256)
-    return row_blocks == 1 ? launch_attn<T, FMT, 256, 1>(p, stream)
-                           : launch_attn<T, FMT, 256, 2>(p, stream);
+    return kind == AttnKind::kNarrow1 ? launch_attn<T, FMT, 256, 1, false>(p, stream)
+                                      : launch_attn<T, FMT, 256, 1, true>(p, stream);
   if (db == 128)
-    return row_blocks == 1   ? launch_attn<T, FMT, 128, 1>(p, stream)
-           : row_blocks == 2 ? launch_attn<T, FMT, 128, 2>(p, stream)
-                             : launch_attn<T, FMT, 128, 4>(p, stream);
-  return row_blocks == 1   ? launch_attn<T, FMT, 64, 1>(p, stream)
-         : row_blocks == 2 ? launch_attn<T, FMT, 64, 2>(p, stream)
-                           : launch_attn<T, FMT, 64, 4>(p, stream);
+    return kind == AttnKind::kNarrow1   ? launch_attn<T, FMT, 128, 1, false>(p, stream)
+           : kind == AttnKind::kNarrow2 ? launch_attn<T, FMT, 128, 2, false>(p, stream)
+           : kind == AttnKind::kWide1   ? launch_attn<T, FMT, 128, 1, true>(p, stream)
+                                        : launch_attn<T, FMT, 128, 2, true>(p, stream);
+  return kind == AttnKind::kNarrow1   ? launch_attn<T, FMT, 64, 1, false>(p, stream)
+         : kind == AttnKind::kNarrow2 ? launch_attn<T, FMT, 64, 2, false>(p, stream)
+         : kind == AttnKind::kWide1   ? launch_attn<T, FMT, 64, 1, true>(p, stream)
+                                      : launch_attn<T, FMT, 64, 2, true>(p, stream);
 }
 
 }  // namespace serve
