@@ -135,7 +135,11 @@ w4a16_status score_workspace(int64_t tokens, int64_t vocab, int32_t top_k, int n
 
 // Work items aimed at: two workgroups per CU. Ranges of a sequence are split
 // no finer than that, nor below kAttnStep tokens.
-constexpr int kAttnItemsPerCu = 2;
+#ifndef ITEMS_N
+#define ITEMS_N 3
+#define ITEMS_W 2
+#endif
+
 // Most groups (sequence, row block, head) of one row block of 16 for which
 // sequences are split: beyond, the groups alone fill the device many times,
 // and the parts would only cost memory.
@@ -162,7 +166,7 @@ w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64
   s->kind = attn_kind(rows, (int)dim);
   s->rows = attn_rows(s->kind);
   const int64_t groups = sequences * div_up(rows, s->rows) * kv_heads;
-  s->target = groups <= kAttnMaxSplitGroups * 16 / s->rows ? kAttnItemsPerCu * num_cus : 0;
+  s->target = groups <= kAttnMaxSplitGroups * 16 / s->rows ? (s->rows <= 32 ? ITEMS_N : ITEMS_W) * num_cus : 0;
   s->grid = groups + s->target;
   if (s->grid >= kMaxInt)
     return report(W4A16_ERR_SHAPE, "too many sequences, tokens and heads for one launch");

@@ -167,20 +167,17 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   return false;
 }
 
-// Writes dims d0..d0+VD-1 of a finished row: o / z, and the row's lse. The
-// held maximum m is in log2, and z was summed `lift` above it.
-template <typename T, int VD>
-__device__ __forceinline__ void finish(const AttnParams& p, const Item& it, int row, int d0, int dim,
-                                       float m, float z, float lift, const float* o) {
+// Four dims from d0 of a finished row: o / z, and (with d0 = 0) the row's lse.
+// The held maximum m is in log2, and z was summed `lift` above it.
+template <typename T>
+__device__ __forceinline__ void finish4(const AttnParams& p, const Item& it, int row, int d0, int dim,
+                                        float m, float z, float lift, f32x4 o) {
   const int query = row / p.group, head = it.head * p.group + row - query * p.group;
   const int64_t at = (int64_t)(it.start + query) * p.hq + head;
   const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-  uint16_t* dst = p.out + at * dim + d0;
-#pragma unroll
-  for (int j = 0; j < VD; j += 4)
-    if (d0 + j < dim)
-      *(u32x2*)(dst + j) = u32x2{pair<T>(o[j] * inv, o[j + 1] * inv),
-                                 pair<T>(o[j + 2] * inv, o[j + 3] * inv)};
+  if (d0 < dim)
+    *(u32x2*)(p.out + at * dim + d0) = u32x2{pair<T>(o[0] * inv, o[1] * inv),
+                                             pair<T>(o[2] * inv, o[3] * inv)};
   if (d0 == 0)
     p.lse[at] = z == 0.0f ? kNegInf : 0.69314718055994530942f * (m - lift + __log2f(z));
 }
@@ -200,7 +197,32 @@ struct Types {
   static constexpr float kLift = P::kCode == W4A16_F16 ? 6.0f : 0.0f;
 };
 
+#ifndef LBN
+#define LBN 3
+#endif
 constexpr float kSlack = 8.0f;  // how far (log2) a score may exceed the held maximum
+
+// 16-bit values: 1, the exponent's mask (all ones: infinity or NaN), and, for a
+// word of two, the halves that are such (as masks), and 1 in each half of a kind.
+template <typename T>
+constexpr uint32_t kOne16 = T::kCode == W4A16_F16 ? 0x3C00u : 0x3F80u;
+template <typename T>
+constexpr uint32_t kExp16 = T::kCode == W4A16_F16 ? 0x7C00u : 0x7F80u;
+template <typename T>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
+  return ((x & kExp16<T>) == kExp16<T> ? 0xFFFFu : 0u) |
+         (((x >> 16) & kExp16<T>) == kExp16<T> ? 0xFFFF0000u : 0u);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t ones_where(uint32_t x, int kind) {
+  auto is = [&](uint32_t h) {
+    return kind == 0 ? h == kExp16<T> : kind == 1 ? h == (kExp16<T> | 0x8000u) : (h & 0x7FFFu) > kExp16<T>;
+  };
+  return (is(x & 0xFFFFu) ? kOne16<T> : 0u) | (is(x >> 16) ? kOne16<T> << 16 : 0u);
+}
+__device__ __forceinline__ bool nan_codes(uint32_t y) {  // of e4m3: seven ones
+  return (((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
 
 // A wave's rows: R blocks of 16, lane (g, c) holding row c of each.
 template <typename T, int FMT, int DB, int R>
@@ -236,8 +258,10 @@ struct Rows {
         const int d = dim_of(s);
         q[r][s] = u32x4{0, 0, 0, 0};
         if (d < dim) q[r][s] = load16(src + d);
+        // the largest score is the largest product times a factor >= 0
+        if (p.scale_log2 < 0.0f) q[r][s] ^= 0x80008000u;
       }
-      factor[r] = p.scale_log2;
+      factor[r] = fabsf(p.scale_log2);
       top[r] = kNegInf;
       total[r] = 0.0f;
 #pragma unroll
@@ -257,7 +281,7 @@ struct Rows {
         const bool some = big >= 0x00800000u && big < 0x7F800000u;
         const int by = some ? min(14 - e, 126) : 0;
         const float up = ldexpf(1.0f, by);
-        factor[r] = ldexpf(p.scale_log2, -by);
+        factor[r] = ldexpf(factor[r], -by);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) q[r][s] = narrow8<F16>(widen8<T>(q[r][s]) * up);
       }
@@ -282,19 +306,20 @@ struct Rows {
 
   // One tile of 32 tokens from t0. k_op(u, i): operand of half tile u and step
   // i; k_scale(u), v_scale(u): scales of this lane's 4 tokens; after(): called
-  // once the K operands are consumed; v_op(j, 0): operand of O^T's tile j. `edge`
-  // (uniform): some token may be unseen by some row; exists[u]: half tile u lies
-  // on a page. v_edge(in): lets the caller clear V of tokens that do not exist
+  // once the K operands are consumed; v_op(j): operand of O^T's tile j. EDGE: some
+  // token may be unseen by some row; without TREE no token is unseen that exists.
+  // exists[u]: half tile u lies on a page. v_edge(in): lets the caller clear V of tokens that do not exist
   // (bit 4u + i of `in`: this lane's token does) and say (uniform) whether V
   // holds an infinity or NaN.
-  template <typename KOp, typename KScale, typename After, typename VEdge, typename VScale,
-            typename VOp>
-  __device__ __forceinline__ void tile(const AttnParams& p, int t0, bool edge, const bool* exists,
+  template <bool EDGE, bool TREE, typename KOp, typename KScale, typename After, typename VEdge,
+            typename VScale, typename VOp, typename Fresh>
+  __device__ __forceinline__ void tile(const AttnParams& p, int t0, const bool* exists,
                                        KOp k_op, KScale k_scale, After after, VEdge v_edge,
-                                       VScale v_scale, VOp v_op) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-    // ---- S^T, in units of log2
+                                       VScale v_scale, VOp v_op, Fresh fresh) {
+    const int g = (threadIdx.x & 63) >> 4;
+    // ---- S^T: in units of log2, or (16-bit caches) raw, `unit` to be multiplied
     f32x4 s[R][2];
+    const float unit = TY::kSame ? factor[0] : 1.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -306,39 +331,36 @@ struct Rows {
         for (int r = 0; r < R; ++r) s[r][u] = mfma16<typename TY::K>(a, q[r][i], s[r][u]);
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if constexpr (TY::kSame)
-          s[r][u] *= factor[r];
-        else
-          s[r][u] *= k_scale(u) * factor[r];
-      }
+      for (int r = 0; r < R; ++r)
+        if constexpr (!TY::kSame) s[r][u] *= k_scale(u) * factor[r];
     }
     after();
 
     // ---- what a row does not see: score -inf (and, below, weight 0)
     uint32_t seen[R], in_all = 0xFF;      // bit 4u + i: this lane's token (u, i)
     bool apart = false;
-    if (edge) {
+    if constexpr (EDGE) {
       in_all = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          in_all |= exists[u] && t0 + 16 * u + 4 * g + i < len ? 1u << (4 * u + i) : 0u;
+      for (int u = 0; u < 2; ++u) {
+        const int left = exists[u] ? min(max(len - (t0 + 16 * u + 4 * g), 0), 4) : 0;
+        in_all |= ((1u << left) - 1) << (4 * u);
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        seen[r] = 0;
+        seen[r] = in_all;
+        if constexpr (TREE) {
+#pragma unroll 1                          // rare: keep it small
+          for (int x = 0; x < 8; ++x)
+            if (!sees(p, r, t0 + 16 * (x >> 2) + 4 * g + (x & 3))) seen[r] &= ~(1u << x);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t bit = 1u << (4 * u + i);
-            const bool in = (in_all & bit) && sees(p, r, t0 + 16 * u + 4 * g + i);
-            seen[r] |= in ? bit : 0u;
-            s[r][u][i] = in ? s[r][u][i] : kNegInf;
-          }
+          for (int i = 0; i < 4; ++i)
+            s[r][u][i] = (seen[r] >> (4 * u + i)) & 1 ? s[r][u][i] : kNegInf;
       }
-      apart = v_edge(in_all);
+      apart = v_edge(in_all) && TREE;
     }
 
     // ---- the held maximum rises only when a score exceeds it by 2^8
@@ -349,12 +371,13 @@ struct Rows {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         vs[u] = v_scale(u);
+        // scales of tokens that do not exist must not matter (NaN and infinite
+        // ones of those that do set no reference: see below)
+        if constexpr (EDGE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // tokens that do not exist, infinities and NaN set no reference
-          const bool use = (in_all >> (4 * u + i) & 1) && vs[u][i] < __builtin_inff();
-          vhigh = use ? fmaxf(vhigh, vs[u][i]) : vhigh;
+          for (int i = 0; i < 4; ++i) vs[u][i] = (in_all >> (4 * u + i)) & 1 ? vs[u][i] : 0.0f;
         }
+        vhigh = fmaxf(fmaxf(vhigh, fmaxf(vs[u][0], vs[u][1])), fmaxf(vs[u][2], vs[u][3]));
       }
       rise = vhigh > vref;
     }
@@ -362,20 +385,26 @@ struct Rows {
     for (int r = 0; r < R; ++r) {
       float m = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3]));
       m = fmaxf(m, fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      high[r] = m;
-      rise |= m > top[r] + kSlack;
+      high[r] = m * unit;
+      rise |= high[r] > top[r] + kSlack;
     }
     if (__any(rise)) {
       float down = 1.0f;
       if constexpr (!TY::kSame) {
-        vhigh = fmaxf(vhigh, __shfl_xor(vhigh, 16));
-        vhigh = fmaxf(vhigh, __shfl_xor(vhigh, 32));
-        if (vhigh > vref) {               // the next power of two above
-          const float to = __uint_as_float(
-              min((__float_as_uint(vhigh) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
-          down = vref == to ? 1.0f : vref / to;
-          vref = to;
-        }
+        // the next power of two above the largest finite scale
+        float most = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            most = vs[u][i] < __builtin_inff() ? fmaxf(most, vs[u][i]) : most;
+        most = fmaxf(most, __shfl_xor(most, 16));
+        most = fmaxf(most, __shfl_xor(most, 32));
+        const float above =
+            __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
+        const float to = most > vref ? above : vref;
+        down = to == vref ? 1.0f : vref / to;
+        vref = to;
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -405,11 +434,11 @@ struct Rows {
         float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(s[r][u][i] - ref);
+          x[i] = __builtin_amdgcn_exp2f(TY::kSame ? fmaf(s[r][u][i], unit, -ref) : s[r][u][i] - ref);
           total[r] += x[i];
           if constexpr (!TY::kSame) x[i] *= vs[u][i];
         }
-        if (edge) {
+        if constexpr (EDGE) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = (seen[r] >> (4 * u + i)) & 1 ? x[i] : 0.0f;
         }
@@ -419,33 +448,43 @@ struct Rows {
     }
 
     // ---- O^T
-    if (!apart) {
+    if (!TREE || !apart) {
 #pragma unroll
       for (int j = 0; j < kVD; ++j) {
-        const u32x4 a = v_op(j, 0u);
+        const u32x4 a = v_op(j);
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[r][j] = mfma16<typename TY::P>(a, w[r], acc[r][j]);
       }
     } else {
-      // An infinity or NaN among values that some rows may not see: token by
-      // token, and a row that does not see the token keeps its sums.
-#pragma unroll 1
-      for (int t = 0; t < kAttnTile; ++t) {
-        const int tu = t >> 4, tg = (t >> 2) & 3, ti = t & 3;
-        u32x4 only = {0, 0, 0, 0};
-        const uint32_t bits = tg == g ? (ti & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+      // Infinities or NaN among values that some rows may not see: the product
+      // takes 0 in their place, and three products of ones tell which sums they
+      // reach. fresh(): operands from here on are formed anew, not for both branches.
+      fresh();
+      u32x4 sees_it[R];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) only[e] = e == 2 * tu + (ti >> 1) ? bits : 0u;
-        uint32_t zero = 0;                // opaque: operands are formed anew for each token,
-        asm volatile("" : "+v"(zero));    // not kept in registers over the loop
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < kVD; ++j) {
-          const u32x4 a = v_op(j, zero) & only;
+        for (int e = 0; e < 4; ++e)
+          sees_it[r][e] = ((seen[r] >> (2 * e)) & 1 ? kOne16<typename TY::P> : 0u) |
+                          ((seen[r] >> (2 * e + 1)) & 1 ? kOne16<typename TY::P> << 16 : 0u);
+#pragma unroll
+      for (int j = 0; j < kVD; ++j) {
+        u32x4 a = v_op(j), finite;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) finite[e] = a[e] & ~odd_halves<typename TY::P>(a[e]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r][j] = mfma16<typename TY::P>(finite, w[r], acc[r][j]);
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind) {  // +inf, -inf, NaN
+          u32x4 at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) at[e] = ones_where<typename TY::P>(a[e], kind);
+          const float value = kind == 0 ? __builtin_inff() : kind == 1 ? kNegInf : __builtin_nanf("");
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const bool in = (__shfl((int)seen[r], tg * 16 + c) >> (4 * tu + ti)) & 1;
-            const f32x4 y = mfma16<typename TY::P>(a, w[r] & only, acc[r][j]);
-            acc[r][j] = in ? y : acc[r][j];
+            const f32x4 n = mfma16<typename TY::P>(at, sees_it[r], f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][j][i] += n[i] > 0.0f ? value : 0.0f;
           }
         }
       }
@@ -465,16 +504,6 @@ struct Rows {
   }
 };
 
-// Word x (two 16-bit values) or code word y holds an infinity or NaN.
-template <typename T>
-__device__ __forceinline__ bool non_finite_pair(uint32_t x) {
-  constexpr uint32_t kExp = T::kCode == W4A16_F16 ? 0x7C00u : 0x7F80u;
-  return (x & kExp) == kExp || ((x >> 16) & kExp) == kExp;
-}
-__device__ __forceinline__ bool nan_codes(uint32_t y) {  // e4m3: seven ones
-  return (((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-}
-
 // Tokens [begin, end) of an item, and the first that some row of it may not see.
 struct Range {
   int begin, end, see_all;
@@ -490,25 +519,44 @@ __device__ __forceinline__ Range range_of(const AttnParams& p, const Item& it, i
   return r;
 }
 
-// The page of token t (uniform): its first row (of head_dim values, or scales)
-// for the item's head, and whether there is one; row 0 where there is not.
-__device__ __forceinline__ int64_t page_row(const AttnParams& p, const Item& it, int t, bool* ok) {
-  const int page = t < it.len ? p.block_table[it.seq * p.table_stride + (t >> p.cache.page_shift)] : -1;
-  *ok = page >= 0 && page < p.cache.pages;
+// The page of token t (uniform; a scalar load), and its first row (of head_dim
+// values, or of scales) for the item's head; row 0 where there is no such page.
+__device__ __forceinline__ int page_of(const AttnParams& p, const Item& it, int t) {
+  // the constant address space: nothing writes the table while the kernel runs,
+  // so the load may be a scalar one, apart from the vector loads' counter
+  typedef const __attribute__((address_space(4))) int32_t* Table;
+  return ((Table)p.block_table)[it.seq * p.table_stride + (min(t, it.len - 1) >> p.cache.page_shift)];
+}
+__device__ __forceinline__ int64_t row_of(const AttnParams& p, const Item& it, int page, int t, bool* ok) {
+  *ok = page >= 0 && page < p.cache.pages && t < it.len;
   return (((int64_t)(*ok ? page : 0) * p.cache.heads + it.head) << p.cache.page_shift) +
          (t & ((1 << p.cache.page_shift) - 1));
 }
 
-// Stores of a part, and the loads that join parts, go to the device's point
-// of coherence; the wait and the counter in arrive() order them.
-__device__ __forceinline__ void put2(float* at, float a, float b) {
-  __hip_atomic_store((uint64_t*)at, (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32),
-                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ f32x2 get2(const float* at) {
-  const uint64_t x = __hip_atomic_load((const uint64_t*)at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return f32x2{__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))};
-}
+// The parts, as a bounded buffer. A part's rows (DB floats each), then their
+// statistics (maximum, denominator). Stores are written through to the device's
+// point of coherence and loads read there (sc1), 16 bytes a lane and 256
+// contiguous ones for the 16 lanes of a row; the wait and the counter in
+// arrive() order them.
+struct Parts {
+  __amdgpu_buffer_rsrc_t buffer;
+  static constexpr int kSc1 = 16;
+  __device__ __forceinline__ Parts(const AttnParams& p, int part_floats)
+      : buffer(__builtin_amdgcn_make_buffer_rsrc(p.parts, 0, p.grid * part_floats * 4, 0x00020000)) {}
+  __device__ __forceinline__ void put4(uint32_t at, f32x4 x) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), buffer, (int)(4 * at), 0, kSc1);
+  }
+  __device__ __forceinline__ void put2(uint32_t at, float a, float b) const {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{a, b}), buffer, (int)(4 * at),
+                                          0, kSc1);
+  }
+  __device__ __forceinline__ f32x4 get4(uint32_t at) const {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer, (int)(4 * at), 0, kSc1));
+  }
+  __device__ __forceinline__ f32x2 get2(uint32_t at) const {
+    return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(buffer, (int)(4 * at), 0, kSc1));
+  }
+};
 
 // Whether this workgroup is the last of its group's splits to arrive.
 __device__ __forceinline__ bool arrive(const AttnParams& p, const Item& it, int* flag) {
@@ -530,65 +578,67 @@ __device__ __forceinline__ bool arrive(const AttnParams& p, const Item& it, int*
 }
 
 // The last workgroup of a group joins its parts, in an order that does not
-// depend on who arrived when. 16 lanes hold a row (VD dims each); with fewer
-// than 16 rows several such lane rows share a row's splits, and are joined
+// depend on who arrived when. 16 lanes hold a row (dims 64 h + 4 lane..); with
+// fewer than 9 rows several such lane rows share a row's splits, and are joined
 // through `lds` (16 rows of DB + 4 floats).
 template <typename T, int DB, int ROWS>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, int rows, int dim,
                                            float lift, float* lds) {
-  constexpr int kVD = DB / 16, kPad = DB + 4;
-  constexpr int64_t kPart = attn_part_floats(ROWS, DB);
-  const int slot = threadIdx.x >> 4, chunk = threadIdx.x & 15;
-  const int64_t stride = (int64_t)it.blocks * p.cache.heads * kPart;
-  const float* parts = p.parts + (int64_t)it.first * kPart;
+  constexpr int kH = DB / 64, kPad = DB + 4;
+  constexpr int kPart = (int)attn_part_floats(ROWS, DB);
+  constexpr int kDeep = 16 / kH;          // parts in flight
+  const Parts parts(p, kPart);
+  const int slot = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+  const uint32_t stride = (uint32_t)(it.blocks * p.cache.heads) * kPart;
+  const uint32_t first = (uint32_t)it.first * kPart;
   rows = min(rows, ROWS);
-  int held = 16;                          // rows at a time: 1, 2, 4, 8 or 16
-  while (held / 2 >= rows) held /= 2;
+  const int held = min(rows, 16);         // rows at a time
   const int share = 16 / held, lead = slot / held;
   for (int at0 = 0; at0 < rows; at0 += held) {
-    const int at = at0 + slot % held;
-    const float* base = parts + (int64_t)at * DB + chunk * kVD;
-    const float* stats = parts + ROWS * DB + 2 * at;
-    float m = kNegInf, z = 0.0f, o[kVD];
+    const int at = at0 + slot - lead * held;
+    const uint32_t base = first + at * DB + 4 * l16, stats = first + ROWS * DB + 2 * at;
+    float m = kNegInf, z = 0.0f;
+    f32x4 o[kH];
 #pragma unroll
-    for (int j = 0; j < kVD; ++j) o[j] = 0.0f;
-    if (at < rows) {
-      for (int sp = lead + share * chunk; sp < it.splits; sp += 16 * share)
-        m = fmaxf(m, get2(stats + sp * stride).x);
-#pragma unroll
-      for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s));
-      constexpr int kDeep = 48 / kVD;     // parts in flight
+    for (int h = 0; h < kH; ++h) o[h] = f32x4{0, 0, 0, 0};
+    if (at < rows && lead < share) {
 #pragma unroll 1
       for (int s0 = lead; s0 < it.splits; s0 += share * kDeep) {
-        f32x2 st[kDeep], x[kDeep][kVD / 2];
+        f32x2 st[kDeep];
+        f32x4 x[kDeep][kH];
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-          const int sp = s0 + d * share;
-          if (sp < it.splits) {
-            st[d] = get2(stats + sp * stride);
+        for (int d = 0; d < kDeep; ++d) {  // past the last split: that one again, not counted
+          const uint32_t off = (uint32_t)min(s0 + d * share, it.splits - 1) * stride;
+          st[d] = parts.get2(stats + off);
 #pragma unroll
-            for (int j = 0; j < kVD; j += 2) x[d][j / 2] = get2(base + sp * stride + j);
-          }
+          for (int h = 0; h < kH; ++h) x[d][h] = parts.get4(base + off + 64 * h);
         }
+        float big = m;
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) big = fmaxf(big, st[d].x);
+        const float f0 = m == big ? 1.0f : __builtin_amdgcn_exp2f(m - big);
+        m = big;
+        z *= f0;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) o[h] *= f0;
 #pragma unroll
         for (int d = 0; d < kDeep; ++d)
           if (s0 + d * share < it.splits) {
             const float f = st[d].x == m ? 1.0f : __builtin_amdgcn_exp2f(st[d].x - m);
             z = fmaf(f, st[d].y, z);
 #pragma unroll
-            for (int j = 0; j < kVD; j += 2) {
-              o[j] = fmaf(f, x[d][j / 2].x, o[j]);
-              o[j + 1] = fmaf(f, x[d][j / 2].y, o[j + 1]);
-            }
+            for (int h = 0; h < kH; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[h][e] = fmaf(f, x[d][h][e], o[h][e]);
           }
       }
     }
-    if (share > 1) {                      // the same in the whole workgroup; rows <= 8
+    if (share > 1) {                      // the same in the whole workgroup
       __syncthreads();
       float* mine = lds + slot * kPad;
 #pragma unroll
-      for (int j = 0; j < kVD; ++j) mine[chunk * kVD + j] = o[j];
-      if (chunk == 0) {
+      for (int h = 0; h < kH; ++h) *(f32x4*)(mine + 64 * h + 4 * l16) = o[h];
+      if (l16 == 0) {
         mine[DB] = m;
         mine[DB + 1] = z;
       }
@@ -597,26 +647,32 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
         float big = m;
         for (int s = 1; s < share; ++s) big = fmaxf(big, lds[(slot + s * held) * kPad + DB]);
         const float f0 = m == big ? 1.0f : __builtin_amdgcn_exp2f(m - big);
+        m = big;
         z *= f0;
 #pragma unroll
-        for (int j = 0; j < kVD; ++j) o[j] *= f0;
+        for (int h = 0; h < kH; ++h) o[h] *= f0;
         for (int s = 1; s < share; ++s) {
           const float* other = lds + (slot + s * held) * kPad;
           const float f = other[DB] == big ? 1.0f : __builtin_amdgcn_exp2f(other[DB] - big);
           z = fmaf(f, other[DB + 1], z);
 #pragma unroll
-          for (int j = 0; j < kVD; ++j) o[j] = fmaf(f, other[chunk * kVD + j], o[j]);
+          for (int h = 0; h < kH; ++h) o[h] += f * *(const f32x4*)(other + 64 * h + 4 * l16);
         }
-        m = big;
       }
     }
-    if (lead == 0 && at < rows) finish<T, kVD>(p, it, it.block * ROWS + at, chunk * kVD, dim, m, z, lift, o);
+    if (lead == 0 && at < rows)
+#pragma unroll
+      for (int h = 0; h < kH; ++h)
+        finish4<T>(p, it, it.block * ROWS + at, 64 * h + 4 * l16, dim, m, z, lift, o[h]);
   }
 }
 
 // ---------------------------------------------------------------- few rows
-template <typename T, int FMT, int DB, int R, bool FULL>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnParams p) {
+// Without TREE (one new token per sequence and no mask) the kernel needs no
+// masks but the length's, and its registers leave room for three waves per
+// SIMD instead of two (16 rows, up to 128 dims).
+template <typename T, int FMT, int DB, int R, bool FULL, bool TREE>
+__global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? LBN : 2) void attn_narrow_kernel(AttnParams p) {
   using TY = Types<T, FMT>;
   constexpr bool kSame = TY::kSame;
   constexpr int kRows = 16 * R;
@@ -651,23 +707,28 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
   int64_t at[2];                               // rows of the next tile's half tiles
   bool ok[2] = {false, false};
 
-  auto look_up = [&](int n) {
+  int pages[2];
+  auto look_up = [&](int n) {                  // two tiles ahead: scalar loads, never waited for
+#pragma unroll
+    for (int u = 0; u < 2; ++u) pages[u] = page_of(p, it, range.begin + n * kAttnTile + 16 * u);
+  };
+  auto take_rows = [&](int n) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      at[u] = page_row(p, it, range.begin + n * kAttnTile + 16 * u, &ok[u]);
+      at[u] = row_of(p, it, pages[u], range.begin + n * kAttnTile + 16 * u, &ok[u]);
   };
   auto load_k = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const char* src = kbase + at[u] * row_bytes + c * row_bytes;
+      const char* src = kbase + at[u] * row_bytes;  // uniform; lanes add 32-bit offsets
 #pragma unroll
       for (int i = 0; i < kKLoads; ++i) {
         const int d = i * (64 / kBytes) + g * (16 / kBytes);
         if constexpr (FULL) {
-          kreg[u][i] = load16(src + d * kBytes);
+          kreg[u][i] = load16(src + (uint32_t)(c * row_bytes + d * kBytes));
         } else {                               // dims past the head's: zeros
           const bool in = d < dim;
-          const u32x4 x = load16(src + (in ? d : 0) * kBytes);
+          const u32x4 x = load16(src + (uint32_t)(c * row_bytes + (in ? d : 0) * kBytes));
           kreg[u][i] = in ? x : u32x4{0, 0, 0, 0};
         }
       }
@@ -678,21 +739,22 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int d = FULL ? c * kVD : min(c * kVD, dim - kVD);  // dims past the head's: not stored
-      const char* src = vbase + at[u] * row_bytes + 4 * g * row_bytes + d * kBytes;
+      const char* src = vbase + at[u] * row_bytes;
+      const uint32_t off = 4 * g * row_bytes + d * kBytes;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int w = 0; w < kVWords; w += 4) {
           if constexpr (kVWords >= 4) {
-            const u32x4 x = load16(src + i * row_bytes + 4 * w);
+            const u32x4 x = load16(src + (off + i * row_bytes + 4 * w));
 #pragma unroll
             for (int e = 0; e < 4; ++e) vreg[u][i][w + e] = x[e];
           } else if constexpr (kVWords == 2) {
-            const u32x2 x = load8(src + i * row_bytes);
+            const u32x2 x = load8(src + (off + i * row_bytes));
             vreg[u][i][0] = x.x;
             vreg[u][i][1] = x.y;
           } else {
-            vreg[u][i][0] = *(const uint32_t*)(src + i * row_bytes);
+            vreg[u][i][0] = *(const uint32_t*)(src + (off + i * row_bytes));
           }
         }
       if constexpr (!kSame) vscale[u] = *(const f32x4*)(p.cache.v_scale + at[u] + 4 * g);
@@ -701,6 +763,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
 
   if (wave < tiles) {
     look_up(wave);
+    take_rows(wave);
+    look_up(wave + kAttnWaves);
     load_k();
     load_v();
   }
@@ -710,14 +774,19 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
   });
 
   rw.settle();
-  for (int n = wave; n < tiles; n += kAttnWaves) {
+  int n = wave;
+  auto tile = [&](auto edge) {
     const int t0 = range.begin + n * kAttnTile;
     const bool exists[2] = {ok[0], ok[1]};
-    const bool edge = t0 + kAttnTile > min(range.see_all, it.len) || !exists[0] || !exists[1];
-    const bool more = n + kAttnWaves < tiles;
-    if (more) look_up(n + kAttnWaves);         // scalar loads, back before they are needed
-    rw.tile(
-        p, t0, edge, exists,
+    // the first loop's tiles all have a next one: no branches, hence no copies of
+    // what the next loads replace
+    const bool more = !decltype(edge)::value || n + kAttnWaves < tiles;
+    if (more) {
+      take_rows(n + kAttnWaves);
+      look_up(n + 2 * kAttnWaves);
+    }
+    rw.template tile<decltype(edge)::value, TREE>(
+        p, t0, exists,
         [&](int u, int i) -> u32x4 {
           if constexpr (kSame) {
             return kreg[u][i];
@@ -742,37 +811,55 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
               for (int x = 0; x < kVWords; ++x) {
                 const uint32_t y = (in >> (4 * u + i)) & 1 ? vreg[u][i][x] : 0u;
                 vreg[u][i][x] = y;
-                if constexpr (kSame) odd |= non_finite_pair<T>(y);
+                if constexpr (kSame) odd |= odd_halves<T>(y) != 0;
                 if constexpr (FMT == W4A16_KV_E4M3) odd |= nan_codes(y);
               }
+          if constexpr (FMT == W4A16_KV_INT8 || !TREE) return false;
           return __any(odd);
         },
         [&](int u) { return vscale[u]; },
         // tokens (i, i + 1) of dim j side by side: one permute per word
-        [&](int j, uint32_t zero) -> u32x4 {
+        [&](int j) -> u32x4 {
           u32x4 a;
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if constexpr (kSame) {
-                a[2 * u + h] = __builtin_amdgcn_perm(vreg[u][2 * h + 1][j / 2], vreg[u][2 * h][j / 2] | zero,
+                a[2 * u + h] = __builtin_amdgcn_perm(vreg[u][2 * h + 1][j / 2], vreg[u][2 * h][j / 2],
                                                      j & 1 ? 0x07060302u : 0x05040100u);
               } else {
                 const uint32_t y = __builtin_amdgcn_perm(
-                    vreg[u][2 * h + 1][j / 4], vreg[u][2 * h][j / 4] | zero,
+                    vreg[u][2 * h + 1][j / 4], vreg[u][2 * h][j / 4],
                     j & 2 ? 0x07030602u : 0x05010400u);
                 using P = typename TY::P;
                 a[2 * u + h] = j & 1 ? widen_pair<P, FMT, true>(y) : widen_pair<P, FMT, false>(y);
               }
             }
           return a;
+        },
+        [&]() {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int x = 0; x < kVWords; ++x) asm volatile("" : "+v"(vreg[u][i][x]));
         });
     if (more) load_v();
-  }
+    n += kAttnWaves;
+  };
+  // First the tiles that every row sees whole, then (in code of its own, which
+  // costs the first loop no registers) those at the end, or after a lost page.
+  const int whole = min(range.see_all, it.len);
+  while (n + kAttnWaves < tiles && range.begin + (n + 1) * kAttnTile <= whole && ok[0] && ok[1])
+    tile(std::false_type{});
+  while (n < tiles) tile(std::true_type{});
 
   // ---- join the four waves, a row block at a time
-  const int row = tid >> 4, chunk = tid & 15;
+  constexpr int kH = DB / 64, kPart = (int)attn_part_floats(kRows, DB);
+  const Parts parts(p, kPart);
+  const int row = tid >> 4, l16 = tid & 15;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float sum = rw.denominator(r);
@@ -787,26 +874,29 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_narrow_kernel(AttnPar
     float m = kNegInf;
 #pragma unroll
     for (int v = 0; v < kAttnWaves; ++v) m = fmaxf(m, l_stat[v][row].x);
-    float z = 0.0f, o[kVD];
+    float z = 0.0f;
+    f32x4 o[kH];
 #pragma unroll
-    for (int j = 0; j < kVD; ++j) o[j] = 0.0f;
+    for (int h = 0; h < kH; ++h) o[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int v = 0; v < kAttnWaves; ++v) {
       const f32x2 st = l_stat[v][row];
       const float f = st.x == m ? 1.0f : __builtin_amdgcn_exp2f(st.x - m);
       z = fmaf(f, st.y, z);
 #pragma unroll
-      for (int j = 0; j < kVD; ++j) o[j] = fmaf(f, l_sum[v][row][chunk * kVD + j], o[j]);
+      for (int h = 0; h < kH; ++h) o[h] += f * *(const f32x4*)&l_sum[v][row][64 * h + 4 * l16];
     }
     const int at = 16 * r + row;
     if (at < rows) {
       if (it.splits == 1) {
-        finish<T, kVD>(p, it, row0 + at, chunk * kVD, dim, m, z, TY::kLift, o);
-      } else {
-        float* part = p.parts + blockIdx.x * attn_part_floats(kRows, DB);
 #pragma unroll
-        for (int j = 0; j < kVD; j += 2) put2(part + at * DB + chunk * kVD + j, o[j], o[j + 1]);
-        if (chunk == 0) put2(part + kRows * DB + 2 * at, m, z);
+        for (int h = 0; h < kH; ++h)
+          finish4<T>(p, it, row0 + at, 64 * h + 4 * l16, dim, m, z, TY::kLift, o[h]);
+      } else {
+        const uint32_t part = (uint32_t)blockIdx.x * kPart;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) parts.put4(part + at * DB + 64 * h + 4 * l16, o[h]);
+        if (l16 == 0) parts.put2(part + kRows * DB + 2 * at, m, z);
       }
     }
   }
@@ -867,44 +957,52 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   float sreg = 0.0f;                                   // a token's scale: K's, then V's threads
   bool exists[4];                                      // of the stage in registers, by 16 tokens
 
+  int pages[4];                                        // of the stage to be loaded next
+  auto look_up = [&](int n) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pages[u] = page_of(p, it, range.begin + n * kAttnStage + 16 * u);
+  };
   auto load = [&](int n) {
     const int t0 = range.begin + n * kAttnStage;
     int64_t at[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) at[u] = page_row(p, it, t0 + 16 * u, &exists[u]);
+    for (int u = 0; u < 4; ++u) at[u] = row_of(p, it, pages[u], t0 + 16 * u, &exists[u]);
+    look_up(n + 1);                                    // scalar loads, back by the next stage
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       // rows of this wave in this pass: all in one group of 16 tokens
       const int u = (i * kPass + wave * (kPass / kAttnWaves)) / 16;
       const int64_t first = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
-      const char* src = kbase + (first + ((krow + i * kPass) & 15)) * row_bytes;
+      const char* src = kbase + first * row_bytes;     // uniform; lanes add 32-bit offsets
       const int d = 8 * piece;
       const bool in = FULL || d < dim;
+      const uint32_t off = ((krow + i * kPass) & 15) * row_bytes + (in ? d : 0) * kBytes;
       if constexpr (kSame) {
-        const u32x4 x = load16(src + (in ? d : 0) * kBytes);
+        const u32x4 x = load16(src + off);
         kreg[i] = in ? x : u32x4{0, 0, 0, 0};
       } else {
-        const u32x2 x = load8(src + (in ? d : 0) * kBytes);
+        const u32x2 x = load8(src + off);
         kreg[i] = in ? u32x4{x.x, x.y, 0, 0} : u32x4{0, 0, 0, 0};
       }
     }
     const int64_t first = wave == 0 ? at[0] : wave == 1 ? at[1] : wave == 2 ? at[2] : at[3];
     const int d = FULL ? chunk * kVD : min(chunk * kVD, dim - kVD);
-    const char* src = vbase + (first + 4 * g) * row_bytes + d * kBytes;
+    const char* src = vbase + first * row_bytes;
+    const uint32_t off = 4 * g * row_bytes + d * kBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int w = 0; w < kVWords; w += 4) {
         if constexpr (kVWords >= 4) {
-          const u32x4 x = load16(src + i * row_bytes + 4 * w);
+          const u32x4 x = load16(src + (off + i * row_bytes + 4 * w));
 #pragma unroll
           for (int e = 0; e < 4; ++e) vreg[i][w + e] = x[e];
         } else if constexpr (kVWords == 2) {
-          const u32x2 x = load8(src + i * row_bytes);
+          const u32x2 x = load8(src + (off + i * row_bytes));
           vreg[i][0] = x.x;
           vreg[i][1] = x.y;
         } else {
-          vreg[i][0] = *(const uint32_t*)(src + i * row_bytes);
+          vreg[i][0] = *(const uint32_t*)(src + (off + i * row_bytes));
         }
       }
     // scales: wave u brings those of tokens 16 u..; lanes 0..15 K's, 16..31 V's
@@ -933,7 +1031,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
         for (int w = 0; w < kVWords; ++w) {
           const uint32_t y = page && t + i < it.len ? vreg[i][w] : 0u;
           vreg[i][w] = y;
-          if constexpr (kSame) odd |= non_finite_pair<T>(y);
+          if constexpr (kSame) odd |= odd_halves<T>(y) != 0;
           if constexpr (FMT == W4A16_KV_E4M3) odd |= nan_codes(y);
         }
     }
@@ -965,7 +1063,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   Rows<T, FMT, DB, R> rw;
   rw.init(p, it, row0 + wave * kWaveRows, dim, [&](int s) { return 32 * s + 8 * g; });
 
-  if (stages > 0) load(0);
+  if (stages > 0) {
+    look_up(0);
+    load(0);
+  }
   if (tid < 2) stage[tid].odd = 0;
   __syncthreads();
   bool held[4] = {false, false, false, false};         // pages of the stage in LDS
@@ -976,66 +1077,87 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   }
   rw.settle();
   __syncthreads();
-  for (int n = 0; n < stages; ++n) {
-    if (n + 1 < stages) load(n + 1);
+  int n = 0;
+  auto pass = [&](auto edge) {
+    const bool more = !decltype(edge)::value || n + 1 < stages;
+    if (more) load(n + 1);
     Stage<DB>& st = stage[n & 1];
     if (busy) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t0 = range.begin + n * kAttnStage + 32 * half;
-        if (t0 >= range.end) break;
-        const bool* on = held + 2 * half;
-        const bool edge = t0 + 32 > min(range.see_all, it.len) || !on[0] || !on[1];
-        rw.tile(
-            p, t0, edge, on,
+        if (decltype(edge)::value && t0 >= range.end) break;
+        rw.template tile<decltype(edge)::value, true>(
+            p, t0, held + 2 * half,
             [&](int u, int i) -> u32x4 {
               const int r = 32 * half + 16 * u + c;
               return st.k[r * kPieces + ((4 * i + g) ^ (r & 7))];
             },
             [&](int u) { return *(const f32x4*)&st.k_scale[32 * half + 16 * u + 4 * g]; },
             []() {},
-            [&](uint32_t) -> bool { return __builtin_amdgcn_readfirstlane(st.odd) != 0; },
+            [&](uint32_t) -> bool {
+              if constexpr (FMT == W4A16_KV_INT8) return false;
+              return __builtin_amdgcn_readfirstlane(st.odd) != 0;
+            },
             [&](int u) { return *(const f32x4*)&st.v_scale[32 * half + 16 * u + 4 * g]; },
-            [&](int j, uint32_t zero) -> u32x4 {
-              const int line = j * 16 + c + (int)zero;
+            [&](int j) -> u32x4 {
+              const int line = j * 16 + c;
               return st.v[half * (DB * 4) + line * 4 + (g ^ ((line >> 1) & 3))];
-            });
+            },
+            []() { asm volatile("" ::: "memory"); });
       }
     }
-    if (n + 1 < stages) {
+    if (more) {
       // the other stage was last read before the previous barrier
       store(n + 1);
 #pragma unroll
       for (int u = 0; u < 4; ++u) held[u] = exists[u];
     }
     __syncthreads();
-  }
+    ++n;
+  };
+  // as in the narrow kernel: whole stages first, the rest in code of its own
+  const int whole = min(range.see_all, it.len);
+  while (n + 1 < stages && range.begin + (n + 1) * kAttnStage <= whole && held[0] && held[1] && held[2] && held[3])
+    pass(std::false_type{});
+  while (n < stages) pass(std::true_type{});
 
-  // ---- a wave's rows are its own: straight to the output, or to the part
+  // ---- a wave's rows are its own: through its part of the LDS (for whole rows
+  // at a time) to the output, or to the part
+  constexpr int kH = DB / 64, kPad = DB + 4, kPart = (int)attn_part_floats(kRows, DB);
+  static_assert(kAttnWaves * 16 * kPad * 4 <= 2 * (int)sizeof(Stage<DB>), "rows fit the stages' LDS");
+  const Parts parts(p, kPart);
+  float* mine = (float*)l_raw + wave * 16 * kPad;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float z = rw.denominator(r);
-    const int at = wave * kWaveRows + 16 * r + c;
-    if (at >= rows) continue;
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d0 = (4 * g + i) * kVD;
-      float o[kVD];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < kVD; j += 4) {
-        const f32x4 x = rw.sums(r, i, j);
+      for (int j = 0; j < kVD; j += 4)
+        *(f32x4*)(mine + c * kPad + (4 * g + i) * kVD + j) = rw.sums(r, i, j);
+    if (g == 0) *(f32x2*)(mine + c * kPad + DB) = f32x2{rw.top[r], z};
+    // LDS accesses of one wave take effect in order; this keeps the compiler to it
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j + e] = x[e];
+    for (int k = 0; k < 4; ++k) {
+      const int row = 4 * k + g, at = wave * kWaveRows + 16 * r + row;
+      if (at >= rows) continue;
+      const f32x2 st = *(const f32x2*)(mine + row * kPad + DB);
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+        const f32x4 o = *(const f32x4*)(mine + row * kPad + 64 * h + 4 * c);
+        if (it.splits == 1)
+          finish4<T>(p, it, row0 + at, 64 * h + 4 * c, dim, st.x, st.y, TY::kLift, o);
+        else
+          parts.put4((uint32_t)blockIdx.x * kPart + at * DB + 64 * h + 4 * c, o);
       }
-      if (it.splits == 1) {
-        finish<T, kVD>(p, it, row0 + at, d0, dim, rw.top[r], z, TY::kLift, o);
-      } else {
-        float* part = p.parts + blockIdx.x * attn_part_floats(kRows, DB);
-#pragma unroll
-        for (int j = 0; j < kVD; j += 2) put2(part + at * DB + d0 + j, o[j], o[j + 1]);
-        if (d0 == 0) put2(part + kRows * DB + 2 * at, rw.top[r], z);
-      }
+      if (it.splits > 1 && c == 0)
+        parts.put2((uint32_t)blockIdx.x * kPart + kRows * DB + 2 * at, st.x, st.y);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   if (it.splits > 1 && arrive(p, it, &stage[0].odd))
     join_parts<T, DB, kRows>(p, it, rows, dim, TY::kLift, (float*)l_raw);
@@ -1049,8 +1171,10 @@ hipError_t launch_attn(const AttnParams& p, hipStream_t stream) {
   void (*kernel)(AttnParams);
   if constexpr (WIDE)
     kernel = full ? attn_wide_kernel<T, FMT, DB, R, true> : attn_wide_kernel<T, FMT, DB, R, false>;
+  else if (p.max_q == 1 && p.mask == nullptr)
+    kernel = full ? attn_narrow_kernel<T, FMT, DB, R, true, false> : attn_narrow_kernel<T, FMT, DB, R, false, false>;
   else
-    kernel = full ? attn_narrow_kernel<T, FMT, DB, R, true> : attn_narrow_kernel<T, FMT, DB, R, false>;
+    kernel = full ? attn_narrow_kernel<T, FMT, DB, R, true, true> : attn_narrow_kernel<T, FMT, DB, R, false, true>;
   if (kLds > 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
