@@ -133,17 +133,11 @@ w4a16_status score_workspace(int64_t tokens, int64_t vocab, int32_t top_k, int n
   return W4A16_OK;
 }
 
-// Work items aimed at: two workgroups per CU. Ranges of a sequence are split
-// no finer than that, nor below kAttnStep tokens.
-#ifndef ITEMS_N
-#define ITEMS_N 3
-#define ITEMS_W 2
-#endif
-
-// Most groups (sequence, row block, head) of one row block of 16 for which
-// sequences are split: beyond, the groups alone fill the device many times,
-// and the parts would only cost memory.
+// Most groups (sequence, row block, head) for which sequences are split, and
+// the most scratch that the parts may take: beyond, the groups alone fill the
+// device many times over.
 constexpr int64_t kAttnMaxSplitGroups = 4096;
+constexpr int64_t kAttnMaxParts = 256ll << 20;
 static_assert(kAttnMaxSplitGroups <= kCounterBytes / 4, "one counter per group");
 
 struct AttnShape {
@@ -151,6 +145,24 @@ struct AttnShape {
   int rows, target;
   int64_t grid, workspace;
 };
+
+// Work items aimed at for `groups` on a device that holds `slots` workgroups.
+// Few groups: as many as there are slots. More: whole rounds of slots cost
+// whole rounds of time, so each group is split in the 1 to 4 that leaves the
+// last round fullest (a split costs about 2 % in parts written and joined).
+int64_t attn_target(int64_t groups, int64_t slots) {
+  if (groups <= slots) return slots;
+  int64_t best = 1;
+  double least = 1e30;
+  for (int64_t s = 1; s <= 4; ++s) {
+    const double time = (double)div_up(groups * s, slots) / (double)s * (1.0 + 0.02 * (double)(s - 1));
+    if (time < least) {
+      least = time;
+      best = s;
+    }
+  }
+  return groups * best;
+}
 
 w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                         int64_t dim, int num_cus, AttnShape* s) {
@@ -166,12 +178,14 @@ w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64
   s->kind = attn_kind(rows, (int)dim);
   s->rows = attn_rows(s->kind);
   const int64_t groups = sequences * div_up(rows, s->rows) * kv_heads;
-  s->target = groups <= kAttnMaxSplitGroups * 16 / s->rows ? (s->rows <= 32 ? ITEMS_N : ITEMS_W) * num_cus : 0;
+  const int64_t part = attn_part_floats(s->rows, attn_dim_block((int)dim)) * 4;
+  s->target = (int)attn_target(groups, 2 * (int64_t)num_cus);
+  if (groups > kAttnMaxSplitGroups || (groups + s->target) * part > kAttnMaxParts) s->target = 0;
   s->grid = groups + s->target;
   if (s->grid >= kMaxInt)
     return report(W4A16_ERR_SHAPE, "too many sequences, tokens and heads for one launch");
   s->workspace =
-      s->target > 0 ? kCounterBytes + s->grid * attn_part_floats(s->rows, attn_dim_block((int)dim)) * 4
+      s->target > 0 ? kCounterBytes + s->grid * part
                     : 0;
   return W4A16_OK;
 }

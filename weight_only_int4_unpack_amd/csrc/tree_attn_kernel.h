@@ -47,6 +47,16 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// The largest of eight; NaN where one is. (IEEE maximum: one instruction for
+// three values, where fmaxf first quiets each product by one of its own.)
+__device__ __forceinline__ float largest(f32x4 a, f32x4 b) {
+  auto max3 = [](float x, float y, float z) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(x, y), z);
+  };
+  const float x = max3(a[0], a[1], a[2]), y = max3(a[3], b[0], b[1]);
+  return __builtin_elementwise_maximum(max3(x, b[2], b[3]), y);
+}
+
 // Two fp32 as a 16-bit pair, rounded to nearest even.
 template <typename T>
 __device__ __forceinline__ uint32_t pair(float lo, float hi) {
@@ -225,7 +235,8 @@ __device__ __forceinline__ bool nan_codes(uint32_t y) {  // of e4m3: seven ones
 }
 
 // A wave's rows: R blocks of 16, lane (g, c) holding row c of each.
-template <typename T, int FMT, int DB, int R>
+// ROWS16: tile j of O^T holds dims 16 j.. (else dims j, j + kVD, ...).
+template <typename T, int FMT, int DB, int R, bool ROWS16>
 struct Rows {
   using TY = Types<T, FMT>;
   static constexpr int kSteps = DB / 32;  // contraction steps of S^T
@@ -377,15 +388,13 @@ struct Rows {
 #pragma unroll
           for (int i = 0; i < 4; ++i) vs[u][i] = (in_all >> (4 * u + i)) & 1 ? vs[u][i] : 0.0f;
         }
-        vhigh = fmaxf(fmaxf(vhigh, fmaxf(vs[u][0], vs[u][1])), fmaxf(vs[u][2], vs[u][3]));
       }
+      vhigh = largest(vs[0], vs[1]);
       rise = vhigh > vref;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float m = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3]));
-      m = fmaxf(m, fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      high[r] = m * unit;
+      high[r] = largest(s[r][0], s[r][1]) * unit;
       rise |= high[r] > top[r] + kSlack;
     }
     if (__any(rise)) {
@@ -496,11 +505,21 @@ struct Rows {
     float z = total[r] + __shfl_xor(total[r], 16);
     return z + __shfl_xor(z, 32);
   }
-  // Four of this lane's sums, V's reference put back: dims (4g + i) kVD + j..j+3 of row c.
-  __device__ __forceinline__ f32x4 sums(int r, int i, int j) const {
-    const f32x4 x = {acc[r][j][i], acc[r][j + 1][i], acc[r][j + 2][i], acc[r][j + 3][i]};
-    if constexpr (TY::kSame) return x;
-    return x * vref;
+  // Puts the sums of row c of block r into a row of DB floats, V's reference put back.
+  __device__ __forceinline__ void put_row(float* row, int r) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const float back = TY::kSame ? 1.0f : vref;
+    if constexpr (ROWS16) {
+#pragma unroll
+      for (int j = 0; j < kVD; ++j) *(f32x4*)(row + 16 * j + 4 * g) = acc[r][j] * back;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kVD; j += 4)
+          *(f32x4*)(row + (4 * g + i) * kVD + j) =
+              f32x4{acc[r][j][i], acc[r][j + 1][i], acc[r][j + 2][i], acc[r][j + 3][i]} * back;
+    }
   }
 };
 
@@ -768,7 +787,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? LBN : 2) 
     load_k();
     load_v();
   }
-  Rows<T, FMT, DB, R> rw;
+  Rows<T, FMT, DB, R, false> rw;
   rw.init(p, it, row0, dim, [&](int s) {
     return kSame ? 32 * s + 8 * g : 64 * (s / 2) + 16 * g + 8 * (s & 1);
   });
@@ -865,11 +884,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? LBN : 2) 
     const float sum = rw.denominator(r);
     if (r > 0) __syncthreads();
     if (g == 0) l_stat[wave][c] = f32x2{rw.top[r], sum};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < kVD; j += 4)
-        *(f32x4*)&l_sum[wave][c][(4 * g + i) * kVD + j] = rw.sums(r, i, j);
+    rw.put_row(l_sum[wave][c], r);
     __syncthreads();
     float m = kNegInf;
 #pragma unroll
@@ -905,34 +920,63 @@ __global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? LBN : 2) 
 }
 
 // ---------------------------------------------------------------- many rows
-// LDS of a stage: K rows as they are read (16-byte pieces of a row permuted by
-// the row's low 3 bits, so that 8 rows' same piece lies in 8 bank groups), and
-// V as operands: for each half stage of 32 tokens, each of DB dims has a 64-byte
-// row of four pieces (lane groups g), a piece being the 8 slots of lane (g, .);
-// pieces permuted by two bits of the dim's index for the same reason.
+// A stage: 64 tokens' K and V rows, 16 bits a value, DB values a row, in
+// 16-byte pieces permuted inside each row so that what is read at once spreads
+// over all 64 banks (256 bytes): an operand read takes one piece of 16 rows, a
+// transposing read two neighbouring pieces of 8 rows.
+template <int PIECES>
+__device__ __forceinline__ int k_place(int piece, int row) {
+  return piece ^ (PIECES >= 16 ? row & 15 : (row >> 1) & 7);
+}
+template <int PIECES>
+__device__ __forceinline__ int v_place(int piece, int row) {
+  return piece ^ (PIECES >= 16 ? (row & 7) << 1 : ((row >> 1) & 3) << 1);
+}
 template <int DB>
 struct Stage {
   u32x4 k[kAttnStage * DB / 8];
-  u32x4 v[2 * DB * 4];
+  u32x4 v[kAttnStage * DB / 8];
   float k_scale[kAttnStage], v_scale[kAttnStage];
-  int odd;                               // V holds an infinity or NaN
 };
+
+typedef __attribute__((address_space(3))) char* Lds;
+
+// 16 bytes per lane from base + the lane's offset straight into LDS, lane after
+// lane from `to` (uniform). The compiler does not count it: drain() before the
+// barrier after which the data are read.
+__device__ __forceinline__ void copy16(const void* base, uint32_t offset, Lds to) {
+  const uint32_t lds = (uint32_t)(uintptr_t)to;
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+               : "memory");
+}
+__device__ __forceinline__ void drain() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Four rows' values of a column: lane (g, c) of the wave gives the address of
+// row 4g + c / 4, columns 4 (c % 4).. of a 16-column tile, and gets column c of
+// rows 4g..4g + 3 (checked on the GPU).
+__device__ __forceinline__ u32x2 read_transposed(Lds at) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4* At;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)at));
+}
 
 template <typename T, int FMT, int DB, int R, bool FULL>
 __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_kernel(AttnParams p) {
   using TY = Types<T, FMT>;
-  using KT = typename TY::K;
-  using PT = typename TY::P;
   constexpr bool kSame = TY::kSame;
   constexpr int kWaveRows = 16 * R, kRows = kAttnWaves * kWaveRows;
   constexpr int kVD = DB / 16;
   constexpr int kBytes = kSame ? 2 : 1;
-  constexpr int kPieces = DB / 8;                      // 8-dim pieces of a K row
-  constexpr int kPass = 64 * kAttnWaves / kPieces;     // K rows that the workgroup loads at once
-  constexpr int kPasses = kAttnStage / kPass;
-  constexpr int kVWords = kVD * kBytes / 4;
+  constexpr int kPieces = DB / 8;              // 8-dim pieces of a row
+  constexpr int kPass = 64 / kPieces;          // rows that a wave brings at once
+  constexpr int kPasses = 16 / kPass;          // wave w brings tokens 16 w..16 w + 15
   extern __shared__ __align__(16) char l_raw[];
-  Stage<DB>* stage = (Stage<DB>*)l_raw;                // two of them
+  Stage<DB>* stage = (Stage<DB>*)l_raw;        // two of them
+  // byte addresses of a stage's K and V in LDS
+  auto k_at = [&](int n) { return (Lds)l_raw + (n & 1) * (int)sizeof(Stage<DB>); };
+  auto v_at = [&](int n) { return k_at(n) + kAttnStage * DB * 2; };
 
   Item it;
   if (!find_item<kRows>(p, blockIdx.x, &it)) return;
@@ -944,175 +988,141 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   const int rows = it.news * p.group - row0;
   const Range range = range_of(p, it, row0, kRows);
   const int stages = range.end > range.begin ? (range.end - range.begin + kAttnStage - 1) / kAttnStage : 0;
-  const bool busy = wave * kWaveRows < rows;           // this wave has rows
+  const bool busy = wave * kWaveRows < rows;   // this wave has rows
 
   const char* kbase = (const char*)p.cache.k;
   const char* vbase = (const char*)p.cache.v;
   const int row_bytes = dim * kBytes;
-  const int piece = tid % kPieces, krow = tid / kPieces;  // of K: row krow + pass * kPass
-  const int quad = tid >> 4, chunk = tid & 15;            // of V: tokens 4 quad.., dims chunk * kVD..
+  const int piece = lane % kPieces, sub = lane / kPieces;  // this lane's place in a pass
 
-  u32x4 kreg[kPasses];                                 // 8-bit: the low two words
-  uint32_t vreg[4][kVWords];
-  float sreg = 0.0f;                                   // a token's scale: K's, then V's threads
-  bool exists[4];                                      // of the stage in registers, by 16 tokens
-
-  int pages[4];                                        // of the stage to be loaded next
+  u32x2 kreg[kPasses], vreg[kPasses];          // 8-bit caches: on their way through registers
+  float sreg = 0.0f;                           // a token's scale: lanes 0..15 K's, 16..31 V's
+  bool exists[4];                              // of the stage on its way, by 16 tokens
+  int pages[4];                                // of the stage after that
   auto look_up = [&](int n) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) pages[u] = page_of(p, it, range.begin + n * kAttnStage + 16 * u);
   };
   auto load = [&](int n) {
     const int t0 = range.begin + n * kAttnStage;
-    int64_t at[4];
+    int64_t at = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) at[u] = row_of(p, it, pages[u], t0 + 16 * u, &exists[u]);
-    look_up(n + 1);                                    // scalar loads, back by the next stage
+    for (int u = 0; u < 4; ++u) {
+      const int64_t x = row_of(p, it, pages[u], t0 + 16 * u, &exists[u]);
+      at = wave == u ? x : at;
+    }
+    look_up(n + 1);                            // scalar loads, back by the next stage
+    const char* ksrc = kbase + at * row_bytes;
+    const char* vsrc = vbase + at * row_bytes;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      // rows of this wave in this pass: all in one group of 16 tokens
-      const int u = (i * kPass + wave * (kPass / kAttnWaves)) / 16;
-      const int64_t first = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
-      const char* src = kbase + first * row_bytes;     // uniform; lanes add 32-bit offsets
-      const int d = 8 * piece;
-      const bool in = FULL || d < dim;
-      const uint32_t off = ((krow + i * kPass) & 15) * row_bytes + (in ? d : 0) * kBytes;
+      const int r = i * kPass + sub;           // row of the 16
+      const int kp = k_place<kPieces>(piece, r), vp = v_place<kPieces>(piece, r);
+      const uint32_t koff = r * row_bytes + kp * 8 * kBytes, voff = r * row_bytes + vp * 8 * kBytes;
+      const bool kin = FULL || kp * 8 < dim, vin = FULL || vp * 8 < dim;
       if constexpr (kSame) {
-        const u32x4 x = load16(src + off);
-        kreg[i] = in ? x : u32x4{0, 0, 0, 0};
+        // lanes past the head's dims bring nothing: those pieces stay zeros
+        if (kin) copy16(ksrc, koff, k_at(n) + (16 * wave + i * kPass) * DB * 2);
+        if (vin) copy16(vsrc, voff, v_at(n) + (16 * wave + i * kPass) * DB * 2);
       } else {
-        const u32x2 x = load8(src + off);
-        kreg[i] = in ? u32x4{x.x, x.y, 0, 0} : u32x4{0, 0, 0, 0};
+        kreg[i] = load8(ksrc + (kin ? koff : 0));
+        vreg[i] = load8(vsrc + (vin ? voff : 0));
+        if (!kin) kreg[i] = u32x2{0, 0};
+        if (!vin) vreg[i] = u32x2{0, 0};
       }
     }
-    const int64_t first = wave == 0 ? at[0] : wave == 1 ? at[1] : wave == 2 ? at[2] : at[3];
-    const int d = FULL ? chunk * kVD : min(chunk * kVD, dim - kVD);
-    const char* src = vbase + first * row_bytes;
-    const uint32_t off = 4 * g * row_bytes + d * kBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int w = 0; w < kVWords; w += 4) {
-        if constexpr (kVWords >= 4) {
-          const u32x4 x = load16(src + (off + i * row_bytes + 4 * w));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) vreg[i][w + e] = x[e];
-        } else if constexpr (kVWords == 2) {
-          const u32x2 x = load8(src + (off + i * row_bytes));
-          vreg[i][0] = x.x;
-          vreg[i][1] = x.y;
-        } else {
-          vreg[i][0] = *(const uint32_t*)(src + (off + i * row_bytes));
-        }
-      }
-    // scales: wave u brings those of tokens 16 u..; lanes 0..15 K's, 16..31 V's
     if constexpr (!kSame)
-      if (lane < 32) sreg = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[first + c];
+      if (lane < 32) sreg = (lane < 16 ? p.cache.k_scale : p.cache.v_scale)[at + c];
   };
-  auto store = [&](int n) {
-    Stage<DB>& st = stage[n & 1];
+  auto store = [&](int n) {                    // 8-bit caches: widened into the stage
+    if constexpr (!kSame) {
+      Stage<DB>& st = stage[n & 1];
+      using KT = typename TY::K;
+      using PT = typename TY::P;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r = krow + i * kPass;
-      u32x4 x = kreg[i];
-      if constexpr (!kSame)
-        x = u32x4{widen_pair<KT, FMT, false>(kreg[i].x), widen_pair<KT, FMT, true>(kreg[i].x),
-                  widen_pair<KT, FMT, false>(kreg[i].y), widen_pair<KT, FMT, true>(kreg[i].y)};
-      st.k[r * kPieces + (piece ^ (r & 7))] = x;
-    }
-    // tokens that do not exist are zeros: a weight of 0 must not meet a NaN
-    const int t = range.begin + n * kAttnStage + 4 * quad;
-    const bool page = wave == 0 ? exists[0] : wave == 1 ? exists[1] : wave == 2 ? exists[2] : exists[3];
-    bool odd = false;
-    if (t + 4 > min(range.see_all, it.len) || !page) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int w = 0; w < kVWords; ++w) {
-          const uint32_t y = page && t + i < it.len ? vreg[i][w] : 0u;
-          vreg[i][w] = y;
-          if constexpr (kSame) odd |= odd_halves<T>(y) != 0;
-          if constexpr (FMT == W4A16_KV_E4M3) odd |= nan_codes(y);
-        }
-    }
-    // quad = 8 half + 4 u + lane group
-    uint32_t* base = (uint32_t*)(st.v + (quad >> 3) * (DB * 4));
-    const int u = (quad >> 2) & 1;
-#pragma unroll
-    for (int j = 0; j < kVD; ++j) {
-      const int line = j * 16 + chunk;
-      uint32_t x[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (kSame) {
-          x[h] = __builtin_amdgcn_perm(vreg[2 * h + 1][j / 2], vreg[2 * h][j / 2],
-                                       j & 1 ? 0x07060302u : 0x05040100u);
-        } else {
-          const uint32_t y = __builtin_amdgcn_perm(vreg[2 * h + 1][j / 4], vreg[2 * h][j / 4],
-                                                   j & 2 ? 0x07030602u : 0x05010400u);
-          x[h] = j & 1 ? widen_pair<PT, FMT, true>(y) : widen_pair<PT, FMT, false>(y);
-        }
+      for (int i = 0; i < kPasses; ++i) {
+        const int x = (16 * wave + i * kPass) * kPieces + lane;
+        st.k[x] = u32x4{widen_pair<KT, FMT, false>(kreg[i].x), widen_pair<KT, FMT, true>(kreg[i].x),
+                        widen_pair<KT, FMT, false>(kreg[i].y), widen_pair<KT, FMT, true>(kreg[i].y)};
+        st.v[x] = u32x4{widen_pair<PT, FMT, false>(vreg[i].x), widen_pair<PT, FMT, true>(vreg[i].x),
+                        widen_pair<PT, FMT, false>(vreg[i].y), widen_pair<PT, FMT, true>(vreg[i].y)};
       }
-      *(u32x2*)(base + line * 16 + ((g ^ ((line >> 1) & 3)) * 4) + u * 2) = u32x2{x[0], x[1]};
-    }
-    if constexpr (!kSame)
       if (lane < 32) (lane < 16 ? st.k_scale : st.v_scale)[16 * wave + c] = sreg;
-    if (odd) st.odd = 1;
+    }
   };
 
-  Rows<T, FMT, DB, R> rw;
-  rw.init(p, it, row0 + wave * kWaveRows, dim, [&](int s) { return 32 * s + 8 * g; });
-
+  if constexpr (kSame && !FULL) {              // pieces that no load will reach
+    for (int i = tid; i < 2 * kAttnStage * kPieces; i += 64 * kAttnWaves) {
+      stage[i & 1].k[i >> 1] = u32x4{0, 0, 0, 0};
+      stage[i & 1].v[i >> 1] = u32x4{0, 0, 0, 0};
+    }
+    __syncthreads();
+  }
   if (stages > 0) {
     look_up(0);
     load(0);
   }
-  if (tid < 2) stage[tid].odd = 0;
-  __syncthreads();
-  bool held[4] = {false, false, false, false};         // pages of the stage in LDS
+  Rows<T, FMT, DB, R, true> rw;
+  rw.init(p, it, row0 + wave * kWaveRows, dim, [&](int s) { return 32 * s + 8 * g; });
+  rw.settle();
+  bool held[4] = {false, false, false, false};  // pages of the stage in LDS
   if (stages > 0) {
     store(0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) held[u] = exists[u];
   }
-  rw.settle();
+  drain();
   __syncthreads();
   int n = 0;
   auto pass = [&](auto edge) {
     const bool more = !decltype(edge)::value || n + 1 < stages;
-    if (more) load(n + 1);
+    if (more) load(n + 1);                     // the other stage was last read before the barrier
     Stage<DB>& st = stage[n & 1];
     if (busy) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t0 = range.begin + n * kAttnStage + 32 * half;
         if (decltype(edge)::value && t0 >= range.end) break;
+        u32x4 clear = {~0u, ~0u, ~0u, ~0u};    // V of tokens that do not exist
+        auto v_raw = [&](int j) -> u32x4 {
+          const Lds at = v_at(n) + (32 * half + 4 * g + (c >> 2)) * DB * 2 +
+                         v_place<kPieces>(2 * j + ((c >> 1) & 1), 4 * g + (c >> 2)) * 16 + (c & 1) * 8;
+          const u32x2 x = read_transposed(at), y = read_transposed(at + 16 * DB * 2);
+          return u32x4{x.x, x.y, y.x, y.y};
+        };
         rw.template tile<decltype(edge)::value, true>(
             p, t0, held + 2 * half,
             [&](int u, int i) -> u32x4 {
-              const int r = 32 * half + 16 * u + c;
-              return st.k[r * kPieces + ((4 * i + g) ^ (r & 7))];
+              return st.k[(32 * half + 16 * u + c) * kPieces + k_place<kPieces>(4 * i + g, c)];
             },
             [&](int u) { return *(const f32x4*)&st.k_scale[32 * half + 16 * u + 4 * g]; },
             []() {},
-            [&](uint32_t) -> bool {
-              if constexpr (FMT == W4A16_KV_INT8) return false;
-              return __builtin_amdgcn_readfirstlane(st.odd) != 0;
+            [&](uint32_t in) -> bool {
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                clear[e] = ((in >> (2 * e)) & 1 ? 0xFFFFu : 0u) | ((in >> (2 * e + 1)) & 1 ? 0xFFFF0000u : 0u);
+              if constexpr (FMT != W4A16_KV_INT8) {
+#pragma unroll 1
+                for (int j = 0; j < kVD; ++j) {
+                  const u32x4 a = v_raw(j) & clear;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) odd |= odd_halves<typename TY::P>(a[e]) != 0;
+                }
+              }
+              return FMT != W4A16_KV_INT8 && __any(odd);
             },
             [&](int u) { return *(const f32x4*)&st.v_scale[32 * half + 16 * u + 4 * g]; },
-            [&](int j) -> u32x4 {
-              const int line = j * 16 + c;
-              return st.v[half * (DB * 4) + line * 4 + (g ^ ((line >> 1) & 3))];
-            },
+            [&](int j) -> u32x4 { return decltype(edge)::value ? v_raw(j) & clear : v_raw(j); },
             []() { asm volatile("" ::: "memory"); });
       }
     }
     if (more) {
-      // the other stage was last read before the previous barrier
       store(n + 1);
 #pragma unroll
       for (int u = 0; u < 4; ++u) held[u] = exists[u];
     }
+    drain();
     __syncthreads();
     ++n;
   };
@@ -1132,11 +1142,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   for (int r = 0; r < R; ++r) {
     const float z = rw.denominator(r);
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < kVD; j += 4)
-        *(f32x4*)(mine + c * kPad + (4 * g + i) * kVD + j) = rw.sums(r, i, j);
+    rw.put_row(mine + c * kPad, r);
     if (g == 0) *(f32x2*)(mine + c * kPad + DB) = f32x2{rw.top[r], z};
     // LDS accesses of one wave take effect in order; this keeps the compiler to it
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -1159,7 +1165,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  if (it.splits > 1 && arrive(p, it, &stage[0].odd))
+  if (it.splits > 1 && arrive(p, it, (int*)stage[0].k_scale))
     join_parts<T, DB, kRows>(p, it, rows, dim, TY::kLift, (float*)l_raw);
 }
 
