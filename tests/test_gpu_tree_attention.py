@@ -292,6 +292,19 @@ def test_views_scales_and_streams():
     assert torch.equal(other[0], c.run()[0])
 
 
+@pytest.mark.parametrize("fmt", ["16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 9, 40])
+def test_a_scale_of_zero_and_negative_ones(new, fmt):
+    for scale in (0.0, -0.0, -0.4):
+        say("scale", scale, new, fmt)
+        c = Case([70, 41], [new, new], 8, 2, 64, fmt, torch.bfloat16, 16, seed=21)
+        c.scale = scale
+        c.check(*c.run())
+        if new > 1:
+            trees = random_trees([new, new], 4)
+            c.check(*c.run(mask=attn.tree_mask(trees)), rows=[ancestors(t) for t in trees])
+
+
 def test_captured_launch_follows_the_lengths():
     c = Case([900, 333], [3, 3], 8, 2, 64, "int8", torch.float16, 16, seed=12)
     mask = attn.tree_mask([[-1, 0, 0]] * 2)

@@ -328,9 +328,8 @@ struct Rows {
                                        KOp k_op, KScale k_scale, After after, VEdge v_edge,
                                        VScale v_scale, VOp v_op, Fresh fresh) {
     const int g = (threadIdx.x & 63) >> 4;
-    // ---- S^T: in units of log2, or (16-bit caches) raw, `unit` to be multiplied
+    // ---- S^T, times the tokens' scales; factor[r] makes it units of log2
     f32x4 s[R][2];
-    const float unit = TY::kSame ? factor[0] : 1.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -343,7 +342,7 @@ struct Rows {
       }
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if constexpr (!TY::kSame) s[r][u] *= k_scale(u) * factor[r];
+        if constexpr (!TY::kSame) s[r][u] *= k_scale(u);
     }
     after();
 
@@ -375,26 +374,22 @@ struct Rows {
     }
 
     // ---- the held maximum rises only when a score exceeds it by 2^8
-    f32x4 vs[2];
-    bool rise = false;
-    float vhigh = 0.0f, high[R];
-    if constexpr (!TY::kSame) {
+    // scales of tokens that do not exist must not matter (NaN and infinite ones of
+    // those that do set no reference)
+    auto v_of = [&](int u) {
+      f32x4 x = v_scale(u);
+      if constexpr (EDGE) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        vs[u] = v_scale(u);
-        // scales of tokens that do not exist must not matter (NaN and infinite
-        // ones of those that do set no reference: see below)
-        if constexpr (EDGE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vs[u][i] = (in_all >> (4 * u + i)) & 1 ? vs[u][i] : 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) x[i] = (in_all >> (4 * u + i)) & 1 ? x[i] : 0.0f;
       }
-      vhigh = largest(vs[0], vs[1]);
-      rise = vhigh > vref;
-    }
+      return x;
+    };
+    bool rise = false;
+    float high[R];
+    if constexpr (!TY::kSame) rise = largest(v_of(0), v_of(1)) > vref;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      high[r] = largest(s[r][0], s[r][1]) * unit;
+      high[r] = largest(s[r][0], s[r][1]) * factor[r];
       rise |= high[r] > top[r] + kSlack;
     }
     if (__any(rise)) {
@@ -405,8 +400,10 @@ struct Rows {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            most = vs[u][i] < __builtin_inff() ? fmaxf(most, vs[u][i]) : most;
+          for (int i = 0; i < 4; ++i) {
+            const float x = v_of(u)[i];
+            most = x < __builtin_inff() ? fmaxf(most, x) : most;
+          }
         most = fmaxf(most, __shfl_xor(most, 16));
         most = fmaxf(most, __shfl_xor(most, 32));
         const float above =
@@ -429,10 +426,11 @@ struct Rows {
     }
 
     // ---- weights
+    const float inv = vref > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.0f;
+    f32x4 vs[2];
     if constexpr (!TY::kSame) {
-      const float inv = vref > 0.0f ? __uint_as_float(0x7F000000u - __float_as_uint(vref)) : 0.0f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) vs[u] *= inv;
+      for (int u = 0; u < 2; ++u) vs[u] = v_of(u) * inv;
     }
     u32x4 w[R];
 #pragma unroll
@@ -443,13 +441,12 @@ struct Rows {
         float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(TY::kSame ? fmaf(s[r][u][i], unit, -ref) : s[r][u][i] - ref);
+          // 0 where unseen, whatever -inf times a factor of 0 and NaN scales make of it
+          const bool in = !EDGE || ((seen[r] >> (4 * u + i)) & 1);
+          x[i] = __builtin_amdgcn_exp2f(fmaf(s[r][u][i], factor[r], -ref));
+          x[i] = in ? x[i] : 0.0f;
           total[r] += x[i];
-          if constexpr (!TY::kSame) x[i] *= vs[u][i];
-        }
-        if constexpr (EDGE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = (seen[r] >> (4 * u + i)) & 1 ? x[i] : 0.0f;
+          if constexpr (!TY::kSame) x[i] = in ? x[i] * vs[u][i] : 0.0f;
         }
         w[r][2 * u] = pair<typename TY::P>(x[0], x[1]);
         w[r][2 * u + 1] = pair<typename TY::P>(x[2], x[3]);
