@@ -6,6 +6,8 @@
 // lanes, 8 dims (16 bytes) per lane, so that its row is one contiguous run of
 // vector accesses, its partner dims are a second (cached) load, and its
 // largest magnitude is found by shuffles inside the group.
+#include <type_traits>
+
 #include "serve_device.h"
 
 namespace w4a16 {
@@ -29,46 +31,73 @@ __global__ __launch_bounds__(256) void rope_table_kernel(RopeTableParams p) {
   }
 }
 
-// Factors of a lane's 8 dims d0..d0+7: y[e] = own[e] x[e] + other[e] x[partner].
-struct Turn {
-  float own[8], other[8];
+// How a lane's 8 dims meet their partners.
+enum Pairing {
+  kPlain,       // nothing is rotated
+  kHalves,      // dims i and i + r/2, r/2 a multiple of 8: one aligned vector each
+  kNeighbours,  // dims 2i and 2i + 1, r a multiple of 8: inside the lane
+  kAny          // either, for other r: element by element
 };
 
-template <typename T, int FMT, int LPH>
+// Largest of the LPH lanes of a group, in all of them.
+template <int LPH>
+__device__ __forceinline__ uint32_t group_max(uint32_t x) {
+  auto dpp = [&](auto ctrl) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  dpp(std::integral_constant<int, 0xB1>{});    // lanes 1 0 3 2
+  dpp(std::integral_constant<int, 0x4E>{});    // lanes 2 3 0 1
+  dpp(std::integral_constant<int, 0x141>{});   // mirrored in 8
+  if constexpr (LPH >= 16) dpp(std::integral_constant<int, 0x140>{});  // mirrored in 16
+  if constexpr (LPH >= 32) x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+  return x;
+}
+
+constexpr int kBatch = 4;  // heads whose loads a lane has in flight
+
+// One lane group takes `per_unit` heads of a token in turn, so that the token's
+// row of the table and its slot are read once for several heads. Before this,
+// with one head a group, address arithmetic and table reads bound the kernel
+// (16384 tokens x 48 heads, e4m3: 149 us; with 8 heads 101 us).
+template <typename T, int FMT, int LPH, Pairing PAIR>
 __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
   const int lane = threadIdx.x % LPH;
   const int unit = blockIdx.x * (256 / LPH) + threadIdx.x / LPH;
   if (unit >= p.tokens * p.units_per_token) return;  // whole lane groups leave
   const int token = unit / p.units_per_token;
   const int first = (unit - token * p.units_per_token) * p.per_unit;
-  const int heads = p.hq + 2 * p.hkv;
-  const int last = min(first + p.per_unit, heads);
+  const int last = min(first + p.per_unit, p.hq + 2 * p.hkv);
   const int d0 = 8 * lane;
   const bool live = d0 < p.dim;
   const int half = p.rot / 2;
-  // Whole vectors: a lane's 8 dims are rotated all or none, and their
-  // partners are one aligned vector (halves) or the lane's own (neighbours).
-  const bool vec = p.interleaved ? p.rot % 8 == 0 : half % 8 == 0;
-  const bool turns = p.table != nullptr && live && d0 < p.rot;
+  const bool turns = PAIR != kPlain && live && d0 < p.rot;
 
-  Turn w;
+  // y[e] = own[e] x[e] + other[e] x[partner]; a position outside the table: NaN
+  float own[8], other[8];
   if (turns) {
     const int64_t pos = p.positions[token];
     const bool known = pos >= 0 && pos < p.table_rows;
     const float* row = p.table + (known ? pos : 0) * p.rot;
-    const float nan = __builtin_nanf("");
-    if (vec && !p.interleaved) {
+    const float bad = known ? 0.0f : __builtin_nanf("");
+    const float flip = p.inverse ? -1.0f : 1.0f;
+    if constexpr (PAIR == kHalves) {
       const int i0 = d0 < half ? d0 : d0 - half;
-      const float sign = (d0 < half) != (p.inverse != 0) ? -1.0f : 1.0f;
+      const float sign = d0 < half ? -flip : flip;
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
-        const f32x4 c = *(const f32x4*)(row + i0 + e);
-        const f32x4 s = *(const f32x4*)(row + half + i0 + e);
+        const f32x4 c = *(const f32x4*)(row + i0 + e), s = *(const f32x4*)(row + half + i0 + e);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          w.own[e + j] = known ? c[j] : nan;
-          w.other[e + j] = known ? sign * s[j] : nan;
+          own[e + j] = c[j] + bad;
+          other[e + j] = sign * s[j];
         }
+      }
+    } else if constexpr (PAIR == kNeighbours) {
+      const f32x4 c = *(const f32x4*)(row + d0 / 2), s = *(const f32x4*)(row + half + d0 / 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        own[e] = c[e / 2] + bad;
+        other[e] = (e & 1 ? flip : -flip) * s[e / 2];
       }
     } else {
 #pragma unroll
@@ -76,99 +105,132 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
         const int d = min(d0 + e, p.rot - 1);
         const int i = p.interleaved ? d / 2 : d < half ? d : d - half;
         const bool low = p.interleaved ? (d & 1) == 0 : d < half;
-        const float c = row[i], s = row[half + i];
-        w.own[e] = known ? c : nan;
-        w.other[e] = known ? (low != (p.inverse != 0) ? -s : s) : nan;
+        own[e] = row[i] + bad;
+        other[e] = (low ? -flip : flip) * row[half + i];
       }
     }
   }
-
-  int64_t slot = 0;
-  bool kept = false;
-  if (p.hkv > 0) {
-    slot = p.slots[token];
-    kept = slot >= 0 && slot < (p.cache.pages << p.cache.page_shift);
-  }
-
-  for (int h = first; h < last; ++h) {
-    const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
-    const int hk = is_q ? 0 : is_v ? h - p.hq - p.hkv : h - p.hq;
-    const uint16_t* src = is_q   ? p.q + token * p.q_token + h * p.q_head
-                          : is_v ? p.v + token * p.v_token + hk * p.v_head
-                                 : p.k + token * p.k_token + hk * p.k_head;
-    u32x4 raw = {0, 0, 0, 0};
-    if (live) raw = load16(src + d0);
-    const bool turned = turns && !is_v;
-    // The partner's load comes before any store of this wave, and every
-    // partner of a head is in the same wave: q_out may be q itself.
-    f32x8 x = widen8<T>(raw);
-    if (turned) {
-      f32x8 y = x;
-      if (p.interleaved) {
-        y = __builtin_shufflevector(x, x, 1, 0, 3, 2, 5, 4, 7, 6);
-      } else if (vec) {
-        y = widen8<T>(load16(src + (d0 < half ? d0 + half : d0 - half)));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
+  // Loads of a head: its own vector, and with halves its partner's. All of a
+  // head's lanes are in one wave, and its loads come before its stores in every
+  // lane: the output may be the input.
+  struct Raw {
+    u32x4 own, other;
+  };
+  auto load = [&](const uint16_t* src) -> Raw {
+    Raw r = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+    if (live) r.own = load16(src + d0);
+    if constexpr (PAIR == kHalves)
+      if (turns) r.other = load16(src + (d0 < half ? d0 + half : d0 - half));
+    if constexpr (PAIR == kAny)
+      if (turns) {
+        // elements past the rotated ones are their own partners, unused
+        auto at = [&](int e) -> uint32_t {
           const int d = d0 + e;
-          if (d < p.rot) y[e] = widen1<T>(src[d < half ? d + half : d - half]);
-        }
+          if (d >= p.rot) return 0;
+          return src[p.interleaved ? d ^ 1 : d < half ? d + half : d - half];
+        };
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) r.other[e / 2] = at(e) | at(e + 1) << 16;
       }
+    return r;
+  };
+  auto turn = [&](const Raw& r) -> f32x8 {
+    const f32x8 x = widen8<T>(r.own);
+    if constexpr (PAIR == kPlain) return x;
+    const f32x8 y = PAIR == kNeighbours ? __builtin_shufflevector(x, x, 1, 0, 3, 2, 5, 4, 7, 6)
+                                        : widen8<T>(r.other);
+    f32x8 z = x;
+    if (turns) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float r = fmaf(w.own[e], x[e], w.other[e] * y[e]);
-        x[e] = (vec || d0 + e < p.rot) ? r : x[e];
+        const float v = fmaf(own[e], x[e], other[e] * y[e]);
+        z[e] = PAIR != kAny || d0 + e < p.rot ? v : x[e];
       }
     }
-    if (is_q) {
-      if (live)
-        *(u32x4*)(p.q_out + token * p.out_token + h * p.out_head + d0) =
-            turned ? narrow8<T>(x) : raw;
-      continue;
+    return z;
+  };
+  // Heads [a, b) of a kind, kBatch at a time.
+  auto each = [&](int a, int b, const uint16_t* src, int64_t stride, auto use) {
+    for (int h = a; h < b; h += kBatch) {
+      Raw r[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (h + i < b) r[i] = load(src + (h + i) * stride);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (h + i < b) use(h + i, r[i]);
     }
-    // Row of this head's token inside its page.
-    const int64_t page = slot >> p.cache.page_shift;
-    const int64_t offset = slot & ((1 << p.cache.page_shift) - 1);
-    const int64_t at = ((page * p.cache.heads + hk) << p.cache.page_shift) + offset;
-    void* base = is_v ? p.cache.v : p.cache.k;
+  };
+
+  each(first, min(last, p.hq), p.q + token * p.q_token, p.q_head, [&](int h, const Raw& r) {
+    const u32x4 y = turns ? narrow8<T>(turn(r)) : r.own;
+    if (live) *(u32x4*)(p.q_out + token * p.out_token + h * p.out_head + d0) = y;
+  });
+  if (last <= p.hq) return;
+
+  const int64_t slot = p.slots[token];
+  const bool kept = slot >= 0 && slot < (p.cache.pages << p.cache.page_shift);
+  const int64_t page = slot >> p.cache.page_shift;
+  // row of head 0's token inside its page; the next head's is a page's tokens on
+  const int64_t at0 = ((page * p.cache.heads) << p.cache.page_shift) +
+                      (slot & ((1 << p.cache.page_shift) - 1));
+  auto write = [&](int h, const u32x4& raw, const f32x8& x, bool as_is, void* base, float* scales) {
+    const int64_t at = at0 + ((int64_t)h << p.cache.page_shift);
     if constexpr (FMT == W4A16_KV_SAME) {
-      if (live && kept)
-        *(u32x4*)((uint16_t*)base + at * p.dim + d0) = turned ? narrow8<T>(x) : raw;
+      const u32x4 y = as_is ? raw : narrow8<T>(x);
+      if (live && kept) *(u32x4*)((uint16_t*)base + at * p.dim + d0) = y;
     } else {
       // Magnitudes compare like integers, infinities and NaN above all.
       uint32_t big = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        big = max(big, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int s = 1; s < LPH; s *= 2) big = max(big, (uint32_t)__shfl_xor((int)big, s, LPH));
+      for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+      big = group_max<LPH>(big);
       constexpr float kTop = FMT == W4A16_KV_E4M3 ? 448.0f : 127.0f;
-      const float amax = __builtin_bit_cast(float, big);
+      const float amax = __uint_as_float(big);
       const bool finite = big < 0x7F800000u;
       const bool some = finite && amax >= 0x1p-100f;
-      const float inv = some ? kTop / amax : 0.0f;
+      const float inv = kTop / amax;
       const float scale = finite ? (some ? amax / kTop : 0.0f) : __builtin_nanf("");
       uint32_t code[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
         float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          y[j] = some ? fminf(fmaxf(x[e + j] * inv, -kTop), kTop) : 0.0f;
+        for (int j = 0; j < 4; ++j) y[j] = __builtin_amdgcn_fmed3f(x[e + j] * inv, -kTop, kTop);
         if constexpr (FMT == W4A16_KV_E4M3) {
           int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
           code[e / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
         } else {
+          // 1.5 x 2^23 in front: the low byte of the sum is the rounded integer
+          uint32_t c[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            code[e / 4] |= ((uint32_t)(int)__builtin_rintf(y[j]) & 0xFFu) << (8 * j);
+          for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(y[j] + 12582912.0f);
+          code[e / 4] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0C0C0400u),
+                                              __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u),
+                                              0x05040100u);
         }
+        code[e / 4] = some ? code[e / 4] : 0u;
       }
-      if (live && kept)
-        *(u32x2*)((uint8_t*)base + at * p.dim + d0) = u32x2{code[0], code[1]};
-      if (lane == 0 && kept) (is_v ? p.cache.v_scale : p.cache.k_scale)[at] = scale;
+      if (live && kept) *(u32x2*)((uint8_t*)base + at * p.dim + d0) = u32x2{code[0], code[1]};
+      if (lane == 0 && kept) scales[at] = scale;
     }
+  };
+  const int k0 = max(first - p.hq, 0), k1 = min(last - p.hq, p.hkv);
+  each(k0, k1, p.k + token * p.k_token, p.k_head, [&](int h, const Raw& r) {
+    write(h, r.own, turn(r), !turns, p.cache.k, p.cache.k_scale);
+  });
+  const int v0 = max(first - p.hq - p.hkv, 0), v1 = last - p.hq - p.hkv;
+  const uint16_t* v = p.v + token * p.v_token;
+  for (int h = v0; h < v1; h += kBatch) {
+    u32x4 r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      r[i] = u32x4{0, 0, 0, 0};
+      if (h + i < v1 && live) r[i] = load16(v + (h + i) * p.v_head + d0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i < v1) write(h + i, r[i], widen8<T>(r[i]), true, p.cache.v, p.cache.v_scale);
   }
 }
 
@@ -185,25 +247,51 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
   const int64_t slot = p.slots[token];
   const bool kept = slot >= 0 && slot < (p.cache.pages << p.cache.page_shift);
   const int64_t page = slot >> p.cache.page_shift;
-  const int64_t offset = slot & ((1 << p.cache.page_shift) - 1);
-  for (int h = first; h < last; ++h) {
-    const bool is_v = h >= p.cache.heads;
-    const int hk = is_v ? h - p.cache.heads : h;
-    const int64_t at = ((page * p.cache.heads + hk) << p.cache.page_shift) + offset;
-    const void* base = is_v ? p.cache.v : p.cache.k;
-    u32x4 y = {0, 0, 0, 0};
-    if (kept) {
-      if constexpr (FMT == W4A16_KV_SAME) {
-        y = load16((const uint16_t*)base + at * p.cache.dim + d0);
-      } else {
-        const u32x2 c = load8((const uint8_t*)base + at * p.cache.dim + d0);
-        const float s = (is_v ? p.cache.v_scale : p.cache.k_scale)[at];
-        const f32x4 lo = decode4<FMT>(c.x) * s, hi = decode4<FMT>(c.y) * s;
-        y = narrow8<T>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  const int64_t at0 = ((page * p.cache.heads) << p.cache.page_shift) +
+                      (slot & ((1 << p.cache.page_shift) - 1));
+  for (int h = first; h < last; h += kBatch) {
+    u32x4 raw[kBatch];
+    float scale[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      raw[i] = u32x4{0, 0, 0, 0};
+      scale[i] = 0.0f;
+      if (h + i < last && kept) {
+        const bool is_v = h + i >= p.cache.heads;
+        const int64_t at = at0 + ((int64_t)(h + i - (is_v ? p.cache.heads : 0)) << p.cache.page_shift);
+        const void* base = is_v ? p.cache.v : p.cache.k;
+        if constexpr (FMT == W4A16_KV_SAME) {
+          raw[i] = load16((const uint16_t*)base + at * p.cache.dim + d0);
+        } else {
+          const u32x2 c = load8((const uint8_t*)base + at * p.cache.dim + d0);
+          raw[i] = u32x4{c.x, c.y, 0, 0};
+          scale[i] = (is_v ? p.cache.v_scale : p.cache.k_scale)[at];
+        }
       }
     }
-    *(u32x4*)((is_v ? p.v_out : p.k_out) +
-              ((int64_t)token * p.cache.heads + hk) * p.cache.dim + d0) = y;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (h + i < last) {
+        u32x4 y = raw[i];
+        if constexpr (FMT != W4A16_KV_SAME) {
+          const f32x4 lo = decode4<FMT>(raw[i].x) * scale[i], hi = decode4<FMT>(raw[i].y) * scale[i];
+          y = kept ? narrow8<T>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)) : y;
+        }
+        const bool is_v = h + i >= p.cache.heads;
+        const int hk = h + i - (is_v ? p.cache.heads : 0);
+        *(u32x4*)((is_v ? p.v_out : p.k_out) +
+                  ((int64_t)token * p.cache.heads + hk) * p.cache.dim + d0) = y;
+      }
+  }
+}
+
+template <typename T, int FMT, int LPH>
+void (*rope_kv_of(Pairing pair))(RopeKvParams) {
+  switch (pair) {
+    case kPlain: return rope_kv_kernel<T, FMT, LPH, kPlain>;
+    case kHalves: return rope_kv_kernel<T, FMT, LPH, kHalves>;
+    case kNeighbours: return rope_kv_kernel<T, FMT, LPH, kNeighbours>;
+    default: return rope_kv_kernel<T, FMT, LPH, kAny>;
   }
 }
 
@@ -212,12 +300,14 @@ hipError_t rope_kv_lanes(const RopeKvParams& p, hipStream_t stream) {
   const int lph = lanes_per_head(p.dim);
   const int64_t units = (int64_t)p.tokens * p.units_per_token;
   const dim3 grid((uint32_t)((units + 256 / lph - 1) / (256 / lph)));
-  if (lph == 8)
-    hipLaunchKernelGGL((rope_kv_kernel<T, FMT, 8>), grid, dim3(256), 0, stream, p);
-  else if (lph == 16)
-    hipLaunchKernelGGL((rope_kv_kernel<T, FMT, 16>), grid, dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL((rope_kv_kernel<T, FMT, 32>), grid, dim3(256), 0, stream, p);
+  const Pairing pair = p.table == nullptr                      ? kPlain
+                       : p.interleaved && p.rot % 8 == 0       ? kNeighbours
+                       : !p.interleaved && p.rot % 16 == 0     ? kHalves
+                                                               : kAny;
+  const auto kernel = lph == 8    ? rope_kv_of<T, FMT, 8>(pair)
+                      : lph == 16 ? rope_kv_of<T, FMT, 16>(pair)
+                                  : rope_kv_of<T, FMT, 32>(pair);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -226,12 +316,10 @@ hipError_t kv_read_lanes(const KvReadParams& p, hipStream_t stream) {
   const int lph = lanes_per_head(p.cache.dim);
   const int64_t units = (int64_t)p.tokens * p.units_per_token;
   const dim3 grid((uint32_t)((units + 256 / lph - 1) / (256 / lph)));
-  if (lph == 8)
-    hipLaunchKernelGGL((kv_read_kernel<T, FMT, 8>), grid, dim3(256), 0, stream, p);
-  else if (lph == 16)
-    hipLaunchKernelGGL((kv_read_kernel<T, FMT, 16>), grid, dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL((kv_read_kernel<T, FMT, 32>), grid, dim3(256), 0, stream, p);
+  const auto kernel = lph == 8    ? kv_read_kernel<T, FMT, 8>
+                      : lph == 16 ? kv_read_kernel<T, FMT, 16>
+                                  : kv_read_kernel<T, FMT, 32>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -92,11 +92,12 @@ w4a16_status check_rotation(const int64_t* positions, const float* table, int64_
   return W4A16_OK;
 }
 
-// Heads that one lane group takes in turn.
+// Heads that one lane group takes in turn: as many, up to 8, as leave 4096 waves
+// (16 a CU), so that few tokens are spread out and many read their row of the
+// table and their slot once for several heads.
 void shape_units(int64_t tokens, int64_t heads, int dim, int32_t* per_unit, int32_t* units) {
-  (void)tokens;
-  (void)dim;
-  *per_unit = 1;
+  const int64_t waves = tokens * heads * lanes_per_head(dim) / 64;
+  *per_unit = (int32_t)std::min<int64_t>({std::max<int64_t>(waves / 4096, 1), 8, heads});
   *units = (int32_t)div_up(heads, *per_unit);
 }
 
@@ -142,7 +143,7 @@ static_assert(kAttnMaxSplitGroups <= kCounterBytes / 4, "one counter per group")
 
 struct AttnShape {
   AttnKind kind;
-  int rows, target;
+  int rows, target, few;
   int64_t grid, workspace;
 };
 
@@ -179,7 +180,11 @@ w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64
   s->rows = attn_rows(s->kind);
   const int64_t groups = sequences * div_up(rows, s->rows) * kv_heads;
   const int64_t part = attn_part_floats(s->rows, attn_dim_block((int)dim)) * 4;
-  s->target = (int)attn_target(groups, 2 * (int64_t)num_cus);
+  // narrow items: 4 a CU (3 are resident; batches of mixed lengths end evener:
+  // 32 x up to 8192 tokens 119.8 us, with 2 or 3 a CU 125); wide ones: 2, all resident
+  const bool narrow = s->rows <= 32;
+  s->target = (int)attn_target(groups, (narrow ? 4 : 2) * (int64_t)num_cus);
+  s->few = narrow ? num_cus : s->target;
   if (groups > kAttnMaxSplitGroups || (groups + s->target) * part > kAttnMaxParts) s->target = 0;
   s->grid = groups + s->target;
   if (s->grid >= kMaxInt)
@@ -468,6 +473,7 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
   p.group = a->q_heads / view.heads;
   p.mask_words = a->mask_words;
   p.target = s.target;
+  p.few = s.few;
   p.grid = (int32_t)s.grid;
   p.scale_log2 = a->scale * 1.44269504088896340736f;
   using Launch = hipError_t (*)(const AttnParams&, AttnKind, hipStream_t);

@@ -131,8 +131,11 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   for (int s = 1; s < 64; s *= 2) steps += (uint32_t)__shfl_xor((int)steps, s);
   steps = (uint32_t)__builtin_amdgcn_readfirstlane((int)steps);
   uint32_t per = 0x7FFFFFFF / kAttnStep;   // steps of a split
-  if (p.target > 0)
-    per = max((steps * (uint32_t)p.cache.heads + p.target - 1) / (uint32_t)p.target, 1u);
+  if (p.target > 0) {
+    const uint32_t work = steps * (uint32_t)p.cache.heads;
+    per = (work + p.target - 1) / (uint32_t)p.target;
+    per = max(max(per, min((work + p.few - 1) / (uint32_t)p.few, (uint32_t)kAttnFewSteps)), 1u);
+  }
   int items_before = 0, groups_before = 0;
   for (int b0 = 0; b0 < p.sequences; b0 += 64) {
     if (!one_round) load(b0 + lane, &len, &news, &start, &blocks);
@@ -207,9 +210,6 @@ struct Types {
   static constexpr float kLift = P::kCode == W4A16_F16 ? 6.0f : 0.0f;
 };
 
-#ifndef LBN
-#define LBN 3
-#endif
 constexpr float kSlack = 8.0f;  // how far (log2) a score may exceed the held maximum
 
 // 16-bit values: 1, the exponent's mask (all ones: infinity or NaN), and, for a
@@ -688,7 +688,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // masks but the length's, and its registers leave room for three waves per
 // SIMD instead of two (16 rows, up to 128 dims).
 template <typename T, int FMT, int DB, int R, bool FULL, bool TREE>
-__global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? LBN : 2) void attn_narrow_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? 3 : 2) void attn_narrow_kernel(AttnParams p) {
   using TY = Types<T, FMT>;
   constexpr bool kSame = TY::kSame;
   constexpr int kRows = 16 * R;

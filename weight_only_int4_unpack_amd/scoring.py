@@ -48,10 +48,10 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top_k: int = 0):
     dev = logits.device
     at = _array(ids, "ids", torch.int64, dev, T)
     need = workspace_bytes(T, V, top_k, _W._num_cus(dev))
-    logprobs = torch.empty((T,), dtype=torch.float32, device=dev)
-    entropy = torch.empty((T,), dtype=torch.float32, device=dev)
-    top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    top_ids = torch.empty((T, top_k), dtype=torch.int64, device=dev)
+    logprobs = torch.empty_like(ids, dtype=torch.float32)
+    entropy = torch.empty_like(logprobs)
+    top = logprobs.new_empty((T, top_k))
+    top_ids = ids.new_empty((T, top_k))
     ws = _W.stream_workspace(dev, need)
     _call(_W.lib().w4a16_token_logprobs, dev,
           _ARGS.pack(logits.data_ptr(), at, logprobs.data_ptr(), entropy.data_ptr(),

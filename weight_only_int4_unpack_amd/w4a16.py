@@ -184,23 +184,27 @@ def _num_cus(dev: torch.device) -> int:
 
 def stream_workspace(dev: torch.device, nbytes: int) -> torch.Tensor | None:
     """A workspace of at least ``nbytes`` from torch's allocator for the
-    current stream of ``dev``, its counter region zero (``torch.zeros``, a
-    fill kernel on that stream). Outside graph capture one workspace per
+    current stream of ``dev``, its counter region zero (a fill kernel on that
+    stream; what follows the counters needs no clearing). Outside graph capture one workspace per
     (device, stream) is kept and reused: every completed launch leaves its
     counters zero. During capture each call gets a fresh one from the
     graph's pool (its fill is recorded in the graph), so no memory of the
     graph is ever handed to eager work."""
     if nbytes <= 0:
         return None
-    stream = torch.cuda.current_stream(dev)
-    key = (dev.index, stream.cuda_stream)
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        return _zero_counters(torch.empty(nbytes, dtype=torch.uint8, device=dev))
+    key = (dev.index, torch._C._cuda_getCurrentRawStream(dev.index))
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
         size = max(nbytes, 2 * (0 if ws is None else ws.numel()))
-        ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+        ws = _zero_counters(torch.empty(size, dtype=torch.uint8, device=dev))
         _WS[key] = ws
+    return ws
+
+
+def _zero_counters(ws: torch.Tensor) -> torch.Tensor:
+    ws[:WORKSPACE_COUNTER_BYTES].zero_()
     return ws
 
 
