@@ -35,6 +35,7 @@ __global__ __launch_bounds__(256) void rope_table_kernel(RopeTableParams p) {
 enum Pairing {
   kPlain,       // nothing is rotated
   kHalves,      // dims i and i + r/2, r/2 a multiple of 8: one aligned vector each
+  kQuads,       // the same, r/2 a multiple of 4 only: two halves of a vector each
   kNeighbours,  // dims 2i and 2i + 1, r a multiple of 8: inside the lane
   kAny          // either, for other r: element by element
 };
@@ -53,12 +54,11 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
   return x;
 }
 
-constexpr int kBatch = 4;  // heads whose loads a lane has in flight
-
-// One lane group takes `per_unit` heads of a token in turn, so that the token's
-// row of the table and its slot are read once for several heads. Before this,
-// with one head a group, address arithmetic and table reads bound the kernel
-// (16384 tokens x 48 heads, e4m3: 149 us; with 8 heads 101 us).
+// One lane group takes `per_unit` (1 or 2) heads of a token in turn, so that the
+// token's row of the table and its slot are read once for both. Bound by HBM:
+// 16384 tokens x 48 heads into e4m3 79.8 us (4.75 TB/s; a large copy reaches
+// 5.2), with one head a group 100 us, with 4 and 8 (longer waves) 90 and 126;
+// a rotation of 8191 x 32 heads 25.6 us (5.3 TB/s).
 template <typename T, int FMT, int LPH, Pairing PAIR>
 __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
   const int lane = threadIdx.x % LPH;
@@ -71,11 +71,13 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
   const bool live = d0 < p.dim;
   const int half = p.rot / 2;
   const bool turns = PAIR != kPlain && live && d0 < p.rot;
+  // both at once, ahead of everything that waits for them
+  const int64_t slot = last > p.hq ? p.slots[token] : 0;
+  const int64_t pos = turns ? p.positions[token] : 0;
 
   // y[e] = own[e] x[e] + other[e] x[partner]; a position outside the table: NaN
   float own[8], other[8];
   if (turns) {
-    const int64_t pos = p.positions[token];
     const bool known = pos >= 0 && pos < p.table_rows;
     const float* row = p.table + (known ? pos : 0) * p.rot;
     const float bad = known ? 0.0f : __builtin_nanf("");
@@ -86,6 +88,19 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
         const f32x4 c = *(const f32x4*)(row + i0 + e), s = *(const f32x4*)(row + half + i0 + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          own[e + j] = c[j] + bad;
+          other[e + j] = sign * s[j];
+        }
+      }
+    } else if constexpr (PAIR == kQuads) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const int d = min(d0 + e, p.rot - 4);
+        const int i = d < half ? d : d - half;
+        const f32x4 c = *(const f32x4*)(row + i), s = *(const f32x4*)(row + half + i);
+        const float sign = d < half ? -flip : flip;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           own[e + j] = c[j] + bad;
@@ -121,6 +136,16 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
     if (live) r.own = load16(src + d0);
     if constexpr (PAIR == kHalves)
       if (turns) r.other = load16(src + (d0 < half ? d0 + half : d0 - half));
+    if constexpr (PAIR == kQuads)
+      if (turns) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const int d = min(d0 + e, p.rot - 4);
+          const u32x2 x = load8(src + (d < half ? d + half : d - half));
+          r.other[e / 2] = x.x;
+          r.other[e / 2 + 1] = x.y;
+        }
+      }
     if constexpr (PAIR == kAny)
       if (turns) {
         // elements past the rotated ones are their own partners, unused
@@ -144,31 +169,18 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float v = fmaf(own[e], x[e], other[e] * y[e]);
-        z[e] = PAIR != kAny || d0 + e < p.rot ? v : x[e];
+        z[e] = (PAIR != kAny && PAIR != kQuads) || d0 + e < p.rot ? v : x[e];
       }
     }
     return z;
   };
-  // Heads [a, b) of a kind, kBatch at a time.
-  auto each = [&](int a, int b, const uint16_t* src, int64_t stride, auto use) {
-    for (int h = a; h < b; h += kBatch) {
-      Raw r[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (h + i < b) r[i] = load(src + (h + i) * stride);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (h + i < b) use(h + i, r[i]);
-    }
-  };
-
-  each(first, min(last, p.hq), p.q + token * p.q_token, p.q_head, [&](int h, const Raw& r) {
+  for (int h = first; h < min(last, p.hq); ++h) {
+    const Raw r = load(p.q + token * p.q_token + h * p.q_head);
     const u32x4 y = turns ? narrow8<T>(turn(r)) : r.own;
     if (live) *(u32x4*)(p.q_out + token * p.out_token + h * p.out_head + d0) = y;
-  });
+  }
   if (last <= p.hq) return;
 
-  const int64_t slot = p.slots[token];
   const bool kept = slot >= 0 && slot < (p.cache.pages << p.cache.page_shift);
   const int64_t page = slot >> p.cache.page_shift;
   // row of head 0's token inside its page; the next head's is a page's tokens on
@@ -215,25 +227,23 @@ __global__ __launch_bounds__(256) void rope_kv_kernel(RopeKvParams p) {
       if (lane == 0 && kept) scales[at] = scale;
     }
   };
-  const int k0 = max(first - p.hq, 0), k1 = min(last - p.hq, p.hkv);
-  each(k0, k1, p.k + token * p.k_token, p.k_head, [&](int h, const Raw& r) {
-    write(h, r.own, turn(r), !turns, p.cache.k, p.cache.k_scale);
-  });
-  const int v0 = max(first - p.hq - p.hkv, 0), v1 = last - p.hq - p.hkv;
-  const uint16_t* v = p.v + token * p.v_token;
-  for (int h = v0; h < v1; h += kBatch) {
-    u32x4 r[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      r[i] = u32x4{0, 0, 0, 0};
-      if (h + i < v1 && live) r[i] = load16(v + (h + i) * p.v_head + d0);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (h + i < v1) write(h + i, r[i], widen8<T>(r[i]), true, p.cache.v, p.cache.v_scale);
+  for (int h = max(first, p.hq); h < min(last, p.hq + p.hkv); ++h) {
+    const Raw r = load(p.k + token * p.k_token + (h - p.hq) * p.k_head);
+    write(h - p.hq, r.own, turn(r), !turns, p.cache.k, p.cache.k_scale);
+  }
+  for (int h = max(first, p.hq + p.hkv); h < last; ++h) {
+    const int hk = h - p.hq - p.hkv;
+    u32x4 r = {0, 0, 0, 0};
+    if (live) r = load16(p.v + token * p.v_token + hk * p.v_head + d0);
+    write(hk, r, widen8<T>(r), true, p.cache.v, p.cache.v_scale);
   }
 }
 
+constexpr int kBatch = 4;  // heads whose loads a lane has in flight
+static_assert(kBatch == kReadUnit, "a unit is one batch");
+
+// Bound by HBM: 65536 tokens x 8 + 8 heads of e4m3 78.8 us (5.2 TB/s); a head at
+// a time 99 us.
 template <typename T, int FMT, int LPH>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
   const int lane = threadIdx.x % LPH;
@@ -290,6 +300,7 @@ void (*rope_kv_of(Pairing pair))(RopeKvParams) {
   switch (pair) {
     case kPlain: return rope_kv_kernel<T, FMT, LPH, kPlain>;
     case kHalves: return rope_kv_kernel<T, FMT, LPH, kHalves>;
+    case kQuads: return rope_kv_kernel<T, FMT, LPH, kQuads>;
     case kNeighbours: return rope_kv_kernel<T, FMT, LPH, kNeighbours>;
     default: return rope_kv_kernel<T, FMT, LPH, kAny>;
   }
@@ -303,6 +314,7 @@ hipError_t rope_kv_lanes(const RopeKvParams& p, hipStream_t stream) {
   const Pairing pair = p.table == nullptr                      ? kPlain
                        : p.interleaved && p.rot % 8 == 0       ? kNeighbours
                        : !p.interleaved && p.rot % 16 == 0     ? kHalves
+                       : !p.interleaved && p.rot % 8 == 0      ? kQuads
                                                                : kAny;
   const auto kernel = lph == 8    ? rope_kv_of<T, FMT, 8>(pair)
                       : lph == 16 ? rope_kv_of<T, FMT, 16>(pair)

@@ -92,12 +92,11 @@ w4a16_status check_rotation(const int64_t* positions, const float* table, int64_
   return W4A16_OK;
 }
 
-// Heads that one lane group takes in turn: as many, up to 8, as leave 4096 waves
-// (16 a CU), so that few tokens are spread out and many read their row of the
-// table and their slot once for several heads.
-void shape_units(int64_t tokens, int64_t heads, int dim, int32_t* per_unit, int32_t* units) {
+// Heads that one lane group takes in turn: `most`, or fewer where that would
+// leave less than 4096 waves (16 a CU).
+void shape_units(int64_t tokens, int64_t heads, int dim, int most, int32_t* per_unit, int32_t* units) {
   const int64_t waves = tokens * heads * lanes_per_head(dim) / 64;
-  *per_unit = (int32_t)std::min<int64_t>({std::max<int64_t>(waves / 4096, 1), 8, heads});
+  *per_unit = (int32_t)std::min<int64_t>({std::max<int64_t>(waves / 4096, 1), most, heads});
   *units = (int32_t)div_up(heads, *per_unit);
 }
 
@@ -316,7 +315,7 @@ w4a16_status w4a16_rope(const w4a16_rope_t* a, void* stream) {
   p.rot = a->rot_dim;
   p.interleaved = a->interleaved != 0;
   p.inverse = a->inverse != 0;
-  shape_units(a->tokens, a->heads, p.dim, &p.per_unit, &p.units_per_token);
+  shape_units(a->tokens, a->heads, p.dim, kRopeUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_rope_kv(p, a->dtype, W4A16_KV_SAME, (hipStream_t)stream));
 }
 
@@ -372,7 +371,7 @@ w4a16_status w4a16_kv_write(const w4a16_kv_write_t* a, void* stream) {
   p.dim = a->cache.head_dim;
   p.rot = a->rot_dim;
   p.interleaved = a->interleaved != 0;
-  shape_units(a->tokens, (int64_t)hq + 2 * p.hkv, p.dim, &p.per_unit, &p.units_per_token);
+  shape_units(a->tokens, (int64_t)hq + 2 * p.hkv, p.dim, kRopeUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_rope_kv(p, a->dtype, a->cache.format, (hipStream_t)stream));
 }
 
@@ -395,7 +394,7 @@ w4a16_status w4a16_kv_read(const w4a16_kv_read_t* a, void* stream) {
   p.k_out = (uint16_t*)a->k_out;
   p.v_out = (uint16_t*)a->v_out;
   p.tokens = (int32_t)a->tokens;
-  shape_units(a->tokens, 2 * (int64_t)view.heads, view.dim, &p.per_unit, &p.units_per_token);
+  shape_units(a->tokens, 2 * (int64_t)view.heads, view.dim, kReadUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_kv_read(p, a->dtype, a->cache.format, (hipStream_t)stream));
 }
 

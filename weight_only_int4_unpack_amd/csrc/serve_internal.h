@@ -56,6 +56,9 @@ struct RopeKvParams {
   int32_t units_per_token;
 };
 
+constexpr int kRopeUnit = 2;  // most heads of a unit: rotation and writing,
+constexpr int kReadUnit = 4;  // and reading
+
 struct KvReadParams {
   KvView cache;
   const int64_t* slots;
