@@ -1,20 +1,23 @@
 // Log probabilities of given tokens, entropy, and the largest alternatives:
 // one pass over each row of logits.
 //
-// A row is cut into `splits` parts, one workgroup each, and a part into tiles
-// of 8192 logits, 32 per thread. Each thread keeps its own running maximum m,
-// s = sum e^(x - m) and t = sum e^(x - m) (x - m) in fp32, joined once at the
-// end, so the stream has no reduction in it. From the joined sums
-//   ln p_id = (x_id - m) - ln s,   entropy = ln s - t / s
+// A row is cut into `splits` parts, one workgroup each, whose four waves read
+// tiles of 2048 logits in turn, 32 per lane, and do not meet until the part's
+// end. Each lane keeps its own running reference m, s = sum e^(x - m) and
+// t = sum e^(x - m) (x - m) in fp32 (in base 2: y = x log2 e - m is one
+// multiply-add, and the same rounded m is taken off everywhere, so it cancels).
+// From the joined sums
+//   log2 p_id = y_id - log2 s,   entropy = ln s - ln 2 t / s
 // (differences to m: no cancellation against a large maximum).
 //
 // Alternatives are ordered by one unsigned 64-bit key: the logit as an
 // order-preserving integer above the complement of its index, so keys are
 // all different, ties go to the lowest index, and "among the k largest" is an
-// exact comparison against a bound. The bound comes from the first tile: of
-// 64 (or 256) threads' own largest keys the k-th largest is below the k
-// largest keys of all, yet few keys pass it. Keys that pass go to a list in
-// LDS; from then on a tile costs one comparison per thread unless one passes.
+// exact comparison against a bound. A wave's bound comes from its first tile:
+// of its 64 lanes' own largest keys the k-th largest is below the k largest
+// keys of all, yet few keys pass it. Those that do go to the wave's list in LDS;
+// the four lists joined and cut to k give the workgroup's bound. From then on a
+// tile costs one comparison a lane, and few logits of it pass.
 #include "serve_device.h"
 
 namespace w4a16 {
@@ -22,9 +25,12 @@ namespace {
 
 using namespace serve;
 
-constexpr int kList = 1024;              // keys of the list in LDS
 constexpr int kWaves = kScoreThreads / 64;
+constexpr int kWaveTile = 64 * kScorePerThread;
+constexpr int kWaveList = 256;           // keys of a wave's list
+constexpr int kList = kScoreMaxTop + kWaves * kWaveList;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
@@ -39,6 +45,7 @@ __device__ __forceinline__ float value_of(uint64_t key) {
   return __builtin_bit_cast(float, u);
 }
 
+// m in units of log2.
 struct Sums {
   float m, s, t;
 };
@@ -46,14 +53,14 @@ struct Sums {
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
   const float m = fmaxf(a.m, b.m);
   const float da = a.m == -kInf ? 0.0f : a.m - m, db = b.m == -kInf ? 0.0f : b.m - m;
-  const float fa = __builtin_amdgcn_exp2f(da * kLog2e), fb = __builtin_amdgcn_exp2f(db * kLog2e);
-  // e^d d is 0 where e^d is: the clamp keeps 0 * inf out
+  const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
+  // 2^d d is 0 where 2^d is: the clamp keeps 0 * inf out
   const float ca = fmaxf(da, -1e4f), cb = fmaxf(db, -1e4f);
   return Sums{m, a.s * fa + b.s * fb, fa * (a.t + a.s * ca) + fb * (b.t + b.s * cb)};
 }
 
 template <typename E>
-struct Row;  // E: F16, BF16 or float
+struct Row;  // E: F16, BF16 or float. pack() undoes widen().
 template <>
 struct Row<float> {
   using Elem = float;
@@ -62,6 +69,10 @@ struct Row<float> {
   static __device__ __forceinline__ void widen(u32x4 r, float* x) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r[e]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* x) {
+    return u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                 __float_as_uint(x[3])};
   }
 };
 template <typename T>
@@ -74,44 +85,88 @@ struct Row16 {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = y[e];
   }
+  static __device__ __forceinline__ u32x4 pack(const float* x) {
+    return narrow8<T>(f32x8{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]});
+  }
 };
 template <>
 struct Row<F16> : Row16<F16> {};
 template <>
 struct Row<BF16> : Row16<BF16> {};
 
+template <int VECS>
 struct Lds {
-  uint64_t list[kList];
-  uint64_t best[kScoreThreads];
+  u32x4 held[kWaves][VECS][64];          // a tile in which logits passed
+  uint64_t list[kList + 16];             // the workgroup's k keys, then the waves' lists
   Sums sums[kWaves];
-  uint64_t bound[kWaves];
-  int32_t count[2][kWaves];
+  int32_t count[kWaves];
   int32_t last;
 };
 
-// The k largest of the n keys in the list, in order, at its start; returns
-// how many there are. A key's place is the number of larger ones.
-__device__ int keep_largest(Lds& l, int n, int k) {
-  __syncthreads();
-  uint64_t key[kList / kScoreThreads];
-  int place[kList / kScoreThreads];
+// How many of list[0..n) are larger than `key`; n rounded up to a multiple of
+// 16 whose rest holds zeros (no key is larger than itself, 0 than none).
+__device__ __forceinline__ int larger_than(const uint64_t* list, int n, uint64_t key) {
+  int larger = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; j += 16) {
 #pragma unroll
-  for (int i = 0; i < kList / kScoreThreads; ++i) {
-    const int at = threadIdx.x + i * kScoreThreads;
+    for (int i = 0; i < 16; ++i) larger += list[j + i] > key;
+  }
+  return larger;
+}
+
+// A wave's LDS accesses take effect in order; this holds the compiler to it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The k largest of the n keys of a list (room for 16 more), in order, at its
+// start; returns how many there are. A key's place is the number of larger
+// ones. THREADS: the wave or workgroup whose threads (`at` of them) come here.
+template <int THREADS, int MOST>
+__device__ __forceinline__ int keep_largest(uint64_t* list, int at, int n, int k) {
+  auto sync = [] {
+    if constexpr (THREADS > 64)
+      __syncthreads();
+    else
+      wave_sync();
+  };
+  constexpr int kEach = (MOST + THREADS - 1) / THREADS;
+  if (at < 16) list[n + at] = 0;
+  sync();
+  uint64_t key[kEach];
+  int place[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
     place[i] = k;
-    if (at < n) {
-      key[i] = l.list[at];
-      int larger = 0;
-      for (int j = 0; j < n; ++j) larger += l.list[j] > key[i];
-      place[i] = larger;
+    if (i * THREADS < n) {               // uniform
+      key[i] = list[min(at + i * THREADS, n)];
+      place[i] = at + i * THREADS < n ? larger_than(list, n, key[i]) : k;
     }
   }
-  __syncthreads();
+  sync();
 #pragma unroll
-  for (int i = 0; i < kList / kScoreThreads; ++i)
-    if (place[i] < k) l.list[place[i]] = key[i];
-  __syncthreads();
+  for (int i = 0; i < kEach; ++i)
+    if (place[i] < k) list[place[i]] = key[i];
+  sync();
   return min(n, k);
+}
+
+// The value of the lane whose number differs in one bit (or, inside 8 and 16
+// lanes, the mirrored one: enough where whole groups agree already).
+template <int STEP>
+__device__ __forceinline__ float other_lane(float x) {
+  if constexpr (STEP >= 16) return __shfl_xor(x, STEP);
+  constexpr int kCtrl = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), kCtrl, 0xF, 0xF, true));
+}
+template <int STEP>
+__device__ __forceinline__ Sums join_lanes(Sums a) {
+  return join(a, Sums{other_lane<STEP>(a.m), other_lane<STEP>(a.s), other_lane<STEP>(a.t)});
+}
+__device__ __forceinline__ Sums join_wave(Sums a) {
+  return join_lanes<32>(join_lanes<16>(join_lanes<8>(join_lanes<4>(join_lanes<2>(join_lanes<1>(a))))));
 }
 
 template <typename E>
@@ -119,19 +174,21 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
   using R = Row<E>;
   using Elem = typename R::Elem;
   constexpr int kVecs = kScorePerThread / R::kVec;
-  __shared__ Lds l;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ Lds<kVecs> l;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = blockIdx.x / p.splits, part = blockIdx.x - row * p.splits;
   const Elem* x0 = (const Elem*)p.logits + row * p.row_stride;
   const int lo = part * p.part, hi = min(p.vocab, lo + p.part);
   const int k = p.top_k;
   // Vectors start at 16-byte boundaries of memory: `lead` logits before lo.
   const int lead = (int)(((uintptr_t)(x0 + lo) & 15) / sizeof(Elem));
-  const int tiles = (hi - lo + lead + kScoreTile - 1) / kScoreTile;
+  const int tiles = (hi - lo + lead + kWaveTile - 1) / kWaveTile;
+  uint64_t* list = l.list + kScoreMaxTop + wave * kWaveList;
 
-  // First logit index of this thread's vector v of a tile.
+  // First logit index of this lane's vector v of a tile.
   auto first_of = [&](int tile, int v) {
-    return lo - lead + tile * kScoreTile + (v * kScoreThreads + tid) * R::kVec;
+    return lo - lead + tile * kWaveTile + (v * 64 + lane) * R::kVec;
   };
   u32x4 raw[kVecs];
   auto load = [&](int tile) {
@@ -142,136 +199,173 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
     }
   };
 
+  // ahead of the stream, for whichever part finishes the row
+  const int64_t id = p.ids[row];
+  const bool known = id >= 0 && id < p.vocab;
+  const float x_id = R::one(x0[known ? id : 0]);
+
   Sums sum{-kInf, 0.0f, 0.0f};
-  int kept = 0;                          // keys in the list, the same in every thread
+  int kept = 0;                          // keys in the wave's list
   uint64_t bound = 0;                    // keys below it are not among the k largest
-  load(0);
-  for (int tile = 0; tile < tiles; ++tile) {
-    float x[kScorePerThread];
+  float x[kScorePerThread], most[kVecs];
+  // Logit e of this lane's 32 of a tile: its index, and whether it is one of the part.
+  auto index_of = [&](int tile, int e) { return first_of(tile, e / R::kVec) + e % R::kVec; };
+
+  auto stream = [&](int tile) {          // the tile into x, most, sum; the next one on its way
+    const int i0 = lo - lead + tile * kWaveTile;
+    if (i0 >= lo && i0 + kWaveTile <= hi) {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = first_of(tile, v);
-      if (i >= lo && i + R::kVec <= hi) {
-        R::widen(raw[v], x + v * R::kVec);
-      } else {                           // the row's ends, element by element
+      for (int v = 0; v < kVecs; ++v) R::widen(raw[v], x + v * R::kVec);
+    } else {                             // the part's ends, element by element
 #pragma unroll
-        for (int e = 0; e < R::kVec; ++e)
-          x[v * R::kVec + e] = i + e >= lo && i + e < hi ? R::one(x0[i + e]) : -kInf;
+      for (int v = 0; v < kVecs; ++v) {
+        const int i = first_of(tile, v);
+        if (i >= lo && i + R::kVec <= hi) {
+          R::widen(raw[v], x + v * R::kVec);
+        } else {
+#pragma unroll
+          for (int e = 0; e < R::kVec; ++e)
+            x[v * R::kVec + e] = i + e >= lo && i + e < hi ? R::one(x0[i + e]) : -kInf;
+        }
       }
     }
-    if (tile + 1 < tiles) load(tile + 1);
-
-    float top = x[0];
+    if (tile + kWaves < tiles) load(tile + kWaves);
+    // IEEE maximum: NaN where one is, which raises nothing and passes every bound
+    float top = -kInf;
 #pragma unroll
-    for (int e = 1; e < kScorePerThread; ++e) top = fmaxf(top, x[e]);
-    if (top > sum.m) sum = join(sum, Sums{top, 0.0f, 0.0f});
+    for (int v = 0; v < kVecs; ++v) {
+      most[v] = x[v * R::kVec];
+#pragma unroll
+      for (int e = 1; e < R::kVec; ++e)
+        most[v] = __builtin_elementwise_maximum(most[v], x[v * R::kVec + e]);
+      top = __builtin_elementwise_maximum(top, most[v]);
+    }
+    if (top * kLog2e > sum.m) sum = join(sum, Sums{top * kLog2e, 0.0f, 0.0f});
     const float ref = sum.m == -kInf ? 0.0f : sum.m;
 #pragma unroll
     for (int e = 0; e < kScorePerThread; ++e) {
-      const float d = x[e] - ref;
-      const float w = __builtin_amdgcn_exp2f(d * kLog2e);
+      const float d = fmaf(x[e], kLog2e, -ref);
+      const float w = __builtin_amdgcn_exp2f(d);
       sum.s += w;
       sum.t = fmaf(w, fmaxf(d, -1e4f), sum.t);
     }
-    if (k == 0) continue;
-
-    auto key_at = [&](int e) -> uint64_t {  // 0: not a logit of this part
-      const int i = first_of(tile, e / R::kVec) + e % R::kVec;
-      return i >= lo && i < hi ? key_of(x[e], (uint32_t)i) : 0;
-    };
-    if (tile == 0) {
-      uint64_t best = 0;
-#pragma unroll
-      for (int e = 0; e < kScorePerThread; ++e) best = max(best, key_at(e));
-      l.best[tid] = best;
-      __syncthreads();
-      // up to 32 alternatives 64 threads' keys are enough (each wave finds a
-      // bound of its own, the largest serves); above, the workgroup's 256
-      const int from = k <= 32 ? wave * 64 : 0, n = k <= 32 ? 64 : kScoreThreads;
-      int larger = 0;
-      for (int j = from; j < from + n; ++j) larger += l.best[j] > best;
-      if (lane == 0) l.bound[wave] = 0;
-      __syncthreads();
-      if (larger == k - 1 && best != 0) l.bound[wave] = best;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) bound = max(bound, l.bound[w]);
-    }
+    return top;
+  };
+  // The tile's logits that pass the bound, into the wave's list: one a lane at a
+  // time, by way of LDS (a register's number must be known); the list is cut back
+  // whenever it could overflow.
+  auto collect = [&](int tile) {
     const float low = bound == 0 ? -kInf : value_of(bound);
-    int mine = 0;
-    // !(top < low): a thread whose logits are NaN has top = NaN or its others' maximum
-    if (!(top < low)) {
+    uint32_t mine = 0;                   // logits that may pass; NaN is ordered as -inf
+    bool any = false;
 #pragma unroll
-      for (int e = 0; e < kScorePerThread; ++e) {
-        const uint64_t key = key_at(e);
-        mine += key != 0 && key >= bound;
+    for (int v = 0; v < kVecs; ++v) {
+      if (!__any(!(most[v] < low))) continue;
+      any = true;
+#pragma unroll
+      for (int e = v * R::kVec; e < (v + 1) * R::kVec; ++e) mine |= !(x[e] < low) ? 1u << e : 0u;
+    }
+    if (!any) return;
+    const int i0 = lo - lead + tile * kWaveTile;
+    if (i0 < lo || i0 + kWaveTile > hi) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {  // places past the ends are no logits
+        const int i = first_of(tile, v);
+        const int from = min(max(lo - i, 0), R::kVec), to = min(max(hi - i, 0), R::kVec);
+        const uint32_t in = to > from ? ((1u << to) - 1) & ~((1u << from) - 1) : 0u;
+        mine &= ~(((1u << R::kVec) - 1) << (v * R::kVec)) | in << (v * R::kVec);
       }
     }
-    int before = mine;                   // inclusive prefix over the wave
-    if (__any(mine != 0)) {
 #pragma unroll
-      for (int s = 1; s < 64; s *= 2) {
-        const int o = __shfl_up(before, s);
-        before += lane >= s ? o : 0;
+    for (int v = 0; v < kVecs; ++v) l.held[wave][v][lane] = R::pack(x + v * R::kVec);
+    wave_sync();
+    while (__any(mine != 0)) {
+      if (kept + 64 > kWaveList - 16) {
+        kept = keep_largest<64, kWaveList>(list, lane, kept, k);
+        if (kept == k) bound = max(bound, list[k - 1]);
       }
+      uint64_t key = 0;
+      if (mine != 0) {
+        const int e = __builtin_ctz(mine);
+        mine &= mine - 1;
+        Elem it;
+        __builtin_memcpy(&it, (const char*)&l.held[wave][e / R::kVec][lane] + e % R::kVec * sizeof(Elem),
+                         sizeof(Elem));
+        key = key_of(R::one(it), (uint32_t)index_of(tile, e));
+      }
+      const bool in = key != 0 && key >= bound;
+      const uint64_t lanes = __ballot(in);
+      if (in) list[kept + __popcll(lanes & ((1ull << lane) - 1))] = key;
+      kept += __popcll(lanes);
     }
-    if (lane == 63) l.count[tile & 1][wave] = before;
+    wave_sync();                         // before `held` is written again
+  };
+  // The waves' lists and the workgroup's `have` keys into the workgroup's.
+  auto join_lists = [&](int have) {
+    if (lane == 0) l.count[wave] = kept;
     __syncthreads();
-    int total = 0, base = 0;
+    int at = have, all = have;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const int c = l.count[tile & 1][w];
-      base += w < wave ? c : 0;
-      total += c;
+      const int c = l.count[w];
+      at += w < wave ? c : 0;
+      all += c;
     }
-    if (total == 0) continue;
-    if (kept + total <= kList) {
-      int at = kept + base + before - mine;
-      if (mine != 0) {
+    uint64_t key[kWaveList / 64];
 #pragma unroll
-        for (int e = 0; e < kScorePerThread; ++e) {
-          const uint64_t key = key_at(e);
-          if (key != 0 && key >= bound) l.list[at++] = key;
-        }
-      }
-      kept += total;
-    } else {
-      // More than the list holds (ascending or equal logits): one logit of
-      // each thread at a time, the list cut back to k whenever it could
-      // overflow. Unrolled: a logit's register has to be known.
+    for (int i = 0; i < kWaveList / 64; ++i)
+      if (64 * i < kept) key[i] = list[lane + 64 * i];
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < kScorePerThread; ++e) {
-        if (kept + kScoreThreads > kList) {
-          kept = keep_largest(l, kept, k);
-          if (kept == k) bound = max(bound, l.list[k - 1]);
-        }
-        const uint64_t key = key_at(e);
-        const bool in = key != 0 && key >= bound;
-        const uint64_t lanes = __ballot(in);
-        __syncthreads();
-        if (lane == 0) l.count[0][wave] = __popcll(lanes);
-        __syncthreads();
-        int at = kept;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const int c = l.count[0][w];
-          at += w < wave ? c : 0;
-          kept += c;
-        }
-        if (in) l.list[at + __popcll(lanes & ((1ull << lane) - 1))] = key;
-      }
-      __syncthreads();                   // l.count is written again in the next tile
-    }
-    if (tile + 1 < tiles && kept > k) {
-      kept = keep_largest(l, kept, k);
-      bound = max(bound, l.list[k - 1]);
-    }
-  }
-  if (k > 0) kept = keep_largest(l, kept, k);
+    for (int i = 0; i < kWaveList / 64; ++i)
+      if (64 * i + lane < kept) l.list[at + 64 * i + lane] = key[i];
+    kept = 0;
+    return keep_largest<kScoreThreads, kList>(l.list, tid, all, k);
+  };
 
+  int have = 0;                          // keys of the workgroup's list
+  int tile = wave;
+  if (wave < tiles) {
+    load(tile);
+    const float top = stream(tile);
+    if (k > 0) {
+      // the lane's largest key: its largest logit at its lowest index (indices rise
+      // with e; a lane with a NaN, or of nothing but places past the ends: none)
+      int at = kScorePerThread;
 #pragma unroll
-  for (int s = 1; s < 64; s *= 2)
-    sum = join(sum, Sums{__shfl_xor(sum.m, s), __shfl_xor(sum.s, s), __shfl_xor(sum.t, s)});
+      for (int e = kScorePerThread - 1; e >= 0; --e) at = x[e] == top ? e : at;
+      uint64_t best = 0;
+      if (at < kScorePerThread) {
+        const int i = index_of(tile, at);
+        // -inf may be a place past the ends
+        if (i >= lo && i < hi) best = key_of(top, (uint32_t)i);
+      }
+      list[lane] = best;
+      wave_sync();
+      const uint64_t who = __ballot(best != 0 && larger_than(list, 64, best) == k - 1);
+      if (who != 0) {
+        const int from = __builtin_ctzll(who);
+        bound = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(best >> 32), from) << 32) |
+                (uint32_t)__builtin_amdgcn_readlane((int)best, from);
+      }
+      wave_sync();
+      collect(tile);
+    }
+    tile += kWaves;
+  }
+  if (k > 0) {
+    have = join_lists(0);
+    if (have == k) bound = max(bound, l.list[k - 1]);
+  }
+  for (; tile < tiles; tile += kWaves) {
+    stream(tile);
+    if (k > 0) collect(tile);
+  }
+  if (k > 0 && tiles > kWaves) {
+    if (__syncthreads_or(kept > 0)) have = join_lists(have);
+  }
+  kept = have;
+  sum = join_wave(sum);
   if (lane == 0) l.sums[wave] = sum;
   __syncthreads();
   sum = l.sums[0];
@@ -322,51 +416,65 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
                  __builtin_bit_cast(float, (uint32_t)word(lane, 1))};
       if (k > 0) kth = word(lane, 1 + k);
     }
+    sum = join_wave(sum);
 #pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      sum = join(sum, Sums{__shfl_xor(sum.m, s), __shfl_xor(sum.s, s), __shfl_xor(sum.t, s)});
-      kth = max(kth, (uint64_t)__shfl_xor((unsigned long long)kth, s));
-    }
+    for (int s = 1; s < 64; s *= 2) kth = max(kth, (uint64_t)__shfl_xor((unsigned long long)kth, s));
     if (k > 0) {
-      // 256 keys a round; the list is cut back whenever it could overflow.
+      // 1024 keys a round, their loads together
+      constexpr int kEach = 4;
       kept = 0;
       bound = kth;
-      for (int from = 0; from < p.splits * k; from += kScoreThreads) {
-        if (kept + kScoreThreads > kList) {
-          kept = keep_largest(l, kept, k);
+      for (int from = 0; from < p.splits * k; from += kEach * kScoreThreads) {
+        if (kept > kScoreMaxTop) {
+          kept = keep_largest<kScoreThreads, kList>(l.list, tid, kept, k);
           if (kept == k) bound = max(bound, l.list[k - 1]);
         }
-        const int i = from + tid;
-        const uint64_t key = i < p.splits * k ? word(i / k, 2 + i % k) : 0;
-        const bool in = key != 0 && key >= bound;
-        const uint64_t lanes = __ballot(in);
+        uint64_t key[kEach];
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int i = from + j * kScoreThreads + tid;
+          key[j] = i < p.splits * k ? word(i / k, 2 + i % k) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          if (key[j] < bound) key[j] = 0;
+          mine += key[j] != 0;
+        }
+        int upto = mine;                 // inclusive count over the wave
+#pragma unroll
+        for (int s = 1; s < 64; s *= 2) {
+          const int o = __shfl_up(upto, s);
+          upto += lane >= s ? o : 0;
+        }
         __syncthreads();
-        if (lane == 0) l.count[0][wave] = __popcll(lanes);
+        if (lane == 63) l.count[wave] = upto;
         __syncthreads();
-        int at = kept;
+        int at = kept + upto - mine;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const int c = l.count[0][w];
+          const int c = l.count[w];
           at += w < wave ? c : 0;
           kept += c;
         }
-        if (in) l.list[at + __popcll(lanes & ((1ull << lane) - 1))] = key;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (key[j] != 0) l.list[at++] = key[j];
       }
-      kept = keep_largest(l, kept, k);
+      kept = keep_largest<kScoreThreads, kList>(l.list, tid, kept, k);
     }
   }
 
-  // All -inf: no softmax (m = -inf would otherwise give ln 0).
-  const float log_s = sum.m == -kInf ? __builtin_nanf("") : logf(sum.s);
+  // All -inf: no softmax (m = -inf would otherwise give log 0).
+  const float log_s = sum.m == -kInf ? __builtin_nanf("") : __log2f(sum.s);
+  auto log_of = [&](float x) { return kLn2 * (fmaf(x, kLog2e, -sum.m) - log_s); };
   if (tid == 0) {
-    const int64_t id = p.ids[row];
-    const bool known = id >= 0 && id < p.vocab;
-    p.logprobs[row] = known ? (R::one(x0[known ? id : 0]) - sum.m) - log_s : __builtin_nanf("");
-    p.entropy[row] = log_s - sum.t / sum.s;
+    p.logprobs[row] = known ? log_of(x_id) : __builtin_nanf("");
+    p.entropy[row] = kLn2 * (log_s - sum.t / sum.s);
   }
   if (tid < k) {
     const uint64_t key = l.list[tid];
-    p.top_logprobs[(int64_t)row * k + tid] = (value_of(key) - sum.m) - log_s;
+    p.top_logprobs[(int64_t)row * k + tid] = log_of(value_of(key));
     p.top_ids[(int64_t)row * k + tid] = 0xFFFFFFFFu - (uint32_t)key;
   }
 }
