@@ -107,17 +107,19 @@ w4a16_status check_count(int64_t tokens, int64_t heads) {
   return W4A16_OK;
 }
 
-// Parts of a row of logits: enough workgroups to fill the CUs four times over
-// for few rows, never more than a tile each asks for, and one per row when
-// the rows alone are many (or more than the counters).
+// Parts of a row of logits: one round of the workgroups that the CUs hold, four
+// each (300 rows x 50257 fp32: 1200 workgroups 36 us, 900 30 us; 256 rows x 151667
+// bf16: twice as many 45 us, 1024 33 us, half as many 36 us), never more than a
+// tile each asks for, and one per row when the rows alone are many.
 int32_t score_splits(int64_t tokens, int64_t vocab, int num_cus, int32_t* part) {
   const int64_t tiles = div_up(vocab, kScoreTile);
-  int64_t want = div_up(4 * (int64_t)num_cus, std::max<int64_t>(tokens, 1));
+  int64_t want = 4 * (int64_t)num_cus / std::max<int64_t>(tokens, 1);
   want = std::min<int64_t>({want, tiles, kScoreMaxSplits});
-  if (tokens > kCounterBytes / 4) want = 1;
-  const int64_t per = div_up(tiles, std::max<int64_t>(want, 1));
-  *part = (int32_t)(per * kScoreTile);
-  return (int32_t)div_up(tiles, per);
+  if (tokens > kCounterBytes / (4 * kScoreCounterStride)) want = 1;
+  // equal parts, whole cache lines: a part of a few logits more than its waves' tiles
+  // takes as long as one of many
+  *part = (int32_t)(div_up(div_up(vocab, std::max<int64_t>(want, 1)), kScoreAlign) * kScoreAlign);
+  return (int32_t)div_up(vocab, *part);
 }
 
 w4a16_status score_workspace(int64_t tokens, int64_t vocab, int32_t top_k, int num_cus,

@@ -70,9 +70,12 @@ struct KvReadParams {
 
 // ---- token scores
 constexpr int kScoreThreads = 256;
-constexpr int kScorePerThread = 32;                       // logits of a tile that a thread holds
-constexpr int kScoreTile = kScoreThreads * kScorePerThread;
+constexpr int kScoreTile = 8192;                          // least logits of a part: a round of the waves
+constexpr int kScoreAlign = 64;                           // parts are multiples
 constexpr int kScoreMaxTop = 64;
+// Ints from a row's counter to the next one's: a cache line, on which parts of one row
+// only arrive (64 rows x 16 parts on two lines waited 3 us for each other).
+constexpr int kScoreCounterStride = 16;
 constexpr int kScoreMaxSplits = 64;                       // parts of a row: lanes of the last wave
 // What one part of a row hands over: max, sum, weighted sum, and top_k keys.
 __host__ __device__ constexpr int64_t score_part_bytes(int top_k) { return 16 + (int64_t)top_k * 8; }
@@ -89,7 +92,7 @@ struct ScoreParams {
   int32_t* counters;        // [tokens], zero between launches
   int32_t tokens, vocab, top_k;
   int32_t splits;           // parts of a row
-  int32_t part;             // logits of a part: a multiple of kScoreTile
+  int32_t part;             // logits of a part: a multiple of kScoreAlign
 };
 
 // ---- attention over the paged cache

@@ -2,22 +2,28 @@
 // one pass over each row of logits.
 //
 // A row is cut into `splits` parts, one workgroup each, whose four waves read
-// tiles of 2048 logits in turn, 32 per lane, and do not meet until the part's
-// end. Each lane keeps its own running reference m, s = sum e^(x - m) and
-// t = sum e^(x - m) (x - m) in fp32 (in base 2: y = x log2 e - m is one
-// multiply-add, and the same rounded m is taken off everywhere, so it cancels).
-// From the joined sums
+// tiles in turn, 64 bytes a lane, the next tile's loads on their way. Each lane
+// keeps its own running reference m, s = sum e^(x - m) and t = sum e^(x - m) (x - m)
+// in fp32 (in base 2: y = x log2 e - m is one multiply-add, and the same rounded m
+// is taken off everywhere, so it cancels). From the joined sums
 //   log2 p_id = y_id - log2 s,   entropy = ln s - ln 2 t / s
 // (differences to m: no cancellation against a large maximum).
 //
 // Alternatives are ordered by one unsigned 64-bit key: the logit as an
 // order-preserving integer above the complement of its index, so keys are
 // all different, ties go to the lowest index, and "among the k largest" is an
-// exact comparison against a bound. A wave's bound comes from its first tile:
-// of its 64 lanes' own largest keys the k-th largest is below the k largest
-// keys of all, yet few keys pass it. Those that do go to the wave's list in LDS;
-// the four lists joined and cut to k give the workgroup's bound. From then on a
-// tile costs one comparison a lane, and few logits of it pass.
+// exact comparison against a bound. A wave's bound comes from its first tile: the
+// k-th of its vectors' own largest logits is below the k largest of all, yet few
+// logits pass it. Those that do go to the wave's list in LDS. The waves meet after
+// the first tile, for a bound from all lists, and after the last; in between a
+// tile costs one comparison a vector, and few logits of it pass.
+//
+// What bounds it: the stream alone (top_k = 0) runs at 4.1 to 5.1 TB/s, near a
+// copy's 5.2; about 9 instructions a logit keep pace with that. Selection adds
+// a fixed chain of some 15 000 cycles per workgroup, of which every step
+// waits for the one before (bound, list, meeting, hand-off, order), and all
+// workgroups stand at the same place of it: 256 rows x 151667 bf16 take 19 us
+// without alternatives and 33 us with 20 of them; 1 row 5 and 12 us.
 #include "serve_device.h"
 
 namespace w4a16 {
@@ -26,9 +32,9 @@ namespace {
 using namespace serve;
 
 constexpr int kWaves = kScoreThreads / 64;
-constexpr int kWaveTile = 64 * kScorePerThread;
 constexpr int kWaveList = 256;           // keys of a wave's list
-constexpr int kList = kScoreMaxTop + kWaves * kWaveList;
+constexpr int kRound = 2;                // parts' keys that a thread takes at a time
+constexpr int kList = kScoreMaxTop + kRound * kScoreThreads;  // keys of the workgroup's list
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
@@ -59,13 +65,15 @@ __device__ __forceinline__ Sums join(Sums a, Sums b) {
   return Sums{m, a.s * fa + b.s * fb, fa * (a.t + a.s * ca) + fb * (b.t + b.s * cb)};
 }
 
+// Logits of a type: Elem their bits, kNone a word of -inf. pack() undoes widen().
 template <typename E>
-struct Row;  // E: F16, BF16 or float. pack() undoes widen().
+struct Row;  // E: F16, BF16 or float
 template <>
 struct Row<float> {
-  using Elem = float;
+  using Elem = uint32_t;
   static constexpr int kVec = 4;
-  static __device__ __forceinline__ float one(float x) { return x; }
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ float one(uint32_t x) { return __uint_as_float(x); }
   static __device__ __forceinline__ void widen(u32x4 r, float* x) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r[e]);
@@ -79,6 +87,7 @@ template <typename T>
 struct Row16 {
   using Elem = uint16_t;
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = T::kCode == W4A16_F16 ? 0xFC00FC00u : 0xFF80FF80u;
   static __device__ __forceinline__ float one(uint16_t x) { return widen1<T>(x); }
   static __device__ __forceinline__ void widen(u32x4 r, float* x) {
     const f32x8 y = widen8<T>(r);
@@ -97,7 +106,8 @@ struct Row<BF16> : Row16<BF16> {};
 template <int VECS>
 struct Lds {
   u32x4 held[kWaves][VECS][64];          // a tile in which logits passed
-  uint64_t list[kList + 16];             // the workgroup's k keys, then the waves' lists
+  uint64_t lists[kWaves][kWaveList];
+  uint64_t list[kList + 16];
   Sums sums[kWaves];
   int32_t count[kWaves];
   int32_t last;
@@ -121,9 +131,24 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// The largest 14 leading bits (sign, exponent, five of the mantissa) that at least k of
+// the wave's N * 64 words reach, one bit a step; 0: fewer than k are not 0.
+template <int N>
+__device__ __forceinline__ uint32_t kth_leading(const uint32_t (&word)[N], int k) {
+  uint32_t least = 0;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit >= 1u << 18; bit >>= 1) {
+    int reach = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) reach += __popcll(__ballot(word[i] >= (least | bit)));
+    least |= reach >= k ? bit : 0;
+  }
+  return least;
+}
+
 // The k largest of the n keys of a list (room for 16 more), in order, at its
 // start; returns how many there are. A key's place is the number of larger
-// ones. THREADS: the wave or workgroup whose threads (`at` of them) come here.
+// ones; of more than 64 those that cannot be among the k are dropped first. THREADS: the wave or workgroup whose threads (`at` of them) come here.
 template <int THREADS, int MOST>
 __device__ __forceinline__ int keep_largest(uint64_t* list, int at, int n, int k) {
   auto sync = [] {
@@ -133,14 +158,42 @@ __device__ __forceinline__ int keep_largest(uint64_t* list, int at, int n, int k
       wave_sync();
   };
   constexpr int kEach = (MOST + THREADS - 1) / THREADS;
+  uint64_t key[kEach];
+  if (n > 64) {
+    // every wave counts all keys, and moves those of its own chunks of 64
+    constexpr int kChunks = (MOST + 63) / 64, kWaves = THREADS / 64;
+    const int lane = at & 63, wave = at >> 6;
+    uint32_t word[kChunks];
+    int place[kEach];
+    sync();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int i = c * 64 + lane;
+      const uint64_t it = list[min(i, n - 1)];
+      word[c] = i < n ? (uint32_t)(it >> 32) : 0;
+      if (c % kWaves == wave) key[c / kWaves] = it;
+    }
+    const uint32_t least = kth_leading(word, k);
+    n = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const bool in = word[c] != 0 && word[c] >= least;
+      const uint64_t lanes = __ballot(in);
+      if (c % kWaves == wave) place[c / kWaves] = in ? n + __popcll(lanes & ((1ull << lane) - 1)) : -1;
+      n += __popcll(lanes);
+    }
+    sync();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (i * kWaves + wave < kChunks && place[i] >= 0) list[place[i]] = key[i];
+  }
   if (at < 16) list[n + at] = 0;
   sync();
-  uint64_t key[kEach];
   int place[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     place[i] = k;
-    if (i * THREADS < n) {               // uniform
+    if ((at & ~63) + i * THREADS < n) {  // uniform over the wave
       key[i] = list[min(at + i * THREADS, n)];
       place[i] = at + i * THREADS < n ? larger_than(list, n, key[i]) : k;
     }
@@ -170,10 +223,10 @@ __device__ __forceinline__ Sums join_wave(Sums a) {
 }
 
 template <typename E>
-__global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
+__global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) {
   using R = Row<E>;
   using Elem = typename R::Elem;
-  constexpr int kVecs = kScorePerThread / R::kVec;
+  constexpr int kVecs = 4, kPerLane = kVecs * R::kVec, kWaveTile = 64 * kPerLane;
   __shared__ Lds<kVecs> l;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -184,7 +237,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
   // Vectors start at 16-byte boundaries of memory: `lead` logits before lo.
   const int lead = (int)(((uintptr_t)(x0 + lo) & 15) / sizeof(Elem));
   const int tiles = (hi - lo + lead + kWaveTile - 1) / kWaveTile;
-  uint64_t* list = l.list + kScoreMaxTop + wave * kWaveList;
+  uint64_t* list = l.lists[wave];
 
   // First logit index of this lane's vector v of a tile.
   auto first_of = [&](int tile, int v) {
@@ -192,10 +245,40 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
   };
   u32x4 raw[kVecs];
   auto load = [&](int tile) {
+    const int i0 = lo - lead + tile * kWaveTile;
+    if (i0 >= lo && i0 + kWaveTile <= hi) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) raw[v] = load16(x0 + first_of(tile, v));
+      return;
+    }
+    // The part's ends: -inf in the places past them, which adds nothing.
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int i = first_of(tile, v);
+      raw[v] = u32x4{R::kNone, R::kNone, R::kNone, R::kNone};
       if (i >= lo && i + R::kVec <= hi) raw[v] = load16(x0 + i);
+    }
+    // A vector across an end (the first, or the one with hi): one logit a lane, gathered
+    // into the vector's lane.
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const int off = end == 0 ? 0 : hi - i0;
+      if (end == 0 ? i0 >= lo : off >= kWaveTile) continue;
+      const int i = i0 + off / R::kVec * R::kVec + lane;
+      uint32_t bits = (Elem)R::kNone;
+      if (lane < R::kVec && i >= lo && i < hi) bits = x0[i];
+      u32x4 whole;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (sizeof(Elem) == 4)
+          whole[w] = __builtin_amdgcn_readlane(bits, w);
+        else
+          whole[w] = __builtin_amdgcn_readlane(bits, 2 * w) |
+                     __builtin_amdgcn_readlane(bits, 2 * w + 1) << 16;
+      }
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        if (v * 64 + lane == off / R::kVec) raw[v] = whole;
     }
   };
 
@@ -207,29 +290,11 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
   Sums sum{-kInf, 0.0f, 0.0f};
   int kept = 0;                          // keys in the wave's list
   uint64_t bound = 0;                    // keys below it are not among the k largest
-  float x[kScorePerThread], most[kVecs];
+  float x[kPerLane], most[kVecs];
   // Logit e of this lane's 32 of a tile: its index, and whether it is one of the part.
   auto index_of = [&](int tile, int e) { return first_of(tile, e / R::kVec) + e % R::kVec; };
 
-  auto stream = [&](int tile) {          // the tile into x, most, sum; the next one on its way
-    const int i0 = lo - lead + tile * kWaveTile;
-    if (i0 >= lo && i0 + kWaveTile <= hi) {
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) R::widen(raw[v], x + v * R::kVec);
-    } else {                             // the part's ends, element by element
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const int i = first_of(tile, v);
-        if (i >= lo && i + R::kVec <= hi) {
-          R::widen(raw[v], x + v * R::kVec);
-        } else {
-#pragma unroll
-          for (int e = 0; e < R::kVec; ++e)
-            x[v * R::kVec + e] = i + e >= lo && i + e < hi ? R::one(x0[i + e]) : -kInf;
-        }
-      }
-    }
-    if (tile + kWaves < tiles) load(tile + kWaves);
+  auto stream = [&] {                    // x into most and sum
     // IEEE maximum: NaN where one is, which raises nothing and passes every bound
     float top = -kInf;
 #pragma unroll
@@ -243,20 +308,18 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
     if (top * kLog2e > sum.m) sum = join(sum, Sums{top * kLog2e, 0.0f, 0.0f});
     const float ref = sum.m == -kInf ? 0.0f : sum.m;
 #pragma unroll
-    for (int e = 0; e < kScorePerThread; ++e) {
+    for (int e = 0; e < kPerLane; ++e) {
       const float d = fmaf(x[e], kLog2e, -ref);
       const float w = __builtin_amdgcn_exp2f(d);
       sum.s += w;
       sum.t = fmaf(w, fmaxf(d, -1e4f), sum.t);
     }
-    return top;
   };
-  // The tile's logits that pass the bound, into the wave's list: one a lane at a
-  // time, by way of LDS (a register's number must be known); the list is cut back
-  // whenever it could overflow.
-  auto collect = [&](int tile) {
+  // Which of the tile's logits may pass the bound, one bit each; they go to LDS, since
+  // a register's number must be known and the n-th logit that passes is not.
+  auto candidates = [&](int tile) {
     const float low = bound == 0 ? -kInf : value_of(bound);
-    uint32_t mine = 0;                   // logits that may pass; NaN is ordered as -inf
+    uint32_t mine = 0;                   // !(x < low): NaN is ordered as -inf
     bool any = false;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
@@ -265,7 +328,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
 #pragma unroll
       for (int e = v * R::kVec; e < (v + 1) * R::kVec; ++e) mine |= !(x[e] < low) ? 1u << e : 0u;
     }
-    if (!any) return;
+    if (!any) return 0u;
     const int i0 = lo - lead + tile * kWaveTile;
     if (i0 < lo || i0 + kWaveTile > hi) {
 #pragma unroll
@@ -279,11 +342,18 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) l.held[wave][v][lane] = R::pack(x + v * R::kVec);
     wave_sync();
-    while (__any(mine != 0)) {
-      if (kept + 64 > kWaveList - 16) {
+    return mine;
+  };
+  // Those that pass into the wave's list, one a lane at a time. It is cut back to k
+  // whenever it could overflow, and to a lane a key where the waves meet afterwards.
+  auto collect = [&](int tile, uint32_t mine, bool meets) {
+    while (true) {
+      const bool more = __any(mine != 0);
+      if (kept > (more ? kWaveList - 16 - 64 : meets ? 64 : kWaveList)) {
         kept = keep_largest<64, kWaveList>(list, lane, kept, k);
         if (kept == k) bound = max(bound, list[k - 1]);
       }
+      if (!more) break;
       uint64_t key = 0;
       if (mine != 0) {
         const int e = __builtin_ctz(mine);
@@ -300,71 +370,64 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
     }
     wave_sync();                         // before `held` is written again
   };
-  // The waves' lists and the workgroup's `have` keys into the workgroup's.
-  auto join_lists = [&](int have) {
+  // Leading words of all waves' keys, a list in each register, and the bound they give.
+  uint32_t words[kWaves];
+  auto meet = [&] {
     if (lane == 0) l.count[wave] = kept;
     __syncthreads();
-    int at = have, all = have;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const int c = l.count[w];
-      at += w < wave ? c : 0;
-      all += c;
+      const uint32_t word = (uint32_t)(l.lists[w][lane] >> 32);
+      words[w] = lane < l.count[w] ? word : 0;
     }
-    uint64_t key[kWaveList / 64];
-#pragma unroll
-    for (int i = 0; i < kWaveList / 64; ++i)
-      if (64 * i < kept) key[i] = list[lane + 64 * i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWaveList / 64; ++i)
-      if (64 * i + lane < kept) l.list[at + 64 * i + lane] = key[i];
-    kept = 0;
-    return keep_largest<kScoreThreads, kList>(l.list, tid, all, k);
+    bound = max(bound, (uint64_t)kth_leading(words, k) << 32);
   };
 
-  int have = 0;                          // keys of the workgroup's list
-  int tile = wave;
-  if (wave < tiles) {
-    load(tile);
-    const float top = stream(tile);
-    if (k > 0) {
-      // the lane's largest key: its largest logit at its lowest index (indices rise
-      // with e; a lane with a NaN, or of nothing but places past the ends: none)
-      int at = kScorePerThread;
+  // One copy of the code for the first tile and the others: cold instructions cost a
+  // short row more than its arithmetic.
+  const int rounds = (tiles + kWaves - 1) / kWaves;
+#pragma unroll 1
+  for (int r = -1; r < rounds; ++r) {
+    const int tile = r * kWaves + wave;
+    if (r >= 0 && tile < tiles) {
 #pragma unroll
-      for (int e = kScorePerThread - 1; e >= 0; --e) at = x[e] == top ? e : at;
-      uint64_t best = 0;
-      if (at < kScorePerThread) {
-        const int i = index_of(tile, at);
-        // -inf may be a place past the ends
-        if (i >= lo && i < hi) best = key_of(top, (uint32_t)i);
-      }
-      list[lane] = best;
-      wave_sync();
-      const uint64_t who = __ballot(best != 0 && larger_than(list, 64, best) == k - 1);
-      if (who != 0) {
-        const int from = __builtin_ctzll(who);
-        bound = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(best >> 32), from) << 32) |
-                (uint32_t)__builtin_amdgcn_readlane((int)best, from);
-      }
-      wave_sync();
-      collect(tile);
+      for (int v = 0; v < kVecs; ++v) R::widen(raw[v], x + v * R::kVec);
     }
-    tile += kWaves;
+    if (tile + kWaves < tiles) load(tile + kWaves);
+    if (r < 0) continue;
+    uint32_t mine = 0;
+    if (tile < tiles) {
+      stream();
+      if (k > 0) {
+        if (r == 0) {                    // of the vectors' largest logits the k-th
+          uint32_t best[kVecs];
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v)
+            best[v] = most[v] == most[v] ? (uint32_t)(key_of(most[v], 0) >> 32) : 0u;
+          bound = (uint64_t)kth_leading(best, k) << 32;
+        }
+        mine = candidates(tile);
+      }
+    }
+    if (k > 0) {
+      const bool meets = r == 0 || r == rounds - 1;
+      collect(tile, mine, meets);
+      if (meets) meet();
+      if (meets && r < rounds - 1) __syncthreads();  // all have read the lists
+    }
   }
-  if (k > 0) {
-    have = join_lists(0);
-    if (have == k) bound = max(bound, l.list[k - 1]);
+  if (k > 0) {                           // what passes the last bound, in order
+    kept = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const bool in = words[w] != 0 && words[w] >= (uint32_t)(bound >> 32);
+      const uint64_t lanes = __ballot(in);
+      if (w == wave && in) l.list[kept + __popcll(lanes & ((1ull << lane) - 1))] = list[lane];
+      kept += __popcll(lanes);
+    }
+    __syncthreads();
+    kept = keep_largest<kScoreThreads, kList>(l.list, tid, kept, k);
   }
-  for (; tile < tiles; tile += kWaves) {
-    stream(tile);
-    if (k > 0) collect(tile);
-  }
-  if (k > 0 && tiles > kWaves) {
-    if (__syncthreads_or(kept > 0)) have = join_lists(have);
-  }
-  kept = have;
   sum = join_wave(sum);
   if (lane == 0) l.sums[wave] = sum;
   __syncthreads();
@@ -395,62 +458,63 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __syncthreads();
     if (tid == 0)
-      l.last = __hip_atomic_fetch_add(p.counters + row, 1, __ATOMIC_RELAXED,
+      l.last = __hip_atomic_fetch_add(p.counters + row * kScoreCounterStride, 1, __ATOMIC_RELAXED,
                                       __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
     __syncthreads();
     if (!l.last) return;
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    if (tid == 0) __hip_atomic_store(p.counters + row, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid == 0) __hip_atomic_store(p.counters + row * kScoreCounterStride, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     auto word = [&](int s, int i) {
       return __hip_atomic_load((const uint64_t*)(rows + s * bytes) + i, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
     };
-    // Every wave joins the sums (one part per lane) and finds the bound: the
-    // largest of the parts' k-th keys.
-    sum = Sums{-kInf, 0.0f, 0.0f};
-    uint64_t kth = 0;
-    if (lane < p.splits) {
-      const uint64_t a = word(lane, 0);
-      sum = Sums{__builtin_bit_cast(float, (uint32_t)a),
-                 __builtin_bit_cast(float, (uint32_t)(a >> 32)),
-                 __builtin_bit_cast(float, (uint32_t)word(lane, 1))};
-      if (k > 0) kth = word(lane, 1 + k);
-    }
-    sum = join_wave(sum);
+    // Every wave joins the sums (one part per lane) and finds a bound: the k-th of
+    // the parts' first keys, as many of each as there are lanes for.
+    const int each = 64 / p.splits, of = lane / each;
+    const uint64_t a = word(min(lane, p.splits - 1), 0), b = word(min(lane, p.splits - 1), 1);
+    uint64_t key[kRound];
+    auto fetch = [&](int from) {
 #pragma unroll
-    for (int s = 1; s < 64; s *= 2) kth = max(kth, (uint64_t)__shfl_xor((unsigned long long)kth, s));
+      for (int j = 0; j < kRound; ++j) {
+        const int i = from + j * kScoreThreads + tid;
+        key[j] = i < p.splits * k ? word(i / k, 2 + i % k) : 0;
+      }
+    };
     if (k > 0) {
-      // 1024 keys a round, their loads together
-      constexpr int kEach = 4;
+      const int rank = lane - of * each;
+      const uint64_t first = of < p.splits && rank < k ? word(of, 2 + rank) : 0;
+      fetch(0);
+      const uint32_t words[1] = {(uint32_t)(first >> 32)};
+      bound = (uint64_t)kth_leading(words, k) << 32;
+    }
+    sum = Sums{-kInf, 0.0f, 0.0f};
+    if (lane < p.splits)
+      sum = Sums{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)),
+                 __uint_as_float((uint32_t)b)};
+    sum = join_wave(sum);
+    if (k > 0) {
       kept = 0;
-      bound = kth;
-      for (int from = 0; from < p.splits * k; from += kEach * kScoreThreads) {
-        if (kept > kScoreMaxTop) {
+#pragma unroll 1
+      for (int from = 0;; from += kRound * kScoreThreads) {
+        const bool more = from < p.splits * k;
+        if (!more || kept > kScoreMaxTop) {
           kept = keep_largest<kScoreThreads, kList>(l.list, tid, kept, k);
           if (kept == k) bound = max(bound, l.list[k - 1]);
         }
-        uint64_t key[kEach];
-        int mine = 0;
+        if (!more) break;
+        if (from > 0) fetch(from);
+        int place[kRound], mine = 0;
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const int i = from + j * kScoreThreads + tid;
-          key[j] = i < p.splits * k ? word(i / k, 2 + i % k) : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
+        for (int j = 0; j < kRound; ++j) {
           if (key[j] < bound) key[j] = 0;
-          mine += key[j] != 0;
-        }
-        int upto = mine;                 // inclusive count over the wave
-#pragma unroll
-        for (int s = 1; s < 64; s *= 2) {
-          const int o = __shfl_up(upto, s);
-          upto += lane >= s ? o : 0;
+          const uint64_t lanes = __ballot(key[j] != 0);
+          place[j] = mine + __popcll(lanes & ((1ull << lane) - 1));
+          mine += __popcll(lanes);
         }
         __syncthreads();
-        if (lane == 63) l.count[wave] = upto;
+        if (lane == 0) l.count[wave] = mine;
         __syncthreads();
-        int at = kept + upto - mine;
+        int at = kept;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
           const int c = l.count[w];
@@ -458,10 +522,9 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreParams p) {
           kept += c;
         }
 #pragma unroll
-        for (int j = 0; j < kEach; ++j)
-          if (key[j] != 0) l.list[at++] = key[j];
+        for (int j = 0; j < kRound; ++j)
+          if (key[j] != 0) l.list[at + place[j]] = key[j];
       }
-      kept = keep_largest<kScoreThreads, kList>(l.list, tid, kept, k);
     }
   }
 
