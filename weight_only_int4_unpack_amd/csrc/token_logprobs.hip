@@ -371,7 +371,8 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
     wave_sync();                         // before `held` is written again
   };
   // Leading words of all waves' keys, a list in each register, and the bound they give.
-  uint32_t words[kWaves];
+  // `met` is the same in all waves, `bound` a wave's own where that is tighter.
+  uint32_t words[kWaves], met = 0;
   auto meet = [&] {
     if (lane == 0) l.count[wave] = kept;
     __syncthreads();
@@ -380,7 +381,8 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
       const uint32_t word = (uint32_t)(l.lists[w][lane] >> 32);
       words[w] = lane < l.count[w] ? word : 0;
     }
-    bound = max(bound, (uint64_t)kth_leading(words, k) << 32);
+    met = kth_leading(words, k);
+    bound = max(bound, (uint64_t)met << 32);
   };
 
   // One copy of the code for the first tile and the others: cold instructions cost a
@@ -416,11 +418,11 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
       if (meets && r < rounds - 1) __syncthreads();  // all have read the lists
     }
   }
-  if (k > 0) {                           // what passes the last bound, in order
+  if (k > 0) {                           // what passes the common bound, in order
     kept = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const bool in = words[w] != 0 && words[w] >= (uint32_t)(bound >> 32);
+      const bool in = words[w] != 0 && words[w] >= met;
       const uint64_t lanes = __ballot(in);
       if (w == wave && in) l.list[kept + __popcll(lanes & ((1ull << lane) - 1))] = list[lane];
       kept += __popcll(lanes);
