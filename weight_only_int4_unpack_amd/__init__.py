@@ -9,3 +9,4 @@ from . import w4a16  # noqa: F401  (binding; loads the library on first call)
 from . import op  # noqa: F401  (registers torch.ops.w4a16.gemm; calls go through the binding)
 from . import attn  # noqa: F401  (rotary positions, paged cache, attention over it)
 from . import scoring  # noqa: F401  (token log probabilities)
+from . import serve_op  # noqa: F401  (registers torch.ops.w4a16.rope, kv_write, ...)
