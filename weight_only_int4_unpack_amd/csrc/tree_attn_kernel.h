@@ -306,13 +306,25 @@ struct Rows {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   }
 
-  // Whether this lane's row r sees token t (which has to exist).
-  __device__ __forceinline__ bool sees(const AttnParams& p, int r, int t) const {
-    const int j = t - prefix;
-    if (j < 0) return true;
-    if (p.mask == nullptr) return j <= query[r];
-    return j < 64 * p.mask_words &&
-           ((p.mask[(int64_t)(start + query[r]) * p.mask_words + (j >> 6)] >> (j & 63)) & 1);
+  // Which of the tile's tokens that exist this lane's row r sees: bit 4u + i for token
+  // 16u + 4g + i. The row's 32 bits of the mask lie in two words, loaded together
+  // (one load a token cost a drafted tree 10 us).
+  __device__ __forceinline__ uint32_t sees(const AttnParams& p, int r, int t0) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int j0 = t0 - prefix;           // the first token among the new ones, if >= 0
+    uint32_t bits;
+    if (p.mask == nullptr) {
+      const int upto = query[r] - j0 + 1; // tokens of the tile up to the row's own
+      bits = upto >= 32 ? ~0u : upto <= 0 ? 0u : (1u << upto) - 1;
+    } else {
+      const uint64_t* row = p.mask + (int64_t)(start + query[r]) * p.mask_words;
+      const int at = j0 >> 6, by = j0 & 63;
+      const uint64_t a = row[min(max(at, 0), p.mask_words - 1)];
+      const uint64_t b = row[min(max(at + 1, 0), p.mask_words - 1)];
+      auto word = [&](int i, uint64_t x) { return i < 0 ? ~0ull : i < p.mask_words ? x : 0ull; };
+      bits = (uint32_t)(word(at, a) >> by | (by > 0 ? word(at + 1, b) << (64 - by) : 0ull));
+    }
+    return ((bits >> (4 * g)) & 0xFu) | ((bits >> (16 + 4 * g)) & 0xFu) << 4;
   }
 
   // One tile of 32 tokens from t0. k_op(u, i): operand of half tile u and step
@@ -359,11 +371,7 @@ struct Rows {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         seen[r] = in_all;
-        if constexpr (TREE) {
-#pragma unroll 1                          // rare: keep it small
-          for (int x = 0; x < 8; ++x)
-            if (!sees(p, r, t0 + 16 * (x >> 2) + 4 * g + (x & 3))) seen[r] &= ~(1u << x);
-        }
+        if constexpr (TREE) seen[r] &= sees(p, r, t0);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -535,19 +543,35 @@ __device__ __forceinline__ Range range_of(const AttnParams& p, const Item& it, i
   return r;
 }
 
-// The page of token t (uniform; a scalar load), and its first row (of head_dim
-// values, or of scales) for the item's head; row 0 where there is no such page.
-__device__ __forceinline__ int page_of(const AttnParams& p, const Item& it, int t) {
+// The item's row of the block table, and the first row (of head_dim values, or of
+// scales) of a token for the item's head. Scalar arithmetic in 32 bits where it
+// can be: there is no scalar comparison of 64 bits, and the lookups are a part of
+// each pass that nothing hides.
+struct Pages {
   // the constant address space: nothing writes the table while the kernel runs,
-  // so the load may be a scalar one, apart from the vector loads' counter
+  // so the loads may be scalar ones, apart from the vector loads' counter
   typedef const __attribute__((address_space(4))) int32_t* Table;
-  return ((Table)p.block_table)[it.seq * p.table_stride + (min(t, it.len - 1) >> p.cache.page_shift)];
-}
-__device__ __forceinline__ int64_t row_of(const AttnParams& p, const Item& it, int page, int t, bool* ok) {
-  *ok = page >= 0 && page < p.cache.pages && t < it.len;
-  return (((int64_t)(*ok ? page : 0) * p.cache.heads + it.head) << p.cache.page_shift) +
-         (t & ((1 << p.cache.page_shift) - 1));
-}
+  Table table;
+  uint32_t pages;
+  int shift, last, heads, head, len;
+  __device__ __forceinline__ Pages(const AttnParams& p, const Item& it)
+      : table((Table)(p.block_table + it.seq * p.table_stride)),
+        pages((uint32_t)min(p.cache.pages, (int64_t)0x7FFFFFFF)),
+        shift(p.cache.page_shift),
+        last(it.len - 1),
+        heads(p.cache.heads),
+        head(it.head),
+        len(it.len) {}
+  // The page of token t (uniform; past the end, of the last token).
+  __device__ __forceinline__ int of(int t) const { return table[(uint32_t)min(t, last) >> shift]; }
+  __device__ __forceinline__ bool there(int page, int t) const {
+    return (uint32_t)page < pages && t < len;
+  }
+  // Row 0 of page 0 where the token is not there.
+  __device__ __forceinline__ int64_t row(int page, int t, bool there) const {
+    return (((int64_t)(there ? page : 0) * heads + head) << shift) + (t & ((1 << shift) - 1));
+  }
+};
 
 // The parts, as a bounded buffer. A part's rows (DB floats each), then their
 // statistics (maximum, denominator). Stores are written through to the device's
@@ -723,15 +747,19 @@ __global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? 3 : 2) vo
   int64_t at[2];                               // rows of the next tile's half tiles
   bool ok[2] = {false, false};
 
+  const Pages table(p, it);
   int pages[2];
   auto look_up = [&](int n) {                  // two tiles ahead: scalar loads, never waited for
 #pragma unroll
-    for (int u = 0; u < 2; ++u) pages[u] = page_of(p, it, range.begin + n * kAttnTile + 16 * u);
+    for (int u = 0; u < 2; ++u) pages[u] = table.of(range.begin + n * kAttnTile + 16 * u);
   };
   auto take_rows = [&](int n) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      at[u] = row_of(p, it, pages[u], range.begin + n * kAttnTile + 16 * u, &ok[u]);
+    for (int u = 0; u < 2; ++u) {
+      const int t = range.begin + n * kAttnTile + 16 * u;
+      ok[u] = table.there(pages[u], t);
+      at[u] = table.row(pages[u], t, ok[u]);
+    }
   };
   auto load_k = [&]() {
 #pragma unroll
@@ -995,19 +1023,23 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   u32x2 kreg[kPasses], vreg[kPasses];          // 8-bit caches: on their way through registers
   float sreg = 0.0f;                           // a token's scale: lanes 0..15 K's, 16..31 V's
   bool exists[4];                              // of the stage on its way, by 16 tokens
+  const Pages table(p, it);
   int pages[4];                                // of the stage after that
   auto look_up = [&](int n) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) pages[u] = page_of(p, it, range.begin + n * kAttnStage + 16 * u);
+    for (int u = 0; u < 4; ++u) pages[u] = table.of(range.begin + n * kAttnStage + 16 * u);
   };
   auto load = [&](int n) {
     const int t0 = range.begin + n * kAttnStage;
-    int64_t at = 0;
+    int page = 0;
+    bool there = false;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t x = row_of(p, it, pages[u], t0 + 16 * u, &exists[u]);
-      at = wave == u ? x : at;
+      exists[u] = table.there(pages[u], t0 + 16 * u);
+      page = wave == u ? pages[u] : page;
+      there = wave == u ? exists[u] : there;
     }
+    const int64_t at = table.row(page, t0 + 16 * wave, there);
     look_up(n + 1);                            // scalar loads, back by the next stage
     const char* ksrc = kbase + at * row_bytes;
     const char* vsrc = vbase + at * row_bytes;
