@@ -508,8 +508,8 @@ typedef struct {
  * and NaN included). Tokens past table_pages * page_size and tokens on pages
  * outside 0..pages-1 are seen by none. Lengths below 0 count as 0.
  * Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to 16 bits for the matrix cores (bf16 in front of 8-bit codes, else
- * the dtype).
+ * rounded to 16 bits for the matrix cores (fp16 in front of 8-bit codes, with
+ * V's scales in them; else the dtype).
  * Scratch: `workspace` as for w4a16_gemm_ws (counters first, zero before
  * first use), of at least w4a16_tree_attention_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, VALUE (scale), WORKSPACE, DEVICE, HIP.

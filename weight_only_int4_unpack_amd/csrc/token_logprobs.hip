@@ -148,7 +148,8 @@ __device__ __forceinline__ uint32_t kth_leading(const uint32_t (&word)[N], int k
 
 // The k largest of the n keys of a list (room for 16 more), in order, at its
 // start; returns how many there are. A key's place is the number of larger
-// ones; of more than 64 those that cannot be among the k are dropped first. THREADS: the wave or workgroup whose threads (`at` of them) come here.
+// ones; of more than 64 those that cannot be among the k are dropped first.
+// THREADS: the wave or workgroup whose threads (`at` of them) come here.
 template <int THREADS, int MOST>
 __device__ __forceinline__ int keep_largest(uint64_t* list, int at, int n, int k) {
   auto sync = [] {
@@ -465,7 +466,9 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
     __syncthreads();
     if (!l.last) return;
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    if (tid == 0) __hip_atomic_store(p.counters + row * kScoreCounterStride, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid == 0)
+      __hip_atomic_store(p.counters + row * kScoreCounterStride, 0, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
     auto word = [&](int s, int i) {
       return __hip_atomic_load((const uint64_t*)(rows + s * bytes) + i, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);

@@ -13,19 +13,18 @@
 // and rescaling are per lane, and only joining the four lane groups shuffles.
 //
 // The A operands follow: K rows are read along the dims as they lie in memory
-// (lane (g, c): token c, 16 bytes at dim chunk g). V is read in rows too (lane
-// (g, c): its 8 tokens, dims c * DB/16 .. +DB/16, so a row of the page is one
-// contiguous run over 16 lanes); one byte permute joins two tokens' values of
-// a dim into an operand word, and tile j of O^T holds dims c * DB/16 + j.
+// (lane (g, c): token c, 16 bytes at dim chunk g). V is read in rows too.
 //
 // 8-bit codes are widened exactly to 16 bits; a token's scales multiply its
 // scores and its weights, which are one value per lane and token.
 //
-// Two kernels share this. Few rows (narrow): the four waves of a workgroup
-// hold the same rows and take turns at the tokens, operands go from memory
-// into registers, and the waves' sums are joined at the end. Many rows (wide):
-// each wave holds rows of its own, and the workgroup stages 64 tokens at a
-// time through LDS, widened and laid out as operands once for all four.
+// Two kernels share this, by the rows of a group (new tokens x query heads of a
+// key/value head). Up to 32 rows (narrow): the four waves of a workgroup hold the
+// same rows and take turns at the tokens, operands go from memory into
+// registers, and the waves' sums are joined at the end: nothing waits for LDS,
+// and every byte of the cache is read once. More rows (wide): each wave holds
+// rows of its own, and the workgroup stages 64 tokens at a time in LDS for all
+// four, since a wave that reads the cache alone feeds too few products.
 #pragma once
 
 #include <type_traits>
@@ -331,9 +330,9 @@ struct Rows {
   // i; k_scale(u), v_scale(u): scales of this lane's 4 tokens; after(): called
   // once the K operands are consumed; v_op(j): operand of O^T's tile j. EDGE: some
   // token may be unseen by some row; without TREE no token is unseen that exists.
-  // exists[u]: half tile u lies on a page. v_edge(in): lets the caller clear V of tokens that do not exist
-  // (bit 4u + i of `in`: this lane's token does) and say (uniform) whether V
-  // holds an infinity or NaN.
+  // exists[u]: half tile u lies on a page. v_edge(in): lets the caller clear V of
+  // tokens that do not exist (bit 4u + i of `in`: this lane's token does) and say
+  // (uniform) whether V holds an infinity or NaN.
   template <bool EDGE, bool TREE, typename KOp, typename KScale, typename After, typename VEdge,
             typename VScale, typename VOp, typename Fresh>
   __device__ __forceinline__ void tile(const AttnParams& p, int t0, const bool* exists,
@@ -708,11 +707,31 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 }
 
 // ---------------------------------------------------------------- few rows
+// Lane (g, c) reads V of its 8 tokens, dims c * DB/16 .. +DB/16, so that a row of
+// the page is one contiguous run over 16 lanes; one byte permute joins two
+// tokens' values of a dim into an operand word, and tile j of O^T holds dims
+// c * DB/16 + j. A tile's loads are issued one tile ahead, its pages two.
+//
+// Bound by HBM where there is enough to read: 64 sequences of up to 8192 tokens,
+// 8 heads of 128 in e4m3, 118 us (4.7 TB/s; a copy reaches 5.2); 32 such in bf16
+// 109 us (5.1 TB/s). With little to read the chain of launch, item search, a
+// few tiles, parts and their join: 4099 tokens of one sequence 12 us, of which
+// the bytes are 3.
+//
 // Without TREE (one new token per sequence and no mask) the kernel needs no
 // masks but the length's, and its registers leave room for three waves per
 // SIMD instead of two (16 rows, up to 128 dims).
+//
+// With TREE, 32 rows of 128 dims and values that may be infinite or NaN, two waves
+// a SIMD would spill in the token loop: one wave with twice the registers takes 30
+// instead of 38 us (8 tokens of one sequence over 16384, bf16), 36 instead of 43 (16
+// over 4000, e4m3); int8, which does not spill, keeps two (30 us against 39).
+constexpr int narrow_waves(int fmt, int db, int r, bool tree) {
+  return !tree && r * db <= 128 ? 3 : tree && r * db == 256 && fmt != W4A16_KV_INT8 ? 1 : 2;
+}
 template <typename T, int FMT, int DB, int R, bool FULL, bool TREE>
-__global__ __launch_bounds__(64 * kAttnWaves, !TREE && R * DB <= 128 ? 3 : 2) void attn_narrow_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * kAttnWaves, narrow_waves(FMT, DB, R, TREE)) void attn_narrow_kernel(
+    AttnParams p) {
   using TY = Types<T, FMT>;
   constexpr bool kSame = TY::kSame;
   constexpr int kRows = 16 * R;
@@ -987,6 +1006,18 @@ __device__ __forceinline__ u32x2 read_transposed(Lds at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)at));
 }
 
+// Two stages, so that the next one's copies run under the products; 16-bit rows go
+// straight into LDS, 8-bit ones through registers, where they are widened. V lies
+// in rows, as K does, and is read transposed.
+//
+// Bound by issue: at 32 rows a wave, 64 tokens take 64 products (1024 cycles of
+// the matrix core) and about as long again in exponentials (32 x 16 cycles),
+// multiply-adds, sums, conversions and LDS reads, which two waves a SIMD overlap
+// in part. 2 x 1024 new tokens over 16384, 40 query heads, bf16: 720 to 845 us,
+// 0.79 to 0.92 PFLOP/s (a large product reaches 1.55); 16 trees of 24 over 4000 in
+// int8 50 us. Tried: wave priorities around the products (no change), V operands
+// fetched before the exponentials (none), LDS addresses kept in registers (a
+// quarter slower: the registers they take are spilled inside the loop).
 template <typename T, int FMT, int DB, int R, bool FULL>
 __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_kernel(AttnParams p) {
   using TY = Types<T, FMT>;
