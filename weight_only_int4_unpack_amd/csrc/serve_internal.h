@@ -110,9 +110,9 @@ inline int attn_dim_block(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 
 // 32, the waves of a workgroup share the rows and take turns at the tokens;
 // above, each wave has 16 or 32 rows and they share the tokens through LDS.
 // Measured at the borders (us, chosen / other): 32 rows, 64 trees over 4000 e4m3
-// tokens 96 / 130 by the kernel of 64, 16 over int8 30 / 38, 16 over bf16 48 / 41;
+// tokens 82 / 130 by the kernel of 64, 16 over int8 30 / 38, 16 over bf16 47 / 41;
 // 56 rows, 16 trees over bf16 44 / 90 by the kernel of 32, 52 by that of 128; 96
-// rows, 16 trees over int8 53 / 65 by that of 64, 2048 rows and more 229 / 301.
+// rows, 16 trees over int8 53 / 65 by that of 64, 2048 rows and more 213 / 301.
 enum class AttnKind { kNarrow1, kNarrow2, kWide1, kWide2 };
 inline AttnKind attn_kind(int64_t rows, int dim) {
   if (rows <= 16) return AttnKind::kNarrow1;

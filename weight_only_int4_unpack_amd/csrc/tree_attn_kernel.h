@@ -98,6 +98,22 @@ struct Item {
   int first;                     // index of this group's split 0 among the items
 };
 
+// Sums over the lanes up to each one, without LDS: four steps inside rows of 16
+// lanes, then the last lane of the first and third row, and of the second, added
+// to the rows after it. Lanes that a step does not reach add 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lane_step(int x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int sum_upto(int x) {
+  x = lane_step<0x111, 0xF>(x);           // row_shr 1, 2, 4, 8
+  x = lane_step<0x112, 0xF>(x);
+  x = lane_step<0x114, 0xF>(x);
+  x = lane_step<0x118, 0xF>(x);
+  x = lane_step<0x142, 0xA>(x);           // row_bcast 15, 31
+  return lane_step<0x143, 0xC>(x);
+}
+
 // Finds work item `index`: every wave scans the sequences, 64 at a time, each
 // lane one, twice over (the total sets the chunk length, then the item counts
 // are summed up to the item). Lengths live on the device, so that a captured
@@ -126,9 +142,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
     load(b0 + lane, &len, &news, &start, &blocks);
     steps += (uint32_t)blocks * (uint32_t)((len + kAttnStep - 1) / kAttnStep);
   }
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) steps += (uint32_t)__shfl_xor((int)steps, s);
-  steps = (uint32_t)__builtin_amdgcn_readfirstlane((int)steps);
+  steps = (uint32_t)__builtin_amdgcn_readlane(sum_upto((int)steps), 63);
   uint32_t per = 0x7FFFFFFF / kAttnStep;   // steps of a split
   if (p.target > 0) {
     const uint32_t work = steps * (uint32_t)p.cache.heads;
@@ -143,13 +157,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
     if (p.target > 0) own = max(own, (mine + kAttnMaxSplits - 1) / kAttnMaxSplits);
     const int splits = max((int)((mine + own - 1) / own), 1);
     const int groups = blocks * p.cache.heads, items = groups * splits;
-    int upto = items, gupto = groups;
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const int a = __shfl_up(upto, s), g = __shfl_up(gupto, s);
-      upto += lane >= s ? a : 0;
-      gupto += lane >= s ? g : 0;
-    }
+    const int upto = sum_upto(items), gupto = sum_upto(groups);
     const uint64_t past = __ballot(items_before + upto > index);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
@@ -461,7 +469,13 @@ struct Rows {
     }
 
     // ---- O^T
-    if (!TREE || !apart) {
+    // kRare: told that this is rare, the compiler spills there and not in the token loop
+    // (512 tokens over 8192 e4m3 126 us, else 165; 64 trees of 6 over 4000 e4m3 82, else
+    // 97), but for the narrow kernels of 16-bit caches (16 trees of 4 over 4000 40, with
+    // it 51).
+    constexpr bool kRare = ROWS16 || !TY::kSame;
+    const bool usual = !TREE || !apart;
+    if (kRare ? __builtin_expect(usual, 1) : usual) {
 #pragma unroll
       for (int j = 0; j < kVD; ++j) {
         const u32x4 a = v_op(j);
@@ -715,19 +729,18 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // Bound by HBM where there is enough to read: 64 sequences of up to 8192 tokens,
 // 8 heads of 128 in e4m3, 118 us (4.7 TB/s; a copy reaches 5.2); 32 such in bf16
 // 109 us (5.1 TB/s). With little to read the chain of launch, item search, a
-// few tiles, parts and their join: 4099 tokens of one sequence 12 us, of which
+// few tiles, parts and their join: 4099 tokens of one sequence 11.9 us, of which
 // the bytes are 3.
 //
 // Without TREE (one new token per sequence and no mask) the kernel needs no
 // masks but the length's, and its registers leave room for three waves per
 // SIMD instead of two (16 rows, up to 128 dims).
 //
-// With TREE, 32 rows of 128 dims and values that may be infinite or NaN, two waves
-// a SIMD would spill in the token loop: one wave with twice the registers takes 30
-// instead of 38 us (8 tokens of one sequence over 16384, bf16), 36 instead of 43 (16
-// over 4000, e4m3); int8, which does not spill, keeps two (30 us against 39).
+// With TREE, 32 rows of 128 dims and a 16-bit cache, two waves a SIMD would spill in
+// the token loop: one wave with twice the registers takes 30 instead of 38 us (8
+// tokens of one sequence over 16384, bf16), 49 instead of 65 (16 trees over 4000).
 constexpr int narrow_waves(int fmt, int db, int r, bool tree) {
-  return !tree && r * db <= 128 ? 3 : tree && r * db == 256 && fmt != W4A16_KV_INT8 ? 1 : 2;
+  return !tree && r * db <= 128 ? 3 : tree && r * db == 256 && fmt == W4A16_KV_SAME ? 1 : 2;
 }
 template <typename T, int FMT, int DB, int R, bool FULL, bool TREE>
 __global__ __launch_bounds__(64 * kAttnWaves, narrow_waves(FMT, DB, R, TREE)) void attn_narrow_kernel(
@@ -917,7 +930,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, narrow_waves(FMT, DB, R, TREE)) vo
   const int whole = min(range.see_all, it.len);
   while (n + kAttnWaves < tiles && range.begin + (n + 1) * kAttnTile <= whole && ok[0] && ok[1])
     tile(std::false_type{});
-  while (n < tiles) tile(std::true_type{});
+  while (kSame ? n < tiles : __builtin_expect(n < tiles, 0)) tile(std::true_type{});
 
   // ---- join the four waves, a row block at a time
   constexpr int kH = DB / 64, kPart = (int)attn_part_floats(kRows, DB);
@@ -1013,8 +1026,8 @@ __device__ __forceinline__ u32x2 read_transposed(Lds at) {
 // Bound by issue: at 32 rows a wave, 64 tokens take 64 products (1024 cycles of
 // the matrix core) and about as long again in exponentials (32 x 16 cycles),
 // multiply-adds, sums, conversions and LDS reads, which two waves a SIMD overlap
-// in part. 2 x 1024 new tokens over 16384, 40 query heads, bf16: 720 to 845 us,
-// 0.79 to 0.92 PFLOP/s (a large product reaches 1.55); 16 trees of 24 over 4000 in
+// in part. 2 x 1024 new tokens over 16384, 40 query heads, bf16: 720 to 825 us,
+// 0.81 to 0.92 PFLOP/s (a large product reaches 1.55); 16 trees of 24 over 4000 in
 // int8 50 us. Tried: wave priorities around the products (no change), V operands
 // fetched before the exponentials (none), LDS addresses kept in registers (a
 // quarter slower: the registers they take are spilled inside the loop).
@@ -1190,7 +1203,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
   const int whole = min(range.see_all, it.len);
   while (n + 1 < stages && range.begin + (n + 1) * kAttnStage <= whole && held[0] && held[1] && held[2] && held[3])
     pass(std::false_type{});
-  while (n < stages) pass(std::true_type{});
+  while (__builtin_expect(n < stages, 0)) pass(std::true_type{});
 
   // ---- a wave's rows are its own: through its part of the LDS (for whole rows
   // at a time) to the output, or to the part
