@@ -292,7 +292,7 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
   int kept = 0;                          // keys in the wave's list
   uint64_t bound = 0;                    // keys below it are not among the k largest
   float x[kPerLane], most[kVecs];
-  // Logit e of this lane's 32 of a tile: its index, and whether it is one of the part.
+  // Index of this lane's logit e of a tile.
   auto index_of = [&](int tile, int e) { return first_of(tile, e / R::kVec) + e % R::kVec; };
 
   auto stream = [&] {                    // x into most and sum
