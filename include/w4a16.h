@@ -484,7 +484,7 @@ typedef struct {
   const uint64_t* mask;      /* [tokens, mask_words], or NULL */
   int64_t tokens;
   int64_t q_token, q_head;   /* strides, multiples of 8 */
-  int64_t table_stride;      /* of block_table */
+  int64_t table_stride;      /* of block_table's rows: table_pages or more, or 0: one row for all */
   int32_t sequences;
   int32_t table_pages;
   int32_t max_q;             /* most new tokens of a sequence; rows past it are not computed */

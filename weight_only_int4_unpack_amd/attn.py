@@ -297,7 +297,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     holds sequence b's new tokens in rows ``q_starts[b]:q_starts[b + 1]``
     (int32 ``[sequences + 1]``; at most ``max_q`` each); its ``kv_lens[b]``
     (int32) cached tokens, the new ones last, lie in the pages
-    ``block_table[b]`` (int32 ``[sequences, pages]``).
+    ``block_table[b]`` (int32 ``[sequences, pages]``; one row may be expanded
+    to all sequences).
 
     New token i sees everything before the new ones and, of the new ones, j <= i
     or, with ``mask`` (int64 ``[tokens, words]``), those whose bit j % 64 of word
@@ -320,6 +321,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     bs, b1 = block_table.stride()
     if b1 != 1 and pages > 1:
         raise ValueError("block_table: the last dimension must be contiguous")
+    if B <= 1:
+        bs = pages                          # no other row to go to
     lens = _array(kv_lens, "kv_lens", torch.int32, dev, B)
     starts = _array(q_starts, "q_starts", torch.int32, dev, B + 1)
     mp = words = 0
@@ -342,7 +345,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     ws = _W.stream_workspace(dev, need)
     _call(_W.lib().w4a16_tree_attention, dev,
           _ATTEND.pack(*fields, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                       block_table.data_ptr(), lens, starts, mp, T, qt, qh, max(bs, pages), B, pages,
+                       block_table.data_ptr(), lens, starts, mp, T, qt, qh, bs, B, pages,
                        max_q, H, words, code, scale, 0), _W._ptr(ws), need)
     return out, lse
 

@@ -421,8 +421,9 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
   AttnShape s;
   CHECK(attn_shape(a->sequences, a->max_q, a->q_heads, view.heads, view.dim, 256, &s));
   CHECK(check_count(a->tokens, a->q_heads));
-  if (a->table_pages < 0 || a->table_stride < a->table_pages || a->table_stride >= kMaxStride)
-    return report(W4A16_ERR_SHAPE, "need 0 <= table_pages <= table_stride (got %d, %lld)",
+  if (a->table_pages < 0 || a->table_stride < 0 || a->table_stride >= kMaxStride ||
+      (a->table_stride < a->table_pages && a->table_stride != 0))
+    return report(W4A16_ERR_SHAPE, "need 0 <= table_pages <= table_stride, or a stride of 0 (got %d, %lld)",
                   (int)a->table_pages, (long long)a->table_stride);
   // 32-bit counts of work: row blocks times steps of 128 tokens, over all heads
   const int64_t capacity = std::min<int64_t>((int64_t)a->table_pages * a->cache.page_size, kMaxInt - 1);
