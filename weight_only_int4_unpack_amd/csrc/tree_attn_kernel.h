@@ -401,7 +401,16 @@ struct Rows {
     };
     bool rise = false;
     float high[R];
-    if constexpr (!TY::kSame) rise = largest(v_of(0), v_of(1)) > vref;
+    if constexpr (!TY::kSame) {
+      // one by one: the largest of them would be NaN where one is, and a finite one
+      // beside it, which another row sees, would raise nothing
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 x = v_of(u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rise |= x[i] > vref;
+      }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       high[r] = largest(s[r][0], s[r][1]) * factor[r];
