@@ -487,7 +487,8 @@ typedef struct {
   int64_t table_stride;      /* of block_table's rows: table_pages or more, or 0: one row for all */
   int32_t sequences;
   int32_t table_pages;
-  int32_t max_q;             /* most new tokens of a sequence; rows past it are not computed */
+  int32_t max_q;             /* most new tokens of a sequence; rows past it are not computed (the
+                                others are, as they would be with a larger max_q) */
   int32_t q_heads;           /* a multiple of cache.heads: query head h reads head h / (q_heads / heads) */
   int32_t mask_words;
   int32_t dtype;             /* of q, out, and of a SAME cache */

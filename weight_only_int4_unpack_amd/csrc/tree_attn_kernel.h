@@ -93,7 +93,8 @@ struct Item {
   int splits;                    // of this sequence
   int blocks;                    // row blocks of this sequence
   int chunk;                     // tokens of a split
-  int len, news, start;          // cached tokens, new tokens, first row in q
+  int len, prefix;               // cached tokens, and those before the new ones (may be negative)
+  int news, start;               // new tokens that are computed (max_q at most), first row in q
   int group;                     // counter: (sequence, block, head)
   int first;                     // index of this group's split 0 among the items
 };
@@ -124,22 +125,23 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   const int lane = threadIdx.x & 63;
   const int most = p.cache.pages > 0 ? min((int64_t)p.table_pages << p.cache.page_shift,
                                            (int64_t)0x7FFFFF00) : 0;
-  auto load = [&](int b, int* len, int* news, int* start, int* blocks) {
-    *len = *news = *start = *blocks = 0;
+  auto load = [&](int b, int* len, int* prefix, int* news, int* start, int* blocks) {
+    *len = *prefix = *news = *start = *blocks = 0;
     if (b < p.sequences) {
       *len = min(max(p.kv_lens[b], 0), most);
       const int s0 = min(max(p.q_starts[b], 0), p.tokens);
       const int s1 = min(max(p.q_starts[b + 1], s0), p.tokens);
       *start = s0;
+      *prefix = *len - (s1 - s0);
       *news = min(s1 - s0, p.max_q);
       *blocks = (*news * p.group + ROWS - 1) / ROWS;
     }
   };
-  int len, news, start, blocks;
+  int len, prefix, news, start, blocks;
   uint32_t steps = 0;
   const bool one_round = p.sequences <= 64;
   for (int b0 = 0; b0 < p.sequences; b0 += 64) {
-    load(b0 + lane, &len, &news, &start, &blocks);
+    load(b0 + lane, &len, &prefix, &news, &start, &blocks);
     steps += (uint32_t)blocks * (uint32_t)((len + kAttnStep - 1) / kAttnStep);
   }
   steps = (uint32_t)__builtin_amdgcn_readlane(sum_upto((int)steps), 63);
@@ -151,7 +153,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   }
   int items_before = 0, groups_before = 0;
   for (int b0 = 0; b0 < p.sequences; b0 += 64) {
-    if (!one_round) load(b0 + lane, &len, &news, &start, &blocks);
+    if (!one_round) load(b0 + lane, &len, &prefix, &news, &start, &blocks);
     const uint32_t mine = (uint32_t)(len + kAttnStep - 1) / kAttnStep;
     uint32_t own = per;
     if (p.target > 0) own = max(own, (mine + kAttnMaxSplits - 1) / kAttnMaxSplits);
@@ -168,6 +170,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
       it->blocks = of(blocks);
       it->chunk = min(of((int)own), 0x7FFFFF00 / kAttnStep) * kAttnStep;
       it->len = of(len);
+      it->prefix = of(prefix);
       it->news = of(news);
       it->start = of(start);
       const int local = index - (items_before + of(upto - items));
@@ -268,14 +271,15 @@ struct Rows {
   float held_most[R];                     // log2 of the scores' factor x scale that reaches kHeldMost
   int start, prefix, len;
 
-  // `row0`: the wave's first row. `dim_of(s)`: dims of contraction step s.
+  // `row0`: the wave's first row. `stop`: no row sees tokens from there on. `dim_of(s)`:
+  // dims of contraction step s.
   template <typename DimOf>
-  __device__ __forceinline__ void init(const AttnParams& p, const Item& it, int row0, int dim,
+  __device__ __forceinline__ void init(const AttnParams& p, const Item& it, int row0, int stop, int dim,
                                        DimOf dim_of) {
     const int c = threadIdx.x & 15;
     start = it.start;
-    prefix = it.len - it.news;            // may be negative
-    len = it.len;
+    prefix = it.prefix;
+    len = stop;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       unit[r] = kMostUnit;
@@ -350,7 +354,7 @@ struct Rows {
   // One tile of 32 tokens from t0. k_op(u, i): operand of half tile u and step
   // i; k_scale(u), v_scale(u): scales of this lane's 4 tokens; after(): called
   // once the K operands are consumed; v_op(j): operand of O^T's tile j. EDGE: some
-  // token may be unseen by some row; without TREE no token is unseen that exists.
+  // token may be unseen by some row; without TREE none is unseen before `len`.
   // exists[u]: half tile u lies on a page. v_edge(in): lets the caller clear V of
   // tokens that do not exist (bit 4u + i of `in`: this lane's token does) and say
   // (uniform) whether V holds an infinity or NaN.
@@ -561,18 +565,18 @@ struct Rows {
   }
 };
 
-// Tokens [begin, end) of an item, and the first that some row of it may not see.
+// Tokens [begin, end) of an item, the first that some row of it may not see, and the
+// first from which on none sees any.
 struct Range {
-  int begin, end, see_all;
+  int begin, end, see_all, stop;
 };
 __device__ __forceinline__ Range range_of(const AttnParams& p, const Item& it, int row0, int rows) {
-  const int prefix = it.len - it.news;
   const int last = (min(row0 + rows, it.news * p.group) - 1) / p.group;
-  const int block_end = p.mask ? it.len : min(it.len, prefix + last + 1);
   Range r;
-  r.see_all = p.mask ? prefix : prefix + row0 / p.group + 1;
+  r.see_all = p.mask ? it.prefix : it.prefix + row0 / p.group + 1;
+  r.stop = max(p.mask ? it.len : min(it.len, it.prefix + last + 1), 0);
   r.begin = it.split * it.chunk;
-  r.end = (int)min((int64_t)r.begin + it.chunk, (int64_t)max(block_end, 0));
+  r.end = (int)min((int64_t)r.begin + it.chunk, (int64_t)r.stop);
   return r;
 }
 
@@ -752,7 +756,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // few tiles, parts and their join: 4099 tokens of one sequence 11.9 us, of which
 // the bytes are 3.
 //
-// Without TREE (one new token per sequence and no mask) the kernel needs no
+// Without TREE (one row of new tokens per sequence and no mask) the kernel needs no
 // masks but the length's, and its registers leave room for three waves per
 // SIMD instead of two (16 rows, up to 128 dims).
 //
@@ -865,7 +869,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, narrow_waves(FMT, DB, R, TREE)) vo
     load_v();
   }
   Rows<T, FMT, DB, R, false> rw;
-  rw.init(p, it, row0, dim, [&](int s) {
+  rw.init(p, it, row0, range.stop, dim, [&](int s) {
     return kSame ? 32 * s + 8 * g : 64 * (s / 2) + 16 * g + 8 * (s & 1);
   });
 
@@ -1156,7 +1160,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
     load(0);
   }
   Rows<T, FMT, DB, R, true> rw;
-  rw.init(p, it, row0 + wave * kWaveRows, dim, [&](int s) { return 32 * s + 8 * g; });
+  rw.init(p, it, row0 + wave * kWaveRows, range.stop, dim, [&](int s) { return 32 * s + 8 * g; });
   rw.settle();
   bool held[4] = {false, false, false, false};  // pages of the stage in LDS
   if (stages > 0) {
