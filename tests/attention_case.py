@@ -35,7 +35,8 @@ class Strict(Case):
         v, s = self.values(b, t)
         (v if s is None else s).mul_(by)
 
-    def check(self, out, lse, parents=None, rows=None, which=None):
+    def check(self, out, lse, rows=None, which=None, held=None):
+        """`held`: only the first so many cached tokens of a sequence are anywhere."""
         eps16 = torch.finfo(self.dtype).eps / 2
         quantised = self.fmt != "16"
         epsp = 2.0 ** -11 if quantised else eps16
@@ -48,6 +49,7 @@ class Strict(Case):
             if n == 0 or (which is not None and b not in which):
                 continue
             see = S.tree_visible(length, n, None if rows is None else rows[b])
+            see[:, held:] &= held is None
             k, v = self.dense(b)
             for i in range(n):
                 t = np.flatnonzero(see[i])

@@ -54,3 +54,16 @@ def test_more_new_tokens_than_max_q(max_q, news, fmt, dtype):
     trees = random_trees(news, 5)
     mask = attn.tree_mask(trees)
     c.check_first(*c.run(mask=mask), rows=([ancestors(t) for t in trees], mask))
+
+
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+@pytest.mark.parametrize("news", [[1, 1], [5, 3], [20, 12], [40, 70]])
+def test_more_cached_tokens_than_the_table_holds(news, fmt, dtype):
+    # what lies past the table's last page is seen by none; the new ones stay where they are,
+    # the last of all: with 48 of 100 tokens on pages, every new token sees all 48
+    say("short table", news, fmt, dtype)
+    c = Strict([100, 90], news, 4, 2, 64, fmt, dtype, 16, seed=42)
+    c.table = c.table[:, :3].contiguous()
+    c.check(*c.run(), held=48)
+    trees = random_trees(news, 6)
+    c.check(*c.run(mask=attn.tree_mask(trees)), rows=[ancestors(t) for t in trees], held=48)

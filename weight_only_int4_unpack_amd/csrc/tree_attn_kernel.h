@@ -93,7 +93,8 @@ struct Item {
   int splits;                    // of this sequence
   int blocks;                    // row blocks of this sequence
   int chunk;                     // tokens of a split
-  int len, prefix;               // cached tokens, and those before the new ones (may be negative)
+  int len, prefix;               // tokens on pages of the table, and those of them that are before
+                                 // the new ones (negative: some new ones are before the first)
   int news, start;               // new tokens that are computed (max_q at most), first row in q
   int group;                     // counter: (sequence, block, head)
   int first;                     // index of this group's split 0 among the items
@@ -128,11 +129,12 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int index, Item* 
   auto load = [&](int b, int* len, int* prefix, int* news, int* start, int* blocks) {
     *len = *prefix = *news = *start = *blocks = 0;
     if (b < p.sequences) {
-      *len = min(max(p.kv_lens[b], 0), most);
+      const int whole = max(p.kv_lens[b], 0);
+      *len = min(whole, most);
       const int s0 = min(max(p.q_starts[b], 0), p.tokens);
       const int s1 = min(max(p.q_starts[b + 1], s0), p.tokens);
       *start = s0;
-      *prefix = *len - (s1 - s0);
+      *prefix = min(whole - (s1 - s0), *len);
       *news = min(s1 - s0, p.max_q);
       *blocks = (*news * p.group + ROWS - 1) / ROWS;
     }
