@@ -273,7 +273,8 @@ struct Rows {
   float held_most[R];                     // log2 of the scores' factor x scale that reaches kHeldMost
   int start, prefix, len;
 
-  // `row0`: the wave's first row. `stop`: no row sees tokens from there on. `dim_of(s)`:
+  // `row0`: the wave's first row. `stop`: no token from there on exists or (without a mask
+  // of its own, as sees() is one) is seen by a row. `dim_of(s)`:
   // dims of contraction step s.
   template <typename DimOf>
   __device__ __forceinline__ void init(const AttnParams& p, const Item& it, int row0, int stop, int dim,
@@ -450,10 +451,7 @@ struct Rows {
         total[r] *= f;
         float held = f;
         if constexpr (!TY::kSame) {       // the reference sinks with the old weights
-          const float old = over_power(unit[r]) * f;
-          float ref = ref_of(r);
-          held_most[r] = ref;
-          asm("" : "+v"(ref));            // the weights below are formed anew, not taken from here
+          const float old = over_power(unit[r]) * f, ref = ref_of(r);
           float most = 0.0f;              // the largest finite product
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -467,8 +465,10 @@ struct Rows {
           const float sunk = fmaxf(power_of(old), 1.0f / kMostUnit);
           const float to = most > sunk * kHeldMost ? power_of(most) * (1.0f / kHeldLeast) : sunk;
           unit[r] = over_power(to);
+          // (opaque: what the compiler knows of it made it copy all sums on the common path)
+          asm("" : "+v"(unit[r]));
           held = old * unit[r];
-          held_most[r] += __builtin_amdgcn_logf(to * kHeldMost);
+          held_most[r] = ref + __builtin_amdgcn_logf(to * kHeldMost);
         }
 #pragma unroll
         for (int j = 0; j < kVD; ++j) acc[r][j] *= held;
@@ -871,7 +871,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, narrow_waves(FMT, DB, R, TREE)) vo
     load_v();
   }
   Rows<T, FMT, DB, R, false> rw;
-  rw.init(p, it, row0, range.stop, dim, [&](int s) {
+  rw.init(p, it, row0, TREE ? it.len : range.stop, dim, [&](int s) {
     return kSame ? 32 * s + 8 * g : 64 * (s / 2) + 16 * g + 8 * (s & 1);
   });
 
@@ -1162,7 +1162,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, DB == 256 ? 1 : 2) void attn_wide_
     load(0);
   }
   Rows<T, FMT, DB, R, true> rw;
-  rw.init(p, it, row0 + wave * kWaveRows, range.stop, dim, [&](int s) { return 32 * s + 8 * g; });
+  rw.init(p, it, row0 + wave * kWaveRows, it.len, dim, [&](int s) { return 32 * s + 8 * g; });
   rw.settle();
   bool held[4] = {false, false, false, false};  // pages of the stage in LDS
   if (stages > 0) {
