@@ -13,6 +13,9 @@ namespace {
 
 constexpr int64_t kMaxInt = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+// CUs of a device that is not partitioned. Sizes are checked for it before there is a
+// device to ask; scratch, once there is one, for that device's own.
+constexpr int kWholeDevice = 256;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -407,7 +410,7 @@ w4a16_status w4a16_tree_attention_workspace_bytes(int32_t sequences, int32_t max
   if (!bytes) return report(W4A16_ERR_NULL, "bytes must be non-NULL");
   CHECK(check_dim(head_dim));
   AttnShape s;
-  CHECK(attn_shape(sequences, max_q, q_heads, kv_heads, head_dim, num_cus > 0 ? num_cus : 256, &s));
+  CHECK(attn_shape(sequences, max_q, q_heads, kv_heads, head_dim, num_cus > 0 ? num_cus : kWholeDevice, &s));
   *bytes = s.workspace;
   return W4A16_OK;
 }
@@ -419,7 +422,7 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
   KvView view;
   CHECK(check_cache(a->cache, &view));
   AttnShape s;
-  CHECK(attn_shape(a->sequences, a->max_q, a->q_heads, view.heads, view.dim, 256, &s));
+  CHECK(attn_shape(a->sequences, a->max_q, a->q_heads, view.heads, view.dim, kWholeDevice, &s));
   CHECK(check_count(a->tokens, a->q_heads));
   if (a->table_pages < 0 || a->table_stride < 0 || a->table_stride >= kMaxStride ||
       (a->table_stride < a->table_pages && a->table_stride != 0))
@@ -444,13 +447,11 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
       !aligned(a->mask, 8))
     return report(W4A16_ERR_ALIGN, "q and out must be 16-byte aligned, the rest to its elements");
   CHECK(check_strides("q", a->q_token, a->q_head));
+  int cus = kWholeDevice;
+  const w4a16_status device = current_device(&cus);
+  CHECK(attn_shape(a->sequences, a->max_q, a->q_heads, view.heads, view.dim, cus, &s));
   CHECK(check_workspace(workspace, ws_bytes, s.workspace));
-  int cus;
-  CHECK(current_device(&cus));
-  if (cus != 256) {
-    CHECK(attn_shape(a->sequences, a->max_q, a->q_heads, view.heads, view.dim, cus, &s));
-    CHECK(check_workspace(workspace, ws_bytes, s.workspace));
-  }
+  if (device != W4A16_OK) return device;
   AttnParams p{};
   p.cache = view;
   p.q = (const uint16_t*)a->q;
@@ -487,7 +488,7 @@ w4a16_status w4a16_tree_attention(const w4a16_tree_attention_t* a, void* workspa
 w4a16_status w4a16_token_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int32_t top_k,
                                                   int32_t num_cus, int64_t* bytes) {
   if (!bytes) return report(W4A16_ERR_NULL, "bytes must be non-NULL");
-  return score_workspace(tokens, vocab, top_k, num_cus > 0 ? num_cus : 256, bytes);
+  return score_workspace(tokens, vocab, top_k, num_cus > 0 ? num_cus : kWholeDevice, bytes);
 }
 
 w4a16_status w4a16_token_logprobs(const w4a16_token_logprobs_t* a, void* workspace,
@@ -499,7 +500,7 @@ w4a16_status w4a16_token_logprobs(const w4a16_token_logprobs_t* a, void* workspa
                     (int)a->dtype);
   }
   int64_t need;
-  CHECK(score_workspace(a->tokens, a->vocab, a->top_k, 256, &need));
+  CHECK(score_workspace(a->tokens, a->vocab, a->top_k, kWholeDevice, &need));
   if (a->tokens == 0) return W4A16_OK;
   if (a->row_stride < 0 || a->row_stride >= kMaxStride)
     return report(W4A16_ERR_SHAPE, "row_stride must lie in 0..2^40");
@@ -510,13 +511,11 @@ w4a16_status w4a16_token_logprobs(const w4a16_token_logprobs_t* a, void* workspa
       !aligned(a->logprobs, 4) || !aligned(a->entropy, 4) || !aligned(a->top_logprobs, 4) ||
       !aligned(a->top_ids, 8))
     return report(W4A16_ERR_ALIGN, "arrays must be aligned to their elements");
+  int cus = kWholeDevice;
+  const w4a16_status device = current_device(&cus);
+  CHECK(score_workspace(a->tokens, a->vocab, a->top_k, cus, &need));
   CHECK(check_workspace(workspace, ws_bytes, need));
-  int cus;
-  CHECK(current_device(&cus));
-  if (cus != 256) {
-    CHECK(score_workspace(a->tokens, a->vocab, a->top_k, cus, &need));
-    CHECK(check_workspace(workspace, ws_bytes, need));
-  }
+  if (device != W4A16_OK) return device;
   ScoreParams p{};
   p.logits = a->logits;
   p.ids = a->ids;
