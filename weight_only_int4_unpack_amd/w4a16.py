@@ -194,7 +194,8 @@ def stream_workspace(dev: torch.device, nbytes: int) -> torch.Tensor | None:
         return None
     if torch.cuda.is_current_stream_capturing():
         return _zero_counters(torch.empty(nbytes, dtype=torch.uint8, device=dev))
-    key = (dev.index, torch._C._cuda_getCurrentRawStream(dev.index))
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
         size = max(nbytes, 2 * (0 if ws is None else ws.numel()))
