@@ -405,7 +405,8 @@ w4a16_status w4a16_rope_table(const double* inv_freq, int32_t rot_dim, double am
  * dims from r on unchanged; fp32 arithmetic, one rounding to the dtype. */
 typedef struct {
   const void* x;            /* [tokens, heads, head_dim], 16-byte aligned */
-  void* out;                /* the same shape; x itself is allowed (then with x's strides) */
+  void* out;                /* the same shape, no head in another's place; x itself is allowed (then
+                               with x's strides) */
   const int64_t* positions; /* [tokens]; outside 0..table_rows-1: rotated dims become NaN */
   const float* table;       /* [table_rows, rot_dim], 16-byte aligned */
   int64_t tokens;
@@ -431,7 +432,7 @@ typedef struct {
   const void* v;
   const int64_t* slots;     /* [tokens]; outside 0..pages*page_size-1 (e.g. -1): not written */
   const void* q;            /* [tokens, q_heads, head_dim] rotated into q_out, or NULL */
-  void* q_out;              /* q itself is allowed (then with q's strides) */
+  void* q_out;              /* as w4a16_rope's out */
   const int64_t* positions; /* [tokens], or NULL: nothing is rotated */
   const float* table;       /* as for w4a16_rope */
   int64_t tokens;

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "serve_internal.h"
 
@@ -43,6 +44,21 @@ w4a16_status check_strides(const char* what, int64_t token, int64_t head) {
   if (token < 0 || head < 0 || token >= kMaxStride || head >= kMaxStride)
     return report(W4A16_ERR_SHAPE, "%s: strides (%lld, %lld) must lie in 0..2^40", what,
                   (long long)token, (long long)head);
+  return W4A16_OK;
+}
+
+// An output's heads may lie in any order, but not one in another.
+w4a16_status check_apart(const char* what, int64_t tokens, int64_t token, int64_t heads, int64_t head,
+                         int64_t dim) {
+  if (heads < 1) return W4A16_OK;
+  int64_t inner = head, n = heads, outer = token, m = tokens;
+  if (heads == 1 || (tokens > 1 && token < head)) {
+    std::swap(inner, outer);
+    std::swap(n, m);
+  }
+  if ((n > 1 && inner < dim) || (m > 1 && (outer < dim || (outer - dim) / inner < n - 1)))
+    return report(W4A16_ERR_SHAPE, "%s: heads of %lld dims overlap at strides (%lld, %lld)", what,
+                  (long long)dim, (long long)token, (long long)head);
   return W4A16_OK;
 }
 
@@ -300,6 +316,7 @@ w4a16_status w4a16_rope(const w4a16_rope_t* a, void* stream) {
     return report(W4A16_ERR_ALIGN, "x and out must be 16-byte aligned");
   CHECK(check_strides("x", a->x_token, a->x_head));
   CHECK(check_strides("out", a->out_token, a->out_head));
+  CHECK(check_apart("out", a->tokens, a->out_token, a->heads, a->out_head, a->head_dim));
   if (a->x == a->out && (a->x_token != a->out_token || a->x_head != a->out_head))
     return report(W4A16_ERR_SHAPE, "in place, out needs x's strides");
   int cus;
@@ -343,6 +360,7 @@ w4a16_status w4a16_kv_write(const w4a16_kv_write_t* a, void* stream) {
   if (a->q) {
     CHECK(check_strides("q", a->q_token, a->q_head));
     CHECK(check_strides("q_out", a->out_token, a->out_head));
+    CHECK(check_apart("q_out", a->tokens, a->out_token, hq, a->out_head, a->cache.head_dim));
     if (a->q == a->q_out && (a->q_token != a->out_token || a->q_head != a->out_head))
       return report(W4A16_ERR_SHAPE, "in place, q_out needs q's strides");
   }
