@@ -331,6 +331,8 @@ w4a16_status w4a16_unpack_int4_kshuffle(const int32_t* packed, int64_t N,
  * value in those arrays makes a kernel read or write outside the buffers
  * that the struct names; each call says what it does with such values.
  * Strides count elements. The last dimension of every array is contiguous.
+ * A launch holds fewer than 2^32 threads: calls of some 2^27 heads (2^24 rows of
+ * logits) and more are refused with SHAPE.
  * ======================================================================== */
 
 /* How a cache holds its values. */

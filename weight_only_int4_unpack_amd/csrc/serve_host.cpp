@@ -14,6 +14,10 @@ namespace {
 
 constexpr int64_t kMaxInt = (int64_t)1 << 31;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+// All kernels here run workgroups of 256 threads, and a grid holds fewer than 2^32 threads.
+constexpr int kServeThreads = 256;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 32) / kServeThreads - 1;
+static_assert(kScoreThreads == kServeThreads && 64 * kAttnWaves == kServeThreads, "one limit for all");
 // CUs of a device that is not partitioned. Sizes are checked for it before there is a
 // device to ask; scratch, once there is one, for that device's own.
 constexpr int kWholeDevice = 256;
@@ -113,10 +117,14 @@ w4a16_status check_rotation(const int64_t* positions, const float* table, int64_
 
 // Heads that one lane group takes in turn: `most`, or fewer where that would
 // leave less than 4096 waves (16 a CU).
-void shape_units(int64_t tokens, int64_t heads, int dim, int most, int32_t* per_unit, int32_t* units) {
+w4a16_status shape_units(int64_t tokens, int64_t heads, int dim, int most, int32_t* per_unit, int32_t* units) {
   const int64_t waves = tokens * heads * lanes_per_head(dim) / 64;
   *per_unit = (int32_t)std::min<int64_t>({std::max<int64_t>(waves / 4096, 1), most, heads});
   *units = (int32_t)div_up(heads, *per_unit);
+  if (div_up(tokens * *units, kServeThreads / lanes_per_head(dim)) > kMaxGrid)
+    return report(W4A16_ERR_SHAPE, "%lld tokens of %lld heads are too many for one launch", (long long)tokens,
+                  (long long)heads);
+  return W4A16_OK;
 }
 
 w4a16_status check_count(int64_t tokens, int64_t heads) {
@@ -143,8 +151,8 @@ int32_t score_splits(int64_t tokens, int64_t vocab, int num_cus, int32_t* part) 
 
 w4a16_status score_workspace(int64_t tokens, int64_t vocab, int32_t top_k, int num_cus,
                              int64_t* bytes) {
-  if (tokens < 0 || tokens >= kMaxInt / kScoreMaxSplits || vocab < 1 || vocab > kMaxInt / 2)
-    return report(W4A16_ERR_SHAPE, "need 0 <= tokens < 2^25 and 1 <= vocab <= 2^30");
+  if (tokens < 0 || tokens > kMaxGrid || vocab < 1 || vocab > kMaxInt / 2)
+    return report(W4A16_ERR_SHAPE, "need 0 <= tokens < 2^24 and 1 <= vocab <= 2^30");
   if (top_k < 0 || top_k > kScoreMaxTop || top_k > vocab)
     return report(W4A16_ERR_SHAPE, "top_k=%d must lie in 0..%d and not exceed the vocabulary",
                   (int)top_k, kScoreMaxTop);
@@ -207,7 +215,7 @@ w4a16_status attn_shape(int64_t sequences, int64_t max_q, int64_t q_heads, int64
   s->few = narrow ? num_cus : s->target;
   if (groups > kAttnMaxSplitGroups || (groups + s->target) * part > kAttnMaxParts) s->target = 0;
   s->grid = groups + s->target;
-  if (s->grid >= kMaxInt)
+  if (s->grid > kMaxGrid)
     return report(W4A16_ERR_SHAPE, "too many sequences, tokens and heads for one launch");
   s->workspace =
       s->target > 0 ? kCounterBytes + s->grid * part
@@ -319,9 +327,10 @@ w4a16_status w4a16_rope(const w4a16_rope_t* a, void* stream) {
   CHECK(check_apart("out", a->tokens, a->out_token, a->heads, a->out_head, a->head_dim));
   if (a->x == a->out && (a->x_token != a->out_token || a->x_head != a->out_head))
     return report(W4A16_ERR_SHAPE, "in place, out needs x's strides");
+  RopeKvParams p{};
+  CHECK(shape_units(a->tokens, a->heads, a->head_dim, kRopeUnit, &p.per_unit, &p.units_per_token));
   int cus;
   CHECK(current_device(&cus));
-  RopeKvParams p{};
   p.q = (const uint16_t*)a->x;
   p.q_out = (uint16_t*)a->out;
   p.positions = a->positions;
@@ -337,7 +346,6 @@ w4a16_status w4a16_rope(const w4a16_rope_t* a, void* stream) {
   p.rot = a->rot_dim;
   p.interleaved = a->interleaved != 0;
   p.inverse = a->inverse != 0;
-  shape_units(a->tokens, a->heads, p.dim, kRopeUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_rope_kv(p, a->dtype, W4A16_KV_SAME, (hipStream_t)stream));
 }
 
@@ -368,9 +376,11 @@ w4a16_status w4a16_kv_write(const w4a16_kv_write_t* a, void* stream) {
     CHECK(check_rotation(a->positions, a->table, a->table_rows, a->rot_dim, a->cache.head_dim));
   else if (a->q)
     return report(W4A16_ERR_NULL, "q is given to be rotated: positions and a table are needed");
+  RopeKvParams p{};
+  CHECK(shape_units(a->tokens, (int64_t)hq + 2 * view.heads, view.dim, kRopeUnit, &p.per_unit,
+                    &p.units_per_token));
   int cus;
   CHECK(current_device(&cus));
-  RopeKvParams p{};
   p.q = (const uint16_t*)a->q;
   p.k = (const uint16_t*)a->k;
   p.v = (const uint16_t*)a->v;
@@ -394,7 +404,6 @@ w4a16_status w4a16_kv_write(const w4a16_kv_write_t* a, void* stream) {
   p.dim = a->cache.head_dim;
   p.rot = a->rot_dim;
   p.interleaved = a->interleaved != 0;
-  shape_units(a->tokens, (int64_t)hq + 2 * p.hkv, p.dim, kRopeUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_rope_kv(p, a->dtype, a->cache.format, (hipStream_t)stream));
 }
 
@@ -409,15 +418,15 @@ w4a16_status w4a16_kv_read(const w4a16_kv_read_t* a, void* stream) {
     return report(W4A16_ERR_NULL, "slots, k_out and v_out must be non-NULL");
   if (!aligned(a->k_out, 16) || !aligned(a->v_out, 16) || !aligned(a->slots, 8))
     return report(W4A16_ERR_ALIGN, "k_out and v_out must be 16-byte aligned, slots 8-byte");
+  KvReadParams p{};
+  CHECK(shape_units(a->tokens, 2 * (int64_t)view.heads, view.dim, kReadUnit, &p.per_unit, &p.units_per_token));
   int cus;
   CHECK(current_device(&cus));
-  KvReadParams p{};
   p.cache = view;
   p.slots = a->slots;
   p.k_out = (uint16_t*)a->k_out;
   p.v_out = (uint16_t*)a->v_out;
   p.tokens = (int32_t)a->tokens;
-  shape_units(a->tokens, 2 * (int64_t)view.heads, view.dim, kReadUnit, &p.per_unit, &p.units_per_token);
   return launched(launch_kv_read(p, a->dtype, a->cache.format, (hipStream_t)stream));
 }
 
