@@ -1026,7 +1026,8 @@ typedef __attribute__((address_space(3))) char* Lds;
 
 // 16 bytes per lane from base + the lane's offset straight into LDS, lane after
 // lane from `to` (uniform). The compiler does not count it: drain() before the
-// barrier after which the data are read.
+// barrier after which the data are read. (m0 is the compiler's own: it cannot be
+// declared as overwritten, and no other instruction of the library names it.)
 __device__ __forceinline__ void copy16(const void* base, uint32_t offset, Lds to) {
   const uint32_t lds = (uint32_t)(uintptr_t)to;
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
