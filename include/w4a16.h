@@ -554,8 +554,8 @@ typedef struct {
  *   log probabilities and indices.
  * fp32 throughout. A row that holds NaN or +infinity, or -infinity alone, has
  * no softmax: its log probabilities and entropy are NaN (its top_ids are
- * still top_k different indices, NaN ordered as -infinity); a logit above
- * 2^127 counts as +infinity.
+ * still top_k different indices, NaN ordered as -infinity). A log probability
+ * that fp32 cannot hold is -infinity.
  * Scratch: as for w4a16_tree_attention, of at least
  * w4a16_token_logprobs_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.

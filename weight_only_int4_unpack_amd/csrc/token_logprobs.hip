@@ -4,9 +4,8 @@
 // A row is cut into `splits` parts, one workgroup each, whose four waves read
 // tiles in turn, 64 bytes a lane, the next tile's loads on their way. Each lane
 // keeps its own running reference m, s = sum e^(x - m) and t = sum e^(x - m) (x - m)
-// in fp32 (in base 2: y = x log2 e - m is one multiply-add, and the same rounded m
-// is taken off everywhere, so it cancels). From the joined sums
-//   log2 p_id = y_id - log2 s,   entropy = ln s - ln 2 t / s
+// in fp32 (e^ and t in base 2). From the joined sums
+//   ln p_id = x_id - m - ln s,   entropy = ln s - ln 2 t / s
 // (differences to m: no cancellation against a large maximum).
 //
 // Alternatives are ordered by one unsigned 64-bit key: the logit as an
@@ -19,7 +18,7 @@
 // tile costs one comparison a vector, and few logits of it pass.
 //
 // What bounds it: the stream alone (top_k = 0) runs at 4.1 to 5.1 TB/s, near a
-// copy's 5.2; about 9 instructions a logit keep pace with that. Selection adds
+// copy's 5.2; about 10 instructions a logit keep pace with that. Selection adds
 // a fixed chain of some 15 000 cycles per workgroup, of which every step
 // waits for the one before (bound, list, meeting, hand-off, order), and all
 // workgroups stand at the same place of it: 256 rows x 151667 bf16 take 19 us
@@ -51,14 +50,20 @@ __device__ __forceinline__ float value_of(uint64_t key) {
   return __builtin_bit_cast(float, u);
 }
 
-// m in units of log2.
+// log2 of e^(x - m). The difference first: x log2 e is past fp32's range for a logit masked
+// by the lowest finite value, and a row may hold nothing else. (One multiply-add of x and
+// of m log2 e instead: 256 rows x 151667 bf16 21.5 us instead of 22.5, with 20
+// alternatives 35.1 instead of 35.9, and NaN for such a row.)
+__device__ __forceinline__ float log2_of(float x, float m) { return (x - m) * kLog2e; }
+
+// m a logit; t in units of log2.
 struct Sums {
   float m, s, t;
 };
 // m = -inf stands for "nothing yet": its s and t are 0 (or NaN, which stays).
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
   const float m = fmaxf(a.m, b.m);
-  const float da = a.m == -kInf ? 0.0f : a.m - m, db = b.m == -kInf ? 0.0f : b.m - m;
+  const float da = a.m == -kInf ? 0.0f : log2_of(a.m, m), db = b.m == -kInf ? 0.0f : log2_of(b.m, m);
   const float fa = __builtin_amdgcn_exp2f(da), fb = __builtin_amdgcn_exp2f(db);
   // 2^d d is 0 where 2^d is: the clamp keeps 0 * inf out
   const float ca = fmaxf(da, -1e4f), cb = fmaxf(db, -1e4f);
@@ -306,11 +311,11 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
         most[v] = __builtin_elementwise_maximum(most[v], x[v * R::kVec + e]);
       top = __builtin_elementwise_maximum(top, most[v]);
     }
-    if (top * kLog2e > sum.m) sum = join(sum, Sums{top * kLog2e, 0.0f, 0.0f});
+    if (top > sum.m) sum = join(sum, Sums{top, 0.0f, 0.0f});
     const float ref = sum.m == -kInf ? 0.0f : sum.m;
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
-      const float d = fmaf(x[e], kLog2e, -ref);
+      const float d = log2_of(x[e], ref);
       const float w = __builtin_amdgcn_exp2f(d);
       sum.s += w;
       sum.t = fmaf(w, fmaxf(d, -1e4f), sum.t);
@@ -535,7 +540,7 @@ __global__ __launch_bounds__(kScoreThreads, 4) void score_kernel(ScoreParams p) 
 
   // All -inf: no softmax (m = -inf would otherwise give log 0).
   const float log_s = sum.m == -kInf ? __builtin_nanf("") : __log2f(sum.s);
-  auto log_of = [&](float x) { return kLn2 * (fmaf(x, kLog2e, -sum.m) - log_s); };
+  auto log_of = [&](float x) { return (x - sum.m) - kLn2 * log_s; };
   if (tid == 0) {
     p.logprobs[row] = known ? log_of(x_id) : __builtin_nanf("");
     p.entropy[row] = kLn2 * (log_s - sum.t / sum.s);
