@@ -35,8 +35,9 @@ class Strict(Case):
         v, s = self.values(b, t)
         (v if s is None else s).mul_(by)
 
-    def check(self, out, lse, rows=None, which=None, held=None):
-        """`held`: only the first so many cached tokens of a sequence are anywhere."""
+    def check(self, out, lse, rows=None, which=None, held=None, but=()):
+        """`held`: only the first so many cached tokens of a sequence are anywhere. `but`: new
+        tokens that are not looked at."""
         eps16 = torch.finfo(self.dtype).eps / 2
         quantised = self.fmt != "16"
         epsp = 2.0 ** -11 if quantised else eps16
@@ -51,7 +52,7 @@ class Strict(Case):
             see = S.tree_visible(length, n, None if rows is None else rows[b])
             see[:, held:] &= held is None
             k, v = self.dense(b)
-            for i in range(n):
+            for i in set(range(n)) - set(but):
                 t = np.flatnonzero(see[i])
                 for h in range(self.hq):
                     what = (b, i, h)
