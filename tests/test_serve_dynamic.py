@@ -7,7 +7,6 @@ from torch.fx.experimental.proxy_tensor import make_fx
 from weight_only_int4_unpack_amd import attn, serve_op
 
 
-
 def inputs(tokens, sequences, pages, device, dtype=torch.int8, top=100):
     g = torch.Generator().manual_seed(tokens)
     rand = lambda *s: torch.randn(s, generator=g).bfloat16().to(device)      # noqa: E731

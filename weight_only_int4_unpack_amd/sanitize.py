@@ -4,7 +4,7 @@ Builds ``libw4a16_asan.so`` from ``csrc/w4a16_host.cpp`` and ``csrc/serve_host.c
 (argument checks, route/tile selector, workspace bookkeeping, host pack/unpack) with g++ under
 AddressSanitizer and UndefinedBehaviorSanitizer (every finding fatal), linked
 against host-only stand-ins for the kernels (``csrc/sanitize_stubs.cpp``),
-then runs ``tests/test_abi.py`` and ``tests/test_serve_abi.py`` with that library in place of the real one
+then runs the C-ABI tests (``TESTS``) with that library in place of the real one
 (``W4A16_LIB``) and the sanitizer runtimes preloaded into Python. CPU only:
 no GPU code is built or run.
 
@@ -22,6 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libw4a16_asan.so")
 ROCM = "/opt/rocm"
+TESTS = ("test_abi.py", "test_serve_abi.py", "test_attention_tables.py", "test_serve_limits.py",
+         "test_serve_outputs.py")
 
 
 def build() -> str:
@@ -52,9 +54,8 @@ def main() -> int:
     env["UBSAN_OPTIONS"] = "halt_on_error=1:print_stacktrace=1"
     env["CUDA_VISIBLE_DEVICES"] = ""
     env["HIP_VISIBLE_DEVICES"] = ""
-    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider",
-                        os.path.join(ROOT, "tests", "test_abi.py"),
-                        os.path.join(ROOT, "tests", "test_serve_abi.py")], cwd=ROOT, env=env)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-m", "not gpu",
+                        *(os.path.join(ROOT, "tests", t) for t in TESTS)], cwd=ROOT, env=env)
     return r.returncode
 
 
