@@ -434,7 +434,7 @@ typedef struct {
   const void* v;
   const int64_t* slots;     /* [tokens]; outside 0..pages*page_size-1 (e.g. -1): not written */
   const void* q;            /* [tokens, q_heads, head_dim] rotated into q_out, or NULL */
-  void* q_out;              /* as w4a16_rope's out */
+  void* q_out;              /* as w4a16_rope's out, and apart from k and v */
   const int64_t* positions; /* [tokens], or NULL: nothing is rotated */
   const float* table;       /* as for w4a16_rope */
   int64_t tokens;
@@ -452,8 +452,9 @@ typedef struct {
  * and head, scale = amax / top (top = 448 or 127, amax the largest magnitude
  * of the rotated fp32 head) and code = round-to-even(x * (top / amax)). A
  * head with amax < 2^-100 is stored as scale 0 and codes 0; a head that
- * holds an infinity or NaN as scale NaN and codes 0. Of two tokens with one
- * slot either may stay.
+ * holds an infinity or NaN as scale NaN and codes 0. Two tokens with one slot
+ * leave there a mixture (one's codes with the other's scale): a slot that
+ * several padded tokens share is one that nothing reads.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, DEVICE, HIP.
  */
 w4a16_status w4a16_kv_write(const w4a16_kv_write_t* args, void* stream);
@@ -513,7 +514,8 @@ typedef struct {
  * outside 0..pages-1 are seen by none. Lengths below 0 count as 0.
  * Scores, softmax statistics and sums are fp32; the softmax weights are
  * rounded to 16 bits for the matrix cores (fp16 in front of 8-bit codes, with
- * V's scales in them; else the dtype).
+ * V's scales in them; else the dtype). In front of int8 keys bf16 queries are
+ * rounded to fp16, each row scaled by a power of two first.
  * Scratch: `workspace` as for w4a16_gemm_ws (counters first, zero before
  * first use), of at least w4a16_tree_attention_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, VALUE (scale), WORKSPACE, DEVICE, HIP.

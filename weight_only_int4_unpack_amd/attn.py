@@ -205,8 +205,8 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KVCac
              interleaved: bool = False, q: torch.Tensor | None = None,
              q_out: torch.Tensor | None = None) -> torch.Tensor | None:
     """Writes ``k`` and ``v`` ``[tokens, heads, head_dim]`` into the ``slots``
-    (int64 ``[tokens]``; a negative one is skipped) of ``cache``, quantised as
-    the cache is. With ``positions`` and ``table`` ``k`` is rotated first, and
+    (int64 ``[tokens]``, no two alike; a negative one is skipped) of ``cache``,
+    quantised as the cache is. With ``positions`` and ``table`` ``k`` is rotated first, and
     ``q`` ``[tokens, q_heads, head_dim]``, if given, is rotated into ``q_out``
     (returned; ``q_out=q`` in place), all in one pass."""
     code, kt, kh = _heads(k, "k")

@@ -178,7 +178,11 @@ struct AttnShape {
 // Work items aimed at for `groups` on a device that holds `slots` workgroups.
 // Few groups: as many as there are slots. More: whole rounds of slots cost
 // whole rounds of time, so each group is split in the 1 to 4 that leaves the
-// last round fullest (a split costs about 2 % in parts written and joined).
+// last round fullest, a split counted as 2 % (parts are written and joined).
+// Measured in 4, 2 and 1: 640 groups on 512 slots, 2 x 1024 tokens over 16384
+// bf16 715, 705 and 833 us, over int8 889, 908 and 1096; 1 x 2048 over 32768 1316,
+// 1357 and 1623. Where the groups are of different lengths the rounds are not what
+// this takes them for: 2 x 2048 tokens over themselves, e4m3, 227, 226 and 161.
 int64_t attn_target(int64_t groups, int64_t slots) {
   if (groups <= slots) return slots;
   int64_t best = 1;

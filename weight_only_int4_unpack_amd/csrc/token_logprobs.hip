@@ -17,12 +17,12 @@
 // the first tile, for a bound from all lists, and after the last; in between a
 // tile costs one comparison a vector, and few logits of it pass.
 //
-// What bounds it: the stream alone (top_k = 0) runs at 4.1 to 5.1 TB/s, near a
-// copy's 5.2; about 10 instructions a logit keep pace with that. Selection adds
+// What bounds it: the stream alone (top_k = 0) runs at 3.7 TB/s and more, a copy at
+// 5.2; its 10 instructions a logit are most of the difference. Selection adds
 // a fixed chain of some 15 000 cycles per workgroup, of which every step
 // waits for the one before (bound, list, meeting, hand-off, order), and all
-// workgroups stand at the same place of it: 256 rows x 151667 bf16 take 19 us
-// without alternatives and 33 us with 20 of them; 1 row 5 and 12 us.
+// workgroups stand at the same place of it: 256 rows x 151667 bf16 take 20.9 us
+// without alternatives and 33.5 us with 20 of them; 1 row 6 and 12 us.
 #include "serve_device.h"
 
 namespace w4a16 {

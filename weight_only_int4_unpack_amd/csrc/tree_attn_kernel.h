@@ -16,7 +16,8 @@
 // (lane (g, c): token c, 16 bytes at dim chunk g). V is read in rows too.
 //
 // 8-bit codes are widened exactly to 16 bits; a token's scales multiply its
-// scores and its weights, which are one value per lane and token.
+// scores and its weights, which are one value per lane and token. Weights times
+// scales are held between bounds of fp16 by a power of two of each row's own.
 //
 // Two kernels share this, by the rows of a group (new tokens x query heads of a
 // key/value head). Up to 32 rows (narrow): the four waves of a workgroup hold the
@@ -753,10 +754,12 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // c * DB/16 + j. A tile's loads are issued one tile ahead, its pages two.
 //
 // Bound by HBM where there is enough to read: 64 sequences of up to 8192 tokens,
-// 8 heads of 128 in e4m3, 118 us (4.7 TB/s; a copy reaches 5.2); 32 such in bf16
-// 109 us (5.1 TB/s). With little to read the chain of launch, item search, a
-// few tiles, parts and their join: 4099 tokens of one sequence 11.9 us, of which
-// the bytes are 3.
+// 8 heads of 128 in e4m3, 117 us (4.7 TB/s; a copy reaches 5.2); 32 such in bf16
+// 108 us (5.1 TB/s). With little to read the chain of launch, item search, a
+// few tiles, parts and their join: 4099 tokens of one sequence 11.7 us, of which
+// the bytes are 3, and 57 % of the waves' time is waits. Partial head dims above 128
+// over a 16-bit cache spill in the token loop: 32 sequences, 4 heads of 192, 142 us
+// (2.9 TB/s), of 256 117 us (4.7).
 //
 // Without TREE (one row of new tokens per sequence and no mask) the kernel needs no
 // masks but the length's, and its registers leave room for three waves per
@@ -765,6 +768,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Item& it, 
 // With TREE, 32 rows of 128 dims and a 16-bit cache, two waves a SIMD would spill in
 // the token loop: one wave with twice the registers takes 30 instead of 38 us (8
 // tokens of one sequence over 16384, bf16), 49 instead of 65 (16 trees over 4000).
+// 16 rows of 256 dims as well: 36 instead of 48, and 51 instead of 67.
 constexpr int narrow_waves(int fmt, int db, int r, bool tree) {
   return !tree && r * db <= 128 ? 3 : tree && r * db == 256 && fmt == W4A16_KV_SAME ? 1 : 2;
 }
@@ -1050,12 +1054,15 @@ __device__ __forceinline__ u32x2 read_transposed(Lds at) {
 // straight into LDS, 8-bit ones through registers, where they are widened. V lies
 // in rows, as K does, and is read transposed.
 //
-// Bound by issue: at 32 rows a wave, 64 tokens take 64 products (1024 cycles of
-// the matrix core) and about as long again in exponentials (32 x 16 cycles),
-// multiply-adds, sums, conversions and LDS reads, which two waves a SIMD overlap
-// in part. 2 x 1024 new tokens over 16384, 40 query heads, bf16: 720 to 825 us,
-// 0.81 to 0.92 PFLOP/s (a large product reaches 1.55); 16 trees of 24 over 4000 in
-// int8 50 us. Tried: wave priorities around the products (no change), V operands
+// At 32 rows a wave, 64 tokens take 64 products (1024 cycles of the matrix core) and
+// about as long again in exponentials (32 x 16 cycles), multiply-adds, sums,
+// conversions and LDS reads, which two waves a SIMD overlap in part. 2 x 1024 new
+// tokens over 16384, 40 query heads, bf16: 700 to 820 us, 0.81 to 0.95 PFLOP/s (a
+// large product reaches 1.57); the matrix core is busy 42 % of the time, vector
+// instructions issue 51 %. Short items wait more than they issue: 16 trees of 24 over
+// 4000 in int8 take 50 us with the matrix core busy 12 %, vector issue 39 %, and half
+// of the waves' time in waits (a first stage that nothing hides, few stages an item,
+// parts and their join). Tried: wave priorities around the products (no change), V operands
 // fetched before the exponentials (none), LDS addresses kept in registers (a
 // quarter slower: the registers they take are spilled inside the loop).
 template <typename T, int FMT, int DB, int R, bool FULL>
