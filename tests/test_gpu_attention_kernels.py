@@ -65,3 +65,26 @@ def test_siblings_that_are_not_finite(new, dim, fmt, dtype, value):
     c.check(out, lse, rows=rows, which=[1])
     c.check(out, lse, rows=rows, which=[0], but=hit)
     assert hit and not bool(torch.isfinite(out[hit]).all(-1).any())
+
+
+@pytest.mark.parametrize("news", [(1, 1), (10, 15), (20, 32), (40, 70)])
+@pytest.mark.parametrize("fmt", ["16", "e4m3"])
+def test_captured_with_eager_work_between(fmt, news):
+    # every kernel in a graph on its first use in it, replayed as the cache changes
+    say("captured", fmt, news)
+    c = Strict([333, 130], list(news), 4, 2, 128, fmt, torch.bfloat16, 32, seed=55)
+    k, v = (torch.randn((2, 2, 128), device="cuda").bfloat16() for _ in range(2))
+    slots = torch.stack([c.slots[0][5], c.slots[1][-1]])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.kv_write(k, v, slots, c.cache)
+        out, lse = c.run()
+    for seed in range(3):
+        for x in (k, v):
+            x.copy_(torch.randn((2, 2, 128), device="cuda"))
+        graph.replay()
+        want = c.run()                          # eager, on the same stream
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        c.check(out, lse)
