@@ -569,6 +569,217 @@ w4a16_status w4a16_token_logprobs(const w4a16_token_logprobs_t* args, void* work
 w4a16_status w4a16_token_logprobs_workspace_bytes(int64_t tokens, int64_t vocab, int32_t top_k,
                                                   int32_t num_cus, int64_t* bytes);
 
+/* ==========================================================================
+ * For a batch of requests: verification of drafted tokens, pages of the cache
+ * (shared, copied, given back), adapters beside a shared product.
+ * The conventions are those of the section above.
+ * ======================================================================== */
+
+typedef struct {
+  const void* logits;          /* [tokens, vocab], aligned to its elements; row i: what follows token i */
+  const int64_t* ids;          /* [tokens]; outside 0..vocab-1: never accepted */
+  const int32_t* q_starts;     /* [sequences + 1]: sequence b has rows q_starts[b]..q_starts[b+1]-1, its
+                                  nodes 0, 1, ...; node 0 is the token chosen last, the others are drafted */
+  const int32_t* parents;      /* [tokens]: the node that a node follows, a smaller number (else it is never
+                                  reached; node 0's is not read); or NULL: each follows the one before */
+  const float* draft_probs;    /* [tokens, vocab], or NULL: row i is the distribution that the token after
+                                  token i was drawn from; only without parents */
+  const float* temperatures;   /* [sequences], or NULL: 1; 0 (or anything that is not above 0): greedy */
+  const float* uniforms;       /* [tokens], in [0, 1): for accepting a node (node 0's is not used) */
+  const float* final_uniforms; /* [sequences], in [0, 1): for the last token */
+  int64_t* out_tokens;         /* [sequences, max_q]: the accepted tokens, then the one drawn, then -1 */
+  int32_t* path;               /* [sequences, max_q]: node 0, the accepted nodes, then -1 */
+  int32_t* counts;             /* [sequences]: how many of each (0 for a sequence without rows) */
+  int64_t tokens;
+  int64_t row_stride;          /* of logits */
+  int64_t probs_stride;        /* of draft_probs */
+  int64_t vocab;               /* 1..2^20 */
+  int32_t sequences;
+  int32_t max_q;               /* 0..1024: most nodes of a sequence; nodes past it are as if not drafted */
+  int32_t dtype;               /* of logits: w4a16_dtype, or W4A16_F32 */
+  int32_t reserved;            /* 0 */
+} w4a16_verify_drafts_t;
+
+/*
+ * w4a16_verify_drafts - how far each sequence's drafted tokens are accepted,
+ * and the token after them, so that what comes out is distributed as if
+ * drawn token by token from the model. With w_i(t) = exp((x_i(t) - max x_i) /
+ * temperature) for row x_i of node i (greedy: 1 at the first largest logit, 0
+ * elsewhere) and S_i its sum, from node 0:
+ *  - the nodes c that follow i are tried in order; the first accepted is next.
+ *    Given tokens (no draft_probs): c is accepted if
+ *      uniform_c (S_i - R) < w_i(id_c),   R = w_i's sum over the tokens rejected at i,
+ *    and is rejected if its token was already. Drawn tokens (draft_probs q):
+ *      uniform_c q_i(id_c) S_i < w_i(id_c).
+ *  - where none is, the last token is drawn: the first t with
+ *      sum_{j <= t} r(j) > final_uniform sum r,
+ *    r = w_i without the tokens rejected at i, or, where a drawn token was
+ *    rejected, max(w_i / S_i - q_i, 0); where r is 0 everywhere, r = w_i.
+ * A row that holds NaN or +infinity, or -infinity alone, has no softmax: what
+ * follows it is not accepted, and its sequence's last token is -1. Sums and
+ * weights are fp64: of the 2^17 borders that a draw falls between, fp32 sums
+ * (off by 1e-7) move one under one draw in a hundred.
+ * Scratch: as for w4a16_tree_attention, of at least
+ * w4a16_verify_drafts_workspace_bytes.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.
+ */
+w4a16_status w4a16_verify_drafts(const w4a16_verify_drafts_t* args, void* workspace,
+                                 int64_t ws_bytes, void* stream);
+
+/* Scratch of w4a16_verify_drafts, with or without draft_probs (host only; num_cus as for
+ * w4a16_workspace_bytes). Errors: NULL, SHAPE, DTYPE. */
+w4a16_status w4a16_verify_drafts_workspace_bytes(int64_t tokens, int64_t vocab, int32_t sequences,
+                                                 int32_t max_q, int32_t dtype, int32_t num_cus,
+                                                 int64_t* bytes);
+
+/* Who holds the pages of a cache (or of a model's caches, which share one
+ * table): refs[p] is the number of sequences whose table names page p, 0 for a
+ * free page. Sequence r has lens[r] tokens, in the first ceil(lens[r] /
+ * page_size) pages of its row; entries behind those are -1. All of it lies on
+ * the device and is kept by the calls below, which take one workgroup each. */
+typedef struct {
+  int32_t* refs;            /* [pages] */
+  int32_t* block_table;     /* [rows, table_pages] */
+  int32_t* lens;            /* [rows] */
+  int64_t pages;            /* 0..2^30 */
+  int64_t table_stride;     /* of block_table's rows: table_pages or more */
+  int32_t rows;
+  int32_t table_pages;
+  int32_t page_size;        /* a power of two, 16..4096 */
+  int32_t reserved;         /* 0 */
+} w4a16_page_pool_t;
+
+typedef struct {
+  w4a16_page_pool_t pool;
+  const int32_t* from;      /* [count]: resize: the rows; fork: the parents' rows */
+  const int32_t* to;        /* [count]: resize: their new lengths; fork: the children's rows */
+  int32_t* served;          /* [count]: 1, or 0: this one changed nothing */
+  int32_t* src;             /* [count]: a page to be copied ... */
+  int32_t* dst;             /* ... to this one (w4a16_kv_copy_pages), or -1 and -1 */
+  int32_t count;            /* 0..4096 */
+  int32_t reserved;         /* 0 */
+} w4a16_pages_t;
+
+/*
+ * w4a16_pages_resize - gives listed rows pages for a new length, or takes back
+ * those behind it (a length of 0 frees a sequence). Pages that are taken back
+ * are free when no other row holds them. If the shorter of the old and the new
+ * length ends inside a page that other rows hold too, the row gets a page of
+ * its own in its place, to be copied: what is written next is seen by no one else.
+ * Pages are given out in the order of the list, the lowest that were free
+ * before the call first. Not served: a row outside the pool, a length below 0
+ * or above table_pages * page_size, a row that stands in the list before, and,
+ * from the first row for which the free pages do not suffice on, every row that
+ * needs some.
+ * Entries of the table outside 0..pages-1 count as no page.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_pages_resize(const w4a16_pages_t* args, void* stream);
+
+/*
+ * w4a16_pages_fork - children continue their parents' sequences: each child's
+ * row gets the parent's length, shares its full pages, and has a page of its
+ * own, to be copied, in place of a partly filled last one. Lengths are those
+ * before the call. Not served: rows outside the pool, a child that holds tokens
+ * already (or is its own parent), a child that stands in the list before,
+ * and, as for w4a16_pages_resize, those for which the free pages do not suffice.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_pages_fork(const w4a16_pages_t* args, void* stream);
+
+typedef struct {
+  const w4a16_kv_cache_t* caches; /* [count], host memory: alike in all but their addresses */
+  const int32_t* src;       /* [pairs] pages */
+  const int32_t* dst;       /* [pairs]; no page twice, and none that is in src */
+  int64_t pairs;
+  int32_t count;            /* 0..4096 */
+  int32_t reserved;         /* 0 */
+} w4a16_kv_copy_pages_t;
+
+/*
+ * w4a16_kv_copy_pages - page dst[i] of every cache becomes page src[i], scales
+ * included. A pair with a page outside the caches (such as -1) is skipped.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_kv_copy_pages(const w4a16_kv_copy_pages_t* args, void* stream);
+
+typedef struct {
+  const w4a16_kv_cache_t* caches; /* as above */
+  const int32_t* block_table; /* [sequences, table_pages], as for w4a16_tree_attention, but no two
+                                 sequences in one row */
+  const int32_t* kv_lens;   /* [sequences]: cached tokens, the new ones (the last) included */
+  const int32_t* q_starts;  /* [sequences + 1]: where each sequence's new tokens start */
+  const int32_t* path;      /* [sequences, width]: the new tokens to keep, ascending */
+  const int32_t* counts;    /* [sequences]: how many */
+  int32_t* new_lens;        /* [sequences], not kv_lens itself */
+  int64_t table_stride;
+  int32_t sequences;
+  int32_t table_pages;
+  int32_t width;
+  int32_t count;            /* of caches, 0..4096 */
+} w4a16_kv_compact_t;
+
+/*
+ * w4a16_kv_compact - keeps the tokens of an accepted path (w4a16_verify_drafts)
+ * and drops the other new ones: with n new tokens, the last of kv_lens[b], new
+ * token path[b][j] moves to place j of the new ones in every cache, codes and
+ * scales as they are, and new_lens[b] = kv_lens[b] - n + (tokens kept). A path
+ * ends where an entry is not above the one before, or not below n. Tokens in
+ * places that the table or the caches do not have are not moved; a sequence
+ * with n = 0 or n > kv_lens[b] keeps all.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_kv_compact(const w4a16_kv_compact_t* args, void* stream);
+
+/*
+ * w4a16_lora_plan - the tokens of a step in the order of their adapters, for
+ * any number of w4a16_lora calls with the same tokens and number of adapters.
+ * index: [tokens] device, the token's adapter; outside 0..adapters-1 (e.g. -1):
+ * none. plan: device, 16-byte aligned, w4a16_lora_plan_bytes of it; its
+ * contents are the library's own. tokens: 0..2^24, adapters: 1..1024.
+ * Errors: NULL, SHAPE, ALIGN, DEVICE, HIP.
+ */
+w4a16_status w4a16_lora_plan(const int32_t* index, int64_t tokens, int32_t adapters, void* plan,
+                             void* stream);
+
+/* Size of a plan (host only). Errors: NULL, SHAPE. */
+w4a16_status w4a16_lora_plan_bytes(int64_t tokens, int32_t adapters, int64_t* bytes);
+
+typedef struct {
+  const void* x;            /* [tokens, k], 16-byte aligned */
+  const void* a;            /* [adapters, rank, k], 16-byte aligned */
+  const void* b;            /* [adapters, n, rank], 16-byte aligned */
+  const void* base;         /* [tokens, n], 16-byte aligned, or NULL: 0 */
+  void* out;                /* [tokens, n], 16-byte aligned: base itself (then with its stride), or apart from
+                               all that is read */
+  const float* scales;      /* [adapters], or NULL: 1 */
+  const int32_t* ranks;     /* [adapters], or NULL: all of rank; rows of a and columns of b from an
+                               adapter's own rank on are not read into the sums */
+  const void* plan;         /* of w4a16_lora_plan, for these tokens and adapters */
+  int64_t tokens;
+  int64_t x_stride, base_stride, out_stride; /* of rows, multiples of 8 */
+  int32_t k, n;             /* multiples of 8, 8..2^24 and 8..2^22 */
+  int32_t adapters;         /* 1..1024 */
+  int32_t rank;             /* a multiple of 8, 8..128 */
+  int32_t dtype;            /* of x, a, b, base and out */
+  int32_t reserved;         /* 0 */
+} w4a16_lora_t;
+
+/*
+ * w4a16_lora - adds each token's adapter to the product that all share:
+ *   out[t] = base[t] + scales[i] sum_r v_r b[i, :, r],  v_r = sum_k x[t, k] a[i, r, k],
+ * i the token's adapter; without one, out[t] = base[t]. v and the sums are fp32
+ * (v meets b as two 16-bit parts, which hold 16 of its bits in bf16 and 22 in
+ * fp16), rounded once to the dtype.
+ * Scratch: a workspace as for w4a16_gemm_ws, of at least w4a16_lora_workspace_bytes.
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.
+ */
+w4a16_status w4a16_lora(const w4a16_lora_t* args, void* workspace, int64_t ws_bytes, void* stream);
+
+/* Scratch of w4a16_lora (host only; num_cus as for w4a16_workspace_bytes). Errors: NULL, SHAPE. */
+w4a16_status w4a16_lora_workspace_bytes(int64_t tokens, int32_t k, int32_t adapters, int32_t rank,
+                                        int32_t num_cus, int64_t* bytes);
+
 /*
  * Message of the calling thread's last failed call ("" if none): why the
  * problem was refused, as PR #43731's can_implement (Code section) returns

@@ -24,6 +24,7 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wall", "-Wno-unused-function"]
 SOURCES = ["w4a16_host.cpp", "w4a16_kernels.hip", "w4a16_noalloc.hip", "serve_host.cpp",
+           "batch_host.cpp", "verify_drafts.hip", "kv_pages.hip", "lora.hip",
            "rope_kv.hip", "token_logprobs.hip", "tree_attn_f16_same.hip", "tree_attn_f16_e4m3.hip",
            "tree_attn_f16_int8.hip", "tree_attn_bf16_same.hip", "tree_attn_bf16_e4m3.hip",
            "tree_attn_bf16_int8.hip"]

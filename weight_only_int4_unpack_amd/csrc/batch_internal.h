@@ -1,0 +1,159 @@
+// Internal interface between the host side (batch_host.cpp) and the gfx950 kernels of the
+// operators of a batch of requests: verification of drafts, pages of the cache, adapters.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "serve_internal.h"
+
+namespace w4a16 {
+
+// ---- verification of drafts
+constexpr int kVerifyThreads = 256;       // weighing: a chunk of logits a wave
+constexpr int kWalkThreads = 1024;        // walking and drawing
+constexpr int kVerifyMaxNodes = 1024;
+constexpr int64_t kVerifyMaxVocab = (int64_t)1 << 20;
+// Logits of a chunk: 4 vectors of 16 bytes a lane.
+__host__ __device__ constexpr int verify_chunk(int dtype) { return dtype == W4A16_F32 ? 1024 : 2048; }
+// Chunks of a row: they start at 16-byte boundaries of memory, so that the first may hold fewer.
+__host__ __device__ constexpr int verify_chunks(int64_t vocab, int dtype) {
+  return (int)((vocab + 7 + verify_chunk(dtype) - 1) / verify_chunk(dtype));
+}
+constexpr int kVerifyMaxChunks = verify_chunks(kVerifyMaxVocab, W4A16_F32);
+
+// What a wave knows of its chunk: weights' sum against the chunk's own largest logit m
+// (NaN: the chunk holds NaN), and where m stands first.
+struct VerifyChunk {
+  double s;
+  float m;
+  int32_t first;
+};
+
+struct VerifyParams {
+  const void* logits;
+  const int64_t* ids;
+  const int32_t* q_starts;
+  const int32_t* parents;
+  const float* probs;
+  const float* temperatures;
+  const float* uniforms;
+  const float* finals;
+  int64_t* out_tokens;
+  int32_t* path;
+  int32_t* counts;
+  int64_t row_stride, probs_stride;
+  VerifyChunk* parts;       // [tokens][chunks]
+  double* over;             // [sequences][chunks]: sums of max(p - q, 0) (groups > 1)
+  int32_t* counters;        // [sequences], zero between launches (groups > 1)
+  int32_t tokens, vocab, sequences, max_q;
+  int32_t chunks, groups;   // groups: workgroups of a sequence in the second kernel
+};
+
+// ---- pages
+constexpr int kPagesThreads = 1024;
+constexpr int kPagesMaxList = 4096;
+struct PagesParams {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* lens;
+  const int32_t* from;
+  const int32_t* to;
+  int32_t* served;
+  int32_t* src;
+  int32_t* dst;
+  int64_t table_stride;
+  int32_t pages, rows, table_pages, page_shift, count;
+};
+
+constexpr int kGroupCaches = 64;          // caches of one launch: their addresses are kernel arguments
+struct CacheAddresses {
+  char* k;
+  char* v;
+  char* k_scale;
+  char* v_scale;
+};
+struct CopyPagesParams {
+  CacheAddresses caches[kGroupCaches];
+  const int32_t* src;
+  const int32_t* dst;
+  int64_t pages;
+  uint32_t page_units, scale_units;       // 16-byte units of a page of k, and of its scales
+  uint32_t chunks;                        // workgroups of a pair and cache
+  int32_t count;
+  int64_t pairs;
+};
+constexpr int kCopyThreads = 256;
+constexpr int kCopyEach = 4;              // units of a thread
+
+struct CompactParams {
+  CacheAddresses caches[kGroupCaches];
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  const int32_t* path;
+  const int32_t* counts;
+  int32_t* new_lens;                      // null: not of this launch
+  int64_t table_stride, pages;
+  int32_t sequences, table_pages, width, count;
+  int32_t page_shift, heads;
+  int32_t row_units;                      // 16-byte units of a token's row of one head
+  int32_t scaled;
+  int32_t blocks;                         // workgroups of a sequence and cache
+};
+constexpr int kCompactThreads = 256;
+
+// ---- adapters
+constexpr int kLoraMaxAdapters = 1024;
+constexpr int kLoraMaxTokens = 1 << 24;
+constexpr int kLoraPlanThreads = 512;
+constexpr int kLoraThreads = 256;
+constexpr int kLoraMaxSplits = 16;
+// Rows of a tile: tokens of one adapter that are multiplied at a time.
+inline int lora_tile_rows(int64_t tokens, int64_t adapters) { return tokens >= 64 * adapters ? 64 : 16; }
+// Most tiles that a plan can hold; tokens without an adapter are a group of their own.
+inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
+  const int64_t rows = lora_tile_rows(tokens, adapters);
+  const int64_t most = (tokens + rows - 1) / rows + adapters;
+  return most < tokens ? most : tokens;
+}
+// Rank that the kernels are built for.
+__host__ __device__ constexpr int lora_rank_block(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+struct LoraTile {
+  int32_t adapter;          // -1: none
+  int32_t start, rows;      // in the plan's order of tokens
+  int32_t reserved;
+};
+struct LoraPlanParams {
+  const int32_t* index;
+  LoraTile* tiles;          // [max_tiles], those unused with rows = 0
+  int32_t* order;           // [tokens]
+  int32_t tokens, adapters, tile_rows, max_tiles;
+};
+struct LoraParams {
+  const uint16_t* x;
+  const uint16_t* a;
+  const uint16_t* b;
+  const uint16_t* base;
+  uint16_t* out;
+  const float* scales;
+  const int32_t* ranks;
+  const LoraTile* tiles;
+  const int32_t* order;
+  float* parts;             // [splits][tokens][rank block]
+  int64_t x_stride, base_stride, out_stride;
+  int32_t tokens, k, n, adapters, rank, tiles_most;
+  int32_t splits;           // of k over workgroups
+  int32_t steps;            // of 128 k that a split takes
+  int32_t columns;          // of n that a workgroup of the second kernel takes
+};
+
+hipError_t launch_verify(const VerifyParams& p, int dtype, hipStream_t stream);
+hipError_t launch_pages(const PagesParams& p, bool fork, hipStream_t stream);
+hipError_t launch_copy_pages(const CopyPagesParams& p, hipStream_t stream);
+hipError_t launch_compact(const CompactParams& p, hipStream_t stream);
+hipError_t launch_lora_plan(const LoraPlanParams& p, hipStream_t stream);
+hipError_t launch_lora(const LoraParams& p, int tile_rows, int dtype, hipStream_t stream);
+
+}  // namespace w4a16

@@ -1,7 +1,7 @@
 """Sanitizer build of the host side, and the C-ABI tests run against it.
 
-Builds ``libw4a16_asan.so`` from ``csrc/w4a16_host.cpp`` and ``csrc/serve_host.cpp``
-(argument checks, route/tile selector, workspace bookkeeping, host pack/unpack) with g++ under
+Builds ``libw4a16_asan.so`` from ``csrc/w4a16_host.cpp``, ``csrc/serve_host.cpp`` and
+``csrc/batch_host.cpp`` (argument checks, route/tile selector, workspace bookkeeping, host pack/unpack) with g++ under
 AddressSanitizer and UndefinedBehaviorSanitizer (every finding fatal), linked
 against host-only stand-ins for the kernels (``csrc/sanitize_stubs.cpp``),
 then runs the C-ABI tests (``TESTS``) with that library in place of the real one
@@ -23,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libw4a16_asan.so")
 ROCM = "/opt/rocm"
 TESTS = ("test_abi.py", "test_serve_abi.py", "test_attention_tables.py", "test_serve_limits.py",
-         "test_serve_outputs.py")
+         "test_serve_outputs.py", "test_batch_abi.py")
 
 
 def build() -> str:
@@ -31,6 +31,7 @@ def build() -> str:
            "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
            "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", f"-I{os.path.join(ROOT, 'include')}",
            os.path.join(CSRC, "w4a16_host.cpp"), os.path.join(CSRC, "serve_host.cpp"),
+           os.path.join(CSRC, "batch_host.cpp"),
            os.path.join(CSRC, "sanitize_stubs.cpp"),
            f"-L{ROCM}/lib", "-lamdhip64", f"-Wl,-rpath,{ROCM}/lib", "-o", OUT]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -95,13 +95,26 @@ def lib() -> ctypes.CDLL:
                                                        ctypes.POINTER(i64)]
     L.w4a16_token_logprobs.argtypes = [args, vp, i64, vp]
     L.w4a16_token_logprobs_workspace_bytes.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
+    L.w4a16_verify_drafts.argtypes = [args, vp, i64, vp]
+    L.w4a16_verify_drafts_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32, ctypes.POINTER(i64)]
+    L.w4a16_pages_resize.argtypes = [args, vp]
+    L.w4a16_pages_fork.argtypes = [args, vp]
+    L.w4a16_kv_copy_pages.argtypes = [args, vp]
+    L.w4a16_kv_compact.argtypes = [args, vp]
+    L.w4a16_lora_plan.argtypes = [vp, i64, i32, vp, vp]
+    L.w4a16_lora_plan_bytes.argtypes = [i64, i32, ctypes.POINTER(i64)]
+    L.w4a16_lora.argtypes = [args, vp, i64, vp]
+    L.w4a16_lora_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, ctypes.POINTER(i64)]
     for f in ("w4a16_gemm", "w4a16_gemm_bias", "w4a16_gemm_planned", "w4a16_gemm_ws",
               "w4a16_workspace_bytes", "w4a16_gemm_noalloc", "w4a16_plan", "w4a16_plan_route",
               "w4a16_dequant", "w4a16_pack_int4", "w4a16_unpack_int4", "w4a16_gemm_kpacked",
               "w4a16_pack_int4_kshuffle", "w4a16_unpack_int4_kshuffle",
               "w4a16_rope_frequencies", "w4a16_rope_table", "w4a16_rope", "w4a16_kv_write",
               "w4a16_kv_read", "w4a16_tree_attention", "w4a16_tree_attention_workspace_bytes",
-              "w4a16_token_logprobs", "w4a16_token_logprobs_workspace_bytes"):
+              "w4a16_token_logprobs", "w4a16_token_logprobs_workspace_bytes",
+              "w4a16_verify_drafts", "w4a16_verify_drafts_workspace_bytes", "w4a16_pages_resize",
+              "w4a16_pages_fork", "w4a16_kv_copy_pages", "w4a16_kv_compact", "w4a16_lora_plan",
+              "w4a16_lora_plan_bytes", "w4a16_lora", "w4a16_lora_workspace_bytes"):
         getattr(L, f).restype = ctypes.c_int
     L.w4a16_last_error.restype = ctypes.c_char_p
     L.w4a16_last_error.argtypes = []
