@@ -189,17 +189,18 @@ def test_null_arguments():
 
 
 def test_scratch_and_plan_sizes():
-    # counters, then 16 bytes a chunk and row, 8 a chunk and sequence; the chunks of a row may
+    # counters, then 16 bytes a chunk and row, 24 a chunk and sequence; the chunks of a row may
     # start up to 7 logits before it
-    assert scoring.verify_workspace_bytes(6, 2041, 2, 3, torch.bfloat16) == 65536 + 6 * 16 + 2 * 8
-    assert scoring.verify_workspace_bytes(6, 2042, 2, 3, torch.bfloat16) == 65536 + 2 * (6 * 16 + 2 * 8)
+    assert scoring.verify_workspace_bytes(6, 2041, 2, 3, torch.bfloat16) == 65536 + 6 * 16 + 2 * 24
+    assert scoring.verify_workspace_bytes(6, 2042, 2, 3, torch.bfloat16) == 65536 + 2 * (6 * 16 + 2 * 24)
     assert scoring.verify_workspace_bytes(0, 2042, 2, 3, torch.float32) == 0
-    # 16 bytes a tile and 4 a token
-    assert adapters.plan_bytes(1, 4) == 16 + 16 and adapters.plan_bytes(0, 4) == 0
-    assert adapters.plan_bytes(64, 32) == 16 * (4 + 32) + 256
-    assert adapters.workspace_bytes(1, 128, 4, 8) == 65536 + 16 * 4
-    # a range of k has at least one step of 128 for each of 4 waves
-    assert adapters.workspace_bytes(1, 1024, 4, 8) == 65536 + 2 * 16 * 4
+    # 4 bytes a tile, in whole 16, and 4 for each of its 16 or 64 rows
+    assert adapters.plan_bytes(1, 4) == 16 + 64 and adapters.plan_bytes(0, 4) == 0
+    assert adapters.plan_bytes(64, 32) == 4 * 36 + 4 * 16 * 36
+    assert adapters.plan_bytes(640, 2) == 48 + 4 * 64 * 12
+    # counters; for each of 16 rows 16 ranks in two parts and a factor, and 16 sums for each split
+    assert adapters.workspace_bytes(1, 128, 4, 8) == 65536 + 16 * (16 + 1) * 4
+    assert adapters.workspace_bytes(1, 5120, 4, 8) > 65536 + 16 * (2 * 16 + 16 + 1) * 4
     for bad in (dict(rank=7), dict(k=4), dict(tokens=-1), dict(adapters=0)):
         with pytest.raises(W.W4A16Error):
             adapters.workspace_bytes(**{**dict(tokens=1, k=128, adapters=4, rank=8), **bad})

@@ -213,14 +213,16 @@ def test_plan_keeps_the_order_of_tokens():
         data = plan.data.view(torch.int32).cpu().numpy()
         rows = 64 if T >= 64 * R else 16
         most = min(-(-T // rows) + R, T)
-        tiles, order = data[:4 * most].reshape(most, 4), data[4 * most:4 * most + T]
-        key = np.where((index < 0) | (index >= R), R, index)
-        assert np.array_equal(order, np.argsort(key, kind="stable"))
-        used = tiles[tiles[:, 2] > 0]
-        assert used[:, 2].sum() == T and used[:, 2].max() <= rows
-        assert np.array_equal(used[:, 1], np.concatenate([[0], np.cumsum(used[:, 2])[:-1]]))
-        for adapter, start, n, _ in used:
-            assert (key[order[start:start + n]] == (adapter if adapter >= 0 else R)).all()
+        at = -(-most // 4) * 4
+        tile, token = data[:most], data[at:].reshape(most, rows)
+        key = np.where((index < 0) | (index >= R), -1, index)
+        used = tile != -2
+        assert (token[~used] == -1).all()
+        order = token[used][token[used] >= 0]
+        assert np.array_equal(order, np.argsort(np.where(key < 0, R, key), kind="stable"))
+        for i, row in zip(tile[used], token[used]):
+            n = int((row >= 0).sum())
+            assert n > 0 and (row[n:] == -1).all() and (key[row[:n]] == i).all()
 
 
 def test_no_tokens():

@@ -15,8 +15,8 @@ using namespace checks;
 
 // ---- verification of drafts
 int32_t verify_groups(int64_t sequences, int chunks, int num_cus) {
-  // Workgroups of a sequence for the residual of drawn tokens: a chunk a wave, until
-  // the device is full; counters bound how many sequences may share one.
+  // Workgroups of a sequence that share the last row: a chunk a wave, while all of them are
+  // resident; counters bound how many sequences may have several.
   if (sequences > kCounterBytes / 4) return 1;
   const int64_t most = div_up(chunks, kWalkThreads / 64);
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, 2 * (int64_t)num_cus / std::max<int64_t>(sequences, 1)));
@@ -39,7 +39,7 @@ w4a16_status verify_workspace(int64_t tokens, int64_t vocab, int32_t sequences, 
   if (tokens > kMaxGrid * (kVerifyThreads / 64) / chunks)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %lld logits are too many for one launch", (long long)tokens,
                   (long long)vocab);
-  *bytes = tokens == 0 ? 0 : kCounterBytes + tokens * chunks * (int64_t)sizeof(VerifyChunk) + sequences * chunks * 8;
+  *bytes = tokens == 0 ? 0 : kCounterBytes + tokens * chunks * (int64_t)sizeof(VerifyChunk) + sequences * chunks * 24;
   return W4A16_OK;
 }
 
@@ -130,16 +130,17 @@ w4a16_status check_lora_counts(int64_t tokens, int32_t adapters) {
   return W4A16_OK;
 }
 
-constexpr int64_t kPlanAlign = 16;
-int64_t plan_order_at(int64_t tokens, int32_t adapters) {
-  return lora_max_tiles(tokens, adapters) * (int64_t)sizeof(LoraTile);
+// Where the tokens of a plan start.
+int64_t plan_tokens_at(int64_t tokens, int32_t adapters) {
+  return div_up(lora_max_tiles(tokens, adapters) * 4, 16) * 16;
 }
 
-// Splits of k over workgroups, each with at least a step for every wave: as many as make
-// two workgroups a CU.
+// Splits of k over workgroups: as many as make one a CU, each with a step for every wave.
 int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int num_cus, int32_t* steps) {
-  const int64_t all = div_up(k, 128), tiles = std::max<int64_t>(lora_max_tiles(tokens, adapters), 1);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)num_cus / tiles, all / 4, kLoraMaxSplits}));
+  const int64_t all = div_up(k, kLoraStep);
+  const int64_t tiles = std::max<int64_t>(div_up(tokens, lora_tile_rows(tokens, adapters)), 1);
+  const int64_t want = std::max<int64_t>(
+      1, std::min<int64_t>({num_cus / tiles, all * kLoraStep / (64 * (kLoraDownThreads / 64)), kLoraMaxSplits}));
   *steps = (int32_t)div_up(all, want);
   return (int32_t)div_up(all, *steps);
 }
@@ -152,9 +153,10 @@ w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t adapters, int32_t
   if (k < 8 || k > (1 << 24) || k % 8 != 0)
     return report(W4A16_ERR_SHAPE, "k=%d must be a multiple of 8 in 8..2^24", (int)k);
   int32_t steps;
-  *bytes = tokens == 0 ? 0
-                       : kCounterBytes + (int64_t)lora_splits(tokens, adapters, k, num_cus, &steps) * tokens *
-                                             lora_rank_block(rank) * 4;
+  const int64_t splits = lora_splits(tokens, adapters, k, num_cus, &steps);
+  // counters, the splits' sums, v's two parts and a factor for each row
+  const int64_t rows = lora_max_tiles(tokens, adapters) * lora_tile_rows(tokens, adapters);
+  *bytes = tokens == 0 ? 0 : kCounterBytes + rows * (((splits > 1 ? splits : 0) + 1) * lora_rank_block(rank) + 1) * 4;
   return W4A16_OK;
 }
 
@@ -220,7 +222,7 @@ w4a16_status w4a16_verify_drafts(const w4a16_verify_drafts_t* a, void* workspace
   p.sequences = a->sequences;
   p.max_q = a->max_q;
   p.chunks = verify_chunks(a->vocab, a->dtype);
-  p.groups = a->draft_probs && a->tokens > 0 ? verify_groups(a->sequences, p.chunks, cus) : 1;
+  p.groups = a->tokens > 0 ? verify_groups(a->sequences, p.chunks, cus) : 1;
   if (need > 0) {
     p.counters = (int32_t*)workspace;
     p.parts = (VerifyChunk*)((char*)workspace + kCounterBytes);
@@ -320,7 +322,7 @@ w4a16_status w4a16_kv_compact(const w4a16_kv_compact_t* a, void* stream) {
 w4a16_status w4a16_lora_plan_bytes(int64_t tokens, int32_t adapters, int64_t* bytes) {
   if (!bytes) return report(W4A16_ERR_NULL, "bytes must be non-NULL");
   CHECK(check_lora_counts(tokens, adapters));
-  *bytes = plan_order_at(tokens, adapters) + div_up(tokens * 4, kPlanAlign) * kPlanAlign;
+  *bytes = plan_tokens_at(tokens, adapters) + lora_max_tiles(tokens, adapters) * lora_tile_rows(tokens, adapters) * 4;
   return W4A16_OK;
 }
 
@@ -334,8 +336,8 @@ w4a16_status w4a16_lora_plan(const int32_t* index, int64_t tokens, int32_t adapt
   CHECK(current_device(&cus));
   LoraPlanParams p{};
   p.index = index;
-  p.tiles = (LoraTile*)plan;
-  p.order = (int32_t*)((char*)plan + plan_order_at(tokens, adapters));
+  p.tile = (int32_t*)plan;
+  p.token = (int32_t*)((char*)plan + plan_tokens_at(tokens, adapters));
   p.tokens = (int32_t)tokens;
   p.adapters = adapters;
   p.tile_rows = lora_tile_rows(tokens, adapters);
@@ -380,9 +382,8 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   p.out = (uint16_t*)a->out;
   p.scales = a->scales;
   p.ranks = a->ranks;
-  p.tiles = (const LoraTile*)a->plan;
-  p.order = (const int32_t*)((const char*)a->plan + plan_order_at(a->tokens, a->adapters));
-  p.parts = (float*)((char*)workspace + kCounterBytes);
+  p.tile = (const int32_t*)a->plan;
+  p.token = (const int32_t*)((const char*)a->plan + plan_tokens_at(a->tokens, a->adapters));
   p.x_stride = a->x_stride;
   p.base_stride = a->base_stride;
   p.out_stride = a->out_stride;
@@ -394,7 +395,15 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   p.tiles_most = (int32_t)lora_max_tiles(a->tokens, a->adapters);
   p.splits = lora_splits(a->tokens, a->adapters, a->k, cus, &p.steps);
   const int rows = lora_tile_rows(a->tokens, a->adapters);
-  p.columns = rows == 64 ? 1024 : 256;
+  const int64_t values = (int64_t)p.tiles_most * rows * lora_rank_block(a->rank);
+  p.counters = (int32_t*)workspace;
+  p.high = (uint16_t*)((char*)workspace + kCounterBytes);
+  p.low = p.high + values;
+  p.parts = (float*)(p.low + values);
+  p.factor = p.parts + (p.splits > 1 ? p.splits : 0) * values;
+  // columns of a workgroup of the second kernel: the 256 of a step until there are 2048 of them
+  const int64_t blocks = p.tiles_most * div_up(a->n, 256);
+  p.columns = (int32_t)(256 * std::min(div_up(blocks, 2048), div_up(a->n, 256)));
   if ((int64_t)p.tiles_most * div_up(a->n, p.columns) > kMaxGrid)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %d columns are too many for one launch", (long long)a->tokens,
                   (int)a->n);

@@ -11,7 +11,7 @@ namespace w4a16 {
 
 // ---- verification of drafts
 constexpr int kVerifyThreads = 256;       // weighing: a chunk of logits a wave
-constexpr int kWalkThreads = 1024;        // walking and drawing
+constexpr int kWalkThreads = 512;         // walking and drawing
 constexpr int kVerifyMaxNodes = 1024;
 constexpr int64_t kVerifyMaxVocab = (int64_t)1 << 20;
 // Logits of a chunk: 4 vectors of 16 bytes a lane.
@@ -20,10 +20,11 @@ __host__ __device__ constexpr int verify_chunk(int dtype) { return dtype == W4A1
 __host__ __device__ constexpr int verify_chunks(int64_t vocab, int dtype) {
   return (int)((vocab + 7 + verify_chunk(dtype) - 1) / verify_chunk(dtype));
 }
+
 constexpr int kVerifyMaxChunks = verify_chunks(kVerifyMaxVocab, W4A16_F32);
 
-// What a wave knows of its chunk: weights' sum against the chunk's own largest logit m
-// (NaN: the chunk holds NaN), and where m stands first.
+// What a wave knows of its chunk: the weights' sum, formed in fp32, against the chunk's own
+// largest logit m (NaN: the chunk holds NaN), and, greedy, where m stands first.
 struct VerifyChunk {
   double s;
   float m;
@@ -44,7 +45,7 @@ struct VerifyParams {
   int32_t* counts;
   int64_t row_stride, probs_stride;
   VerifyChunk* parts;       // [tokens][chunks]
-  double* over;             // [sequences][chunks]: sums of max(p - q, 0) (groups > 1)
+  double* over;             // [sequences][3][chunks]: fp64 sums of the last node's row
   int32_t* counters;        // [sequences], zero between launches (groups > 1)
   int32_t tokens, vocab, sequences, max_q;
   int32_t chunks, groups;   // groups: workgroups of a sequence in the second kernel
@@ -107,8 +108,10 @@ constexpr int kCompactThreads = 256;
 constexpr int kLoraMaxAdapters = 1024;
 constexpr int kLoraMaxTokens = 1 << 24;
 constexpr int kLoraPlanThreads = 512;
+constexpr int kLoraDownThreads = 512;
 constexpr int kLoraThreads = 256;
 constexpr int kLoraMaxSplits = 16;
+constexpr int kLoraStep = 128;            // of k: splits are multiples
 // Rows of a tile: tokens of one adapter that are multiplied at a time.
 inline int lora_tile_rows(int64_t tokens, int64_t adapters) { return tokens >= 64 * adapters ? 64 : 16; }
 // Most tiles that a plan can hold; tokens without an adapter are a group of their own.
@@ -120,15 +123,15 @@ inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
 // Rank that the kernels are built for.
 __host__ __device__ constexpr int lora_rank_block(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-struct LoraTile {
-  int32_t adapter;          // -1: none
-  int32_t start, rows;      // in the plan's order of tokens
-  int32_t reserved;
-};
+// A plan: each tile's adapter, and each tile's tokens in ascending order, -1 behind them.
+// Rows lie where their tile is, so that a workgroup knows its rows without having seen the
+// tile, and reads both at once.
+constexpr int kLoraNone = -1;             // a tile of tokens without an adapter
+constexpr int kLoraUnused = -2;           // no tile
 struct LoraPlanParams {
   const int32_t* index;
-  LoraTile* tiles;          // [max_tiles], those unused with rows = 0
-  int32_t* order;           // [tokens]
+  int32_t* tile;            // [max_tiles]
+  int32_t* token;           // [max_tiles][tile_rows]
   int32_t tokens, adapters, tile_rows, max_tiles;
 };
 struct LoraParams {
@@ -139,13 +142,17 @@ struct LoraParams {
   uint16_t* out;
   const float* scales;
   const int32_t* ranks;
-  const LoraTile* tiles;
-  const int32_t* order;
-  float* parts;             // [splits][tokens][rank block]
+  const int32_t* tile;
+  const int32_t* token;
+  float* parts;             // [splits][rows of all tiles][rank block] (splits > 1)
+  uint16_t* high;           // [rows of all tiles][rank block]: v's parts
+  uint16_t* low;
+  float* factor;            // [rows of all tiles]: the adapter's scale, and a power of two
+  int32_t* counters;        // [tiles], zero between launches (splits > 1)
   int64_t x_stride, base_stride, out_stride;
   int32_t tokens, k, n, adapters, rank, tiles_most;
   int32_t splits;           // of k over workgroups
-  int32_t steps;            // of 128 k that a split takes
+  int32_t steps;            // of kLoraStep that a split takes
   int32_t columns;          // of n that a workgroup of the second kernel takes
 };
 

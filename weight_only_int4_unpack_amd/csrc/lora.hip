@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kLoraPlanThreads) void plan_kernel(LoraPlanParams p
         const int k = __builtin_amdgcn_readlane(key, __builtin_ctzll(rest));
         const uint64_t same = __ballot(key == k);
         const int before = l.count[wave][k];
-        if (key == k) place(t, before + __popcll(same & ((1ull << lane) - 1)));
+        if (key == k) place(t, before + __popcll(same & ((1ull << lane) - 1)), k);
         __builtin_amdgcn_wave_barrier();
         if (lane == 0) l.count[wave][k] = before + __popcll(same);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kLoraPlanThreads) void plan_kernel(LoraPlanParams p
       }
     }
   };
-  over([](int, int) {});
+  over([](int, int, int) {});
   __syncthreads();
   // groups: tokens and tiles before each, kEach groups a thread
   constexpr int kEach = (kLoraMaxAdapters + 1 + kLoraPlanThreads - 1) / kLoraPlanThreads;
@@ -123,117 +123,39 @@ __global__ __launch_bounds__(kLoraPlanThreads) void plan_kernel(LoraPlanParams p
   __syncthreads();
   const int used = l.tiles[groups];
   for (int i = tid; i < p.max_tiles; i += kLoraPlanThreads) {
-    LoraTile tile{-1, 0, 0, 0};
+    int adapter = kLoraUnused;
+    int first = 0, left = 0;             // of the group's tokens in this tile
     if (i < used) {
       int g = 0, end = groups;           // the last group with tiles before <= i
       while (end - g > 1) {
         const int mid = (g + end) / 2;
         if (l.tiles[mid] <= i) g = mid; else end = mid;
       }
-      tile.adapter = g < p.adapters ? g : -1;
-      tile.start = l.start[g] + (i - l.tiles[g]) * p.tile_rows;
-      tile.rows = min(p.tile_rows, l.start[g + 1] - tile.start);
+      adapter = g < p.adapters ? g : kLoraNone;
+      first = (i - l.tiles[g]) * p.tile_rows;
+      left = l.start[g + 1] - l.start[g] - first;
     }
-    p.tiles[i] = tile;
+    p.tile[i] = adapter;
+    for (int r = max(left, 0); r < p.tile_rows; ++r) p.token[(int64_t)i * p.tile_rows + r] = -1;
   }
-  over([&](int t, int at) { p.order[at] = t; });
+  over([&](int t, int at, int key) {
+    const int in = at - l.start[key];
+    const int tile = l.tiles[key] + in / p.tile_rows;
+    p.token[(int64_t)tile * p.tile_rows + in % p.tile_rows] = t;
+  });
 }
 
-// A tile as the kernels may use it, whatever the plan holds.
-__device__ __forceinline__ LoraTile tile_of(const LoraParams& p, int i, int most) {
-  LoraTile t = p.tiles[i];
-  t.start = min(max(t.start, 0), p.tokens);
-  t.rows = min(min(max(t.rows, 0), most), p.tokens - t.start);
-  if (t.adapter >= p.adapters) t.adapter = -1;
-  return t;
+// A row's token, or -1, whatever the plan holds; and the tile's adapter.
+__device__ __forceinline__ int token_of(const LoraParams& p, int64_t row) {
+  const int t = p.token[row];
+  return t < p.tokens ? t : -1;
 }
-__device__ __forceinline__ int token_of(const LoraParams& p, int at) {
-  return min(max(p.order[at], 0), p.tokens - 1);
+__device__ __forceinline__ int adapter_of(const LoraParams& p, int tile) {
+  const int i = p.tile[tile];
+  return i < p.adapters ? i : kLoraUnused;
 }
 __device__ __forceinline__ int rank_of(const LoraParams& p, int adapter) {
   return p.ranks ? min(max(p.ranks[adapter], 0), p.rank) : p.rank;
-}
-
-// ---- down: MT tiles of 16 tokens, RB ranks (padded). A lane holds 8 PIECES consecutive k
-// of its token (or rank) and step, four lanes 32 PIECES: any order of k will do, as long as x
-// and a have the same.
-template <typename T, int MT, int RB>
-__global__ __launch_bounds__(kLoraThreads) void down_kernel(LoraParams p) {
-  constexpr int RT = RB / 16;
-  constexpr int PIECES = MT * RT <= 2 ? 4 : 2;
-  constexpr int kStep = 32 * PIECES;
-  constexpr int kMeet = MT * RT < 8 ? MT * RT : 8;          // results that meet at a time
-  __shared__ f32x4 meet[4][kMeet][64];
-  const LoraTile tile = tile_of(p, blockIdx.x, 16 * MT);
-  if (tile.rows == 0 || tile.adapter < 0) return;
-  const int split = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, group = lane >> 4;
-  const int rank = rank_of(p, tile.adapter);
-  const uint16_t* x[MT];
-  const uint16_t* a[RT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    x[m] = p.x + token_of(p, tile.start + min(16 * m + col, tile.rows - 1)) * p.x_stride;
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    a[r] = p.a + ((int64_t)tile.adapter * p.rank + min(16 * r + col, p.rank - 1)) * p.k;
-  f32x4 sum[MT][RT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0, 0, 0, 0};
-
-  // this wave's range: a quarter of the split's
-  const int k_lo = split * p.steps * 128, k_hi = min(p.k, k_lo + p.steps * 128);
-  const int each = ((k_hi - k_lo + 4 * kStep - 1) / (4 * kStep)) * kStep;
-  const int from = k_lo + wave * each, to = min(k_hi, from + each);
-  for (int k0 = from; k0 < to; k0 += kStep) {
-    u32x4 xs[MT][PIECES], as[RT][PIECES];
-    const int k = k0 + group * 8 * PIECES;
-#pragma unroll
-    for (int j = 0; j < PIECES; ++j) {
-      const bool in = k + 8 * j < to;
-      const int at = in ? k + 8 * j : 0;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) xs[m][j] = load16(x[m] + at);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) as[r][j] = load16(a[r] + at);
-      // past the end and the rank: zeros on both sides, as 0 x NaN is NaN
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        if (!in) xs[m][j] = u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-        if (!in) as[r][j] = u32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int j = 0; j < PIECES; ++j)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) sum[m][r] = mfma<T>(as[r][j], xs[m][j], sum[m][r]);
-  }
-  // The waves' sums: a lane holds ranks 16 r + 4 group .. + 3 of token 16 m + col.
-  float* out = p.parts + ((int64_t)split * p.tokens + tile.start) * RB;
-#pragma unroll
-  for (int first = 0; first < MT * RT; first += kMeet) {
-    if (first > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMeet; ++i) meet[wave][i][lane] = sum[(first + i) / RT][(first + i) % RT];
-    __syncthreads();
-    for (int i = wave; i < kMeet; i += 4) {
-      f32x4 v = meet[0][i][lane];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) v += meet[w][i][lane];
-      const int m = (first + i) / RT, r = (first + i) % RT;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * r + 4 * group + e >= rank) v[e] = 0.0f;
-      if (16 * m + col < tile.rows) *(f32x4*)(out + (16 * m + col) * RB + 16 * r + 4 * group) = v;
-    }
-  }
 }
 
 // v as two 16-bit parts; what is not finite has no second one.
@@ -248,150 +170,371 @@ __device__ __forceinline__ void halves(const f32x8& v, u32x4* high, u32x4* low) 
   *low = narrow8<T>(rest);
 }
 
-// ---- up: a wave takes 64 columns of MT tiles of 16 tokens at a time. Rank blocks of 16
-// are one matrix instruction of depth 32, v's high parts in the first half and its low ones
-// in the second; larger ones two for each 32 ranks. b is the left operand, its rows in the
-// order that gives a lane 8 consecutive columns of its token.
+// Values that other workgroups read: 8 bytes at a time, past the caches that are not shared.
+__device__ __forceinline__ void store_shared(float* to, const f32x4& v) {
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+  const u64x2 w = __builtin_bit_cast(u64x2, v);
+  __hip_atomic_store((uint64_t*)to, w.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store((uint64_t*)to + 1, w.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x8 load_shared(const float* from) {
+  typedef uint64_t u64x4 __attribute__((ext_vector_type(4)));
+  u64x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __hip_atomic_load((const uint64_t*)from + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f32x8, w);
+}
+// This wave's stores are where everybody sees them.
+__device__ __forceinline__ void wait_stores() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0F70);    // vmcnt(0)
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// ---- down: MT tiles of 16 tokens, RB ranks (padded). Where k is split over workgroups, the
+// last one to arrive adds the splits, in their order: their sums are stored and loaded at the
+// device's point of coherence (a release and acquire by fences writes back and invalidates
+// a whole L2: 64 tokens, 10 splits 48 us instead of 7).
 template <typename T, int MT, int RB>
-__global__ __launch_bounds__(kLoraThreads) void up_kernel(LoraParams p) {
-  constexpr int KS = RB <= 16 ? 1 : RB / 32;
-  constexpr bool kPacked = RB <= 16;
-  const LoraTile tile = tile_of(p, blockIdx.x, 16 * MT);
-  if (tile.rows == 0) return;
+__global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
+  constexpr int kWaves = kLoraDownThreads / 64;
+  constexpr int RT = RB / 16, kRows = 16 * MT;
+  constexpr int PIECES = MT * RT <= 2 ? 4 : 2;
+  constexpr int kStep = 32 * PIECES;
+  constexpr int kMeet = MT * RT < 4 ? MT * RT : 4;          // results that meet at a time
+  __shared__ f32x4 meet[kWaves][kMeet][64];
+  __shared__ float whole[kRows][RB];
+  __shared__ int arrived;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, group = lane >> 4;
-  int64_t token[MT];
+  const int64_t rows = (int64_t)blockIdx.x * kRows;
+  int token[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) token[m] = token_of(p, tile.start + min(16 * m + col, tile.rows - 1));
-  const int n_lo = blockIdx.y * p.columns, n_hi = min(p.n, n_lo + p.columns);
-  if (tile.adapter < 0) {
-    if (p.base == p.out) return;
-    for (int n = n_lo + wave * 64 + group * 8; n < n_hi; n += 256) {
+  for (int m = 0; m < MT; ++m) token[m] = token_of(p, rows + 16 * m + col);
+  const int adapter = adapter_of(p, blockIdx.x);
+  if (adapter < 0) return;
+  const int split = blockIdx.y;
+  const int rank = rank_of(p, adapter);
+  // rows without a token take part with another's x: each row's sums are its own
+  const uint16_t* x[MT];
+  const uint16_t* a[RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = p.x + (int64_t)max(token[m], 0) * p.x_stride;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    a[r] = p.a + ((int64_t)adapter * p.rank + min(16 * r + col, p.rank - 1)) * p.k;
+  f32x4 sum[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0, 0, 0, 0};
+
+  // this wave's range of the split's
+  const int k_lo = split * p.steps * kLoraStep, k_hi = min(p.k, k_lo + p.steps * kLoraStep);
+  const int each = ((k_hi - k_lo + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
+  const int from = k_lo + wave * each, to = min(k_hi, from + each);
+  struct Stage {
+    u32x4 x[MT][PIECES], a[RT][PIECES];
+  };
+  auto load = [&](int k0, Stage& s) {
+    const int k = k0 + group * 8;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const int at = k + 32 * j < to ? k + 32 * j : 0;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) s.x[m][j] = load16(x[m] + at);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s.a[r][j] = load16(a[r] + at);
+    }
+  };
+  auto multiply = [&](int k0, Stage& s) {
+    const int k = k0 + group * 8;
+    if (k0 + kStep > to) {
+      // past the end: zeros on both sides, as 0 x NaN is NaN
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        const bool in = k + 32 * j < to;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (!in) s.x[m][j] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (!in) s.a[r][j] = u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (16 * m + col < tile.rows && n + 32 * j < n_hi) {
-            u32x4 y{0, 0, 0, 0};
-            if (p.base) y = load16(p.base + token[m] * p.base_stride + n + 32 * j);
-            *(u32x4*)(p.out + token[m] * p.out_stride + n + 32 * j) = y;
-          }
+        for (int r = 0; r < RT; ++r) sum[m][r] = mfma<T>(s.a[r][j], s.x[m][j], sum[m][r]);
+  };
+  // the next step's loads are on their way while one is multiplied (a step past the range
+  // loads its first values again)
+  if (from < to) {
+    Stage s0, s1;
+    load(from, s0);
+    for (int k0 = from; k0 < to; k0 += 2 * kStep) {
+      load(k0 + kStep, s1);
+      multiply(k0, s0);
+      load(k0 + 2 * kStep, s0);
+      if (k0 + kStep < to) multiply(k0 + kStep, s1);
     }
-    return;
   }
-  const int rank = rank_of(p, tile.adapter);
-  // v of this lane's tokens: the splits in order, then its parts
-  u32x4 high[MT][KS], low[MT][KS];
-  float factor[MT];
-  const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
+  // The waves' sums: a lane holds ranks 16 r + 4 group .. + 3 of token 16 m + col.
+  const int64_t all_rows = (int64_t)p.tiles_most * kRows;
+  float* parts = p.parts + (split * all_rows + rows) * RB;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    f32x8 v[KS];
-    const bool in = 16 * m + col < tile.rows;
+  for (int first = 0; first < MT * RT; first += kMeet) {
+    if (first > 0) __syncthreads();
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      v[s] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
-      if (in) {
-        const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
-        const float* at = p.parts + ((int64_t)tile.start + 16 * m + col) * RB + r0;
-        for (int i = 0; i < p.splits; ++i) v[s] += *(const f32x8*)(at + (int64_t)i * p.tokens * RB);
+    for (int i = 0; i < kMeet; ++i) meet[wave][i][lane] = sum[(first + i) / RT][(first + i) % RT];
+    __syncthreads();
+    for (int i = wave; i < kMeet; i += kWaves) {
+      f32x4 v = meet[0][i][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += meet[w][i][lane];
+      const int m = (first + i) / RT, r = (first + i) % RT;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * r + 4 * group + e >= rank) v[e] = 0.0f;
+      const int row = 16 * m + col, at = 16 * r + 4 * group;
+      if (p.splits > 1) {
+        store_shared(parts + row * RB + at, v);
+      } else {
+        *(f32x4*)&whole[row][at] = v;
       }
     }
-    factor[m] = scale;
+  }
+  if (p.splits > 1) {
+    wait_stores();
+    __syncthreads();
+    if (tid == 0) {
+      arrived = __hip_atomic_fetch_add(p.counters + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (arrived == p.splits - 1)
+        __hip_atomic_store(p.counters + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (arrived != p.splits - 1) return;
+  } else {
+    __syncthreads();
+  }
+  // 8 ranks of a row a thread; the RB / 8 lanes of a row are neighbours
+  constexpr int kLanes = RB / 8;
+  const float scale = p.scales ? p.scales[adapter] : 1.0f;
+  for (int i = tid; i < kRows * kLanes; i += kLoraDownThreads) {
+    const int row = i / kLanes, r0 = i % kLanes * 8;
+    f32x8 v;
+    if (p.splits > 1) {
+      const float* at = p.parts + (rows + row) * RB + r0;
+      v = load_shared(at);
+      constexpr int kAhead = 5;
+      for (int k = 1; k < p.splits; k += kAhead) {
+        f32x8 next[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) next[j] = load_shared(at + min(k + j, p.splits - 1) * all_rows * RB);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + j < p.splits) v += next[j];
+      }
+    } else {
+      v = *(const f32x8*)&whole[row][r0];
+    }
+    float factor = scale;
     if constexpr (T::kCode == W4A16_F16) {
       // the row's largest magnitude to 2^14..2^15, if it is finite and not 0
       uint32_t most = 0;
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[s][e]) & 0x7FFFFFFFu);
-      most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-      most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+      for (int s = 1; s < kLanes; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
       const int exponent = (int)(most >> 23);
       if (exponent > 0 && exponent < 255) {
         const int lift = 127 + 14 - exponent;
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[s][e] = __builtin_ldexpf(v[s][e], lift);
-        factor[m] = __builtin_ldexpf(scale, -lift);
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], lift);
+        factor = __builtin_ldexpf(scale, -lift);
       } else if (exponent == 255) {
         // beside what is not finite the others only must not become infinite
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (__builtin_isfinite(v[s][e])) v[s][e] = fminf(fmaxf(v[s][e], -65504.0f), 65504.0f);
+        for (int e = 0; e < 8; ++e)
+          if (__builtin_isfinite(v[e])) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
       }
     }
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      halves<T>(v[s], &high[m][s], &low[m][s]);
-      if (kPacked && group >= 2) high[m][s] = low[m][s];
-    }
+    u32x4 high, low;
+    halves<T>(v, &high, &low);
+    *(u32x4*)(p.high + (rows + row) * RB + r0) = high;
+    *(u32x4*)(p.low + (rows + row) * RB + r0) = low;
+    if (r0 == 0) p.factor[rows + row] = factor;
   }
-  const uint16_t* b = p.b + (int64_t)tile.adapter * p.n * p.rank;
+}
+
+#ifndef LORA_OCC
+#define LORA_OCC 2
+#endif
+#ifndef LORA_D
+#define LORA_D 4
+#endif
+// ---- up: a wave takes 64 columns of a tile at a time, one step for each of its MT parts of
+// 16 tokens. b of the columns stays in registers for the steps, v of the steps in LDS (one
+// step: in registers too). Rank blocks of 16 are one matrix instruction of depth 32, v's high
+// parts in the first half and its low ones in the second; larger ones two for each 32 ranks.
+// b is the left operand, its rows in the order that gives a lane 8 consecutive columns of its
+// token.
+// Loads return in the order in which they were issued: base is loaded kAhead steps ahead, and
+// b of the next columns before the base that is needed after it.
+template <typename T, int MT, int RB>
+__global__ __launch_bounds__(kLoraThreads, LORA_OCC) void up_kernel(LoraParams p) {
+  constexpr int KS = RB <= 16 ? 1 : RB / 32;
+  constexpr bool kPacked = RB <= 16;
+  constexpr int kRows = 16 * MT, kColumns = 256;
+  constexpr int kAhead = MT == 1 ? 1 : LORA_D;
+  constexpr int kParts = kPacked ? 1 : 2;              // loads of v for 32 ranks
+  constexpr int kStride = (kPacked ? 32 : 2 * RB) + 8; // of a row in LDS: 16 bytes apart from the banks' period
+  __shared__ uint16_t vs[MT > 1 ? kRows * kStride : 8];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, group = lane >> 4;
+  const int64_t rows = (int64_t)blockIdx.x * kRows;
+  int token[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) token[m] = token_of(p, rows + 16 * m + col);
+  const int adapter = adapter_of(p, blockIdx.x);
+  if (adapter == kLoraUnused) return;
+  const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
+  const uint16_t* base[MT];
+  uint16_t* out[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    base[m] = p.base + (int64_t)max(token[m], 0) * p.base_stride + group * 8;
+    out[m] = p.out + (int64_t)max(token[m], 0) * p.out_stride + group * 8;
+  }
+  struct Held {
+    u32x4 x[2];
+  };
+  auto load_base = [&](int n0, int m) {
+    Held h;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      h.x[i] = u32x4{0, 0, 0, 0};
+      if (p.base && token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) h.x[i] = load16(base[m] + n0 + 32 * i);
+    }
+    return h;
+  };
+  if (adapter < 0) {
+    if (p.base == p.out) return;
+    for (int n0 = n_lo; n0 < n_hi; n0 += kColumns) {
+      Held h[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) h[m] = load_base(n0, m);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) *(u32x4*)(out[m] + n0 + 32 * i) = h[m].x[i];
+    }
+    return;
+  }
+  const int rank = rank_of(p, adapter);
+  const uint16_t* b = p.b + (int64_t)adapter * p.n * p.rank;
   const int row = (col >> 2) * 8 + (col & 3);
-  for (int n0 = n_lo + wave * 64; n0 < n_hi; n0 += 256) {
-    f32x4 sum[4][MT];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sum[j][m] = f32x4{0, 0, 0, 0};
-    u32x4 held[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        held[m][h] = u32x4{0, 0, 0, 0};
-        const int n = n0 + 32 * h + group * 8;
-        if (p.base && n < n_hi) held[m][h] = load16(p.base + token[m] * p.base_stride + n);
-      }
+  struct Columns {
+    u32x4 x[KS][4];
+  };
+  auto load_b = [&](int n0) {
+    Columns c;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      u32x4 bs[4];
+      const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = n0 + (j >> 1) * 32 + (j & 1) * 4 + row;
-        const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
-        bs[j] = u32x4{0, 0, 0, 0};
-        if (n < n_hi && r0 < rank) {
-          bs[j] = load16(b + (int64_t)n * p.rank + r0);
-          // past the adapter's own rank: zeros, as 0 x NaN is NaN
-          if (r0 + 8 > rank) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (r0 + e >= rank) bs[j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-          }
-        }
+        c.x[s][j] = u32x4{0, 0, 0, 0};
+        if (n < n_hi && r0 < rank) c.x[s][j] = load16(b + (int64_t)n * p.rank + r0);
       }
+    }
+    return c;
+  };
+  // past the adapter's own rank: zeros, as 0 x NaN is NaN
+  auto cut_b = [&](Columns& c) {
+    if ((rank & 7) == 0) return;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          sum[j][m] = mfma<T>(bs[j], high[m][s], sum[j][m]);
-          if constexpr (!kPacked) sum[j][m] = mfma<T>(bs[j], low[m][s], sum[j][m]);
+        for (int e = 0; e < 8; ++e)
+          if (r0 + e >= rank) c.x[s][j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+  };
+  float factor[MT];
+  u32x4 v1[KS][kParts];                  // of the only step
+  if constexpr (MT > 1) {
+    constexpr int kLanes = RB / 8;       // 16-byte pieces of a row's high (or low) parts
+    for (int i = tid; i < 2 * kRows * kLanes; i += kLoraThreads) {
+      const int part = i / (kRows * kLanes), at = i % (kRows * kLanes);
+      *(u32x4*)&vs[at / kLanes * kStride + part * RB + at % kLanes * 8] = load16((part ? p.low : p.high) + rows * RB + at * 8);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int64_t at = (rows + col) * RB + (kPacked ? (group & 1) * 8 : 32 * s + group * 8);
+      if constexpr (kPacked) {
+        v1[s][0] = load16((group < 2 ? p.high : p.low) + at);
+      } else {
+        v1[s][0] = load16(p.high + at);
+        v1[s][1] = load16(p.low + at);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) factor[m] = p.factor[rows + 16 * m + col];
+  Columns next = load_b(n_lo);
+  Held held[kAhead];
+#pragma unroll
+  for (int m = 0; m < kAhead; ++m) held[m] = load_base(n_lo + m / MT * kColumns, m % MT);
+  if constexpr (MT > 1) __syncthreads();
+
+  for (int n0 = n_lo; n0 < n_hi; n0 += kColumns) {
+    Columns c = next;
+    cut_b(c);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          u32x4 v;
+          if constexpr (MT > 1)
+            v = *(const u32x4*)&vs[(16 * m + col) * kStride + (kPacked ? group * 8 : i * RB + 32 * s + group * 8)];
+          else
+            v = v1[s][i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v, sum[j]);
+        }
+      if (m == 0) next = load_b(n0 + kColumns);
+      const Held now = held[m % kAhead];
+      held[m % kAhead] = load_base(n0 + (m + kAhead) / MT * kColumns, (m + kAhead) % MT);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) {
+          f32x8 y = widen8<T>(now.x[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = fmaf(sum[2 * i + e / 4][e % 4], factor[m], y[e]);
+          *(u32x4*)(out[m] + n0 + 32 * i) = narrow8<T>(y);
         }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = n0 + 32 * h + group * 8;
-        if (16 * m + col < tile.rows && n < n_hi) {
-          f32x8 y = widen8<T>(held[m][h]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = fmaf(sum[2 * h + e / 4][m][e % 4], factor[m], y[e]);
-          *(u32x4*)(p.out + token[m] * p.out_stride + n) = narrow8<T>(y);
-        }
-      }
   }
 }
 
 template <typename T, int MT, int RB>
 hipError_t launch(const LoraParams& p, hipStream_t stream) {
-  down_kernel<T, MT, RB><<<dim3(p.tiles_most, p.splits), kLoraThreads, 0, stream>>>(p);
+  down_kernel<T, MT, RB><<<dim3(p.tiles_most, p.splits), kLoraDownThreads, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   up_kernel<T, MT, RB><<<dim3(p.tiles_most, (p.n + p.columns - 1) / p.columns), kLoraThreads, 0, stream>>>(p);

@@ -1,16 +1,24 @@
 // Verification of drafted tokens against the model's logits, and the draw of the token
 // after the accepted ones.
 //
-// Two kernels. The first weighs every row: a wave takes a chunk of 2048 (fp32: 1024)
-// logits, finds its largest m and sums 2^((x - m) c), c = log2(e) / temperature, in fp64.
-// The second has one workgroup for a sequence: it joins the chunks' sums of the sequence's
-// rows, weighs the drafted tokens, walks from node to node, and draws the last token: the
-// chunk in which the cumulative sum passes the border from the chunks' sums, the logit from
-// that chunk alone. Where a drawn token was rejected, the weights max(w / S - q, 0) are not
-// yet summed: several workgroups take a sequence's chunks, and whoever is last draws.
+// Two kernels. The first weighs every row in fp32: a wave takes a chunk of 2048 (fp32: 1024)
+// logits, finds its largest m and sums 2^((x - m) c), c = log2(e) / temperature. It is one
+// pass over the logits. The second has one or more workgroups for a sequence: it joins the
+// chunks' sums of the sequence's rows, weighs the drafted tokens, walks from node to node,
+// and draws the last token from the last node's row, whose chunks it sums again in fp64: the
+// chunk in which the cumulative sum passes the border from those sums, the logit from that
+// chunk alone. All workgroups of a sequence walk alike and share the chunks; whoever is last
+// draws.
 //
-// fp64, because a draw is a border in a cumulative sum over 2^17 terms: its rounding moves
-// a draw once in 1 / (terms x rounding), a hundred draws with fp32 and 10^10 with fp64.
+// What needs fp64: a draw is a border in a cumulative sum over 2^17 terms, and rounding moves
+// one draw in 1 / (terms x rounding), a hundred with fp32 and 10^8 with sums that are right
+// to 2^-46. A token is accepted by one comparison; where the row's fp32 sum is too near to
+// tell (2^-16 of it, some 16 times its error), the row is summed in fp64 and compared again.
+// Where a drawn token was rejected, max(w - S q, 0) is summed with S of the first kernel,
+// together with the sum Q of the q under w: with the exact S, known when all chunks are, the
+// sum is that plus (S_first - S) Q (what changes sides on the way is 2^-24 of 2^-24).
+#include <climits>
+
 #include "batch_internal.h"
 #include "serve_device.h"
 
@@ -22,44 +30,76 @@ using namespace serve;
 constexpr float kInf = __builtin_inff();
 constexpr double kLog2e = 1.4426950408889634074;
 
-// 2^t for t <= 0 (NaN and -inf: 0): 2^n 2^f, n = t rounded, |f| <= 1/2. The polynomial is
-// the one of degree 10 with the least largest relative error, 2^-52 (exchange method);
-// below 2^-1074 there is nothing to hold.
-__device__ __forceinline__ double exp2_of(double t) {
-  t = __builtin_fmax(t, -1100.0);
-  const double n = __builtin_rint(t), f = t - n;
-  double p = 0x1.e3991e644e6abp-28;
-  p = __builtin_fma(p, f, 0x1.b6740fc28f781p-24);
-  p = __builtin_fma(p, f, 0x1.62c157ee59177p-20);
-  p = __builtin_fma(p, f, 0x1.ffcb55e82f22cp-17);
-  p = __builtin_fma(p, f, 0x1.4309126056718p-13);
-  p = __builtin_fma(p, f, 0x1.5d87fe9cc5d6fp-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab6fbde0f7p-7);
-  p = __builtin_fma(p, f, 0x1.c6b08d703d48ap-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff82c3b9p-3);
-  p = __builtin_fma(p, f, 0x1.62e42fefa3a17p-1);
+// Below 2^-1000 a weight is 0: there is no sum of weights that it would change.
+constexpr double kLeast = -1000.0;
+
+// 2^(d c) for kLeast <= d c <= 0: 2^n 2^f, n = d c rounded (by an addition that leaves it in
+// the low bits), f = d c - n rounded once, |f| <= 1/2, n added to the exponent. The polynomial
+// is the one of degree 9 with the least largest relative error, 2^-46 (exchange method).
+__device__ __forceinline__ double exp2_of(double d, double c) {
+  const double shifted = __builtin_fma(d, c, 0x1.8p52);
+  const double f = __builtin_fma(d, c, -(shifted - 0x1.8p52));
+  double p = 0x1.b3f421492867dp-24;
+  p = __builtin_fma(p, f, 0x1.63edf1058a76ep-20);
+  p = __builtin_fma(p, f, 0x1.ffce24611c0dap-17);
+  p = __builtin_fma(p, f, 0x1.43088fca9a183p-13);
+  p = __builtin_fma(p, f, 0x1.5d87fd9011eeep-10);
+  p = __builtin_fma(p, f, 0x1.3b2ab72a1098dp-7);
+  p = __builtin_fma(p, f, 0x1.c6b08d70d2003p-5);
+  p = __builtin_fma(p, f, 0x1.ebfbdff81570dp-3);
+  p = __builtin_fma(p, f, 0x1.62e42fefa3752p-1);
   p = __builtin_fma(p, f, 1.0);
-  return __builtin_ldexp(p, (int)n);
+  typedef uint32_t Halves __attribute__((ext_vector_type(2)));
+  Halves h = __builtin_bit_cast(Halves, p);
+  h.y += __builtin_bit_cast(Halves, shifted).x << 20;
+  return __builtin_bit_cast(double, h);
 }
 
-// Weight of a logit against the row's (or chunk's) largest, m finite.
-__device__ __forceinline__ double weigh(float x, double m, double c) { return exp2_of(((double)x - m) * c); }
-
-// log2(e) / temperature of a sequence; 0: greedy.
-__device__ __forceinline__ double exponent_of(const VerifyParams& p, int sequence) {
-  if (!p.temperatures) return kLog2e;
-  const float t = p.temperatures[sequence];
-  return t > 0.0f ? kLog2e / (double)t : 0.0;
+// How a sequence's logits are weighed: c = log2(e) / temperature, and the least difference
+// that has a weight.
+struct Scale {
+  double c, least;
+  bool greedy;
+};
+__device__ __forceinline__ Scale scale_of(const VerifyParams& p, int sequence) {
+  Scale s{kLog2e, kLeast / kLog2e, false};
+  if (p.temperatures) {
+    const float t = p.temperatures[sequence];
+    s.greedy = !(t > 0.0f);
+    // an infinite temperature: every difference but an infinite one is 0
+    s.c = s.greedy ? 1.0 : __builtin_fmax(kLog2e / (double)t, 1e-300);
+    s.least = s.greedy ? 0.0 : __builtin_fmax(kLeast / kLog2e * (double)t, -1e303);
+  }
+  return s;
 }
-__device__ __forceinline__ bool is_greedy(const VerifyParams& p, int sequence) {
-  return p.temperatures && !(p.temperatures[sequence] > 0.0f);
+// Weight of a logit against the row's (or chunk's) largest, m finite; 0 for -infinity.
+__device__ __forceinline__ double weigh(float x, double m, const Scale& s) {
+  const double d = (double)x - m;
+  const double w = exp2_of(__builtin_fmax(d, s.least), s.c);
+  return d > s.least ? w : 0.0;
 }
-
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) x += __shfl_xor(x, s);
-  return x;
+// The same with 2^-1000 in place of 0, for sums: those below kNothing are 0.
+__device__ __forceinline__ double weigh_near(float x, double m, const Scale& s) {
+  return exp2_of(__builtin_fmax((double)x - m, s.least), s.c);
 }
+constexpr double kNothing = 0x1p-900;
+// The value of the lane whose number differs in one bit (or, inside 8 and 16 lanes, the
+// mirrored one: enough where whole groups agree already).
+template <int STEP>
+__device__ __forceinline__ int other_lane(int x) {
+  if constexpr (STEP >= 16) return __shfl_xor(x, STEP);
+  constexpr int kCtrl = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+  return __builtin_amdgcn_update_dpp(0, x, kCtrl, 0xF, 0xF, true);
+}
+template <int STEP>
+__device__ __forceinline__ double add_lane(double x) {
+  typedef int Halves __attribute__((ext_vector_type(2)));
+  const Halves h = __builtin_bit_cast(Halves, x);
+  return x + __builtin_bit_cast(double, Halves{other_lane<STEP>(h.x), other_lane<STEP>(h.y)});
+}
+// Sums over 16 lanes, in all of them, and over the wave.
+__device__ __forceinline__ double row_sum(double x) { return add_lane<8>(add_lane<4>(add_lane<2>(add_lane<1>(x)))); }
+__device__ __forceinline__ double wave_sum(double x) { return add_lane<32>(add_lane<16>(row_sum(x))); }
 // Sum of the lanes up to this one.
 __device__ __forceinline__ double wave_prefix(double x, int lane) {
 #pragma unroll
@@ -70,16 +110,18 @@ __device__ __forceinline__ double wave_prefix(double x, int lane) {
   return x;
 }
 // NaN where one is.
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) x = __builtin_elementwise_maximum(x, __shfl_xor(x, s));
-  return x;
+template <int STEP>
+__device__ __forceinline__ float max_lane(float x) {
+  return __builtin_elementwise_maximum(x, __int_as_float(other_lane<STEP>(__float_as_int(x))));
 }
-__device__ __forceinline__ int wave_min(int x) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) x = min(x, __shfl_xor(x, s));
-  return x;
+__device__ __forceinline__ float row_max(float x) { return max_lane<8>(max_lane<4>(max_lane<2>(max_lane<1>(x)))); }
+__device__ __forceinline__ float wave_max(float x) { return max_lane<32>(max_lane<16>(row_max(x))); }
+template <int STEP>
+__device__ __forceinline__ int min_lane(int x) {
+  return min(x, other_lane<STEP>(x));
 }
+__device__ __forceinline__ int row_min(int x) { return min_lane<8>(min_lane<4>(min_lane<2>(min_lane<1>(x)))); }
+__device__ __forceinline__ int wave_min(int x) { return min_lane<32>(min_lane<16>(row_min(x))); }
 
 template <typename E>
 struct Logits;  // E: F16, BF16 or float
@@ -87,7 +129,7 @@ template <>
 struct Logits<float> {
   using Elem = uint32_t;
   static constexpr int kVec = 4;
-  static constexpr uint32_t kNone = 0xFF800000u;
+  static constexpr uint32_t kNoneWord = 0xFF800000u;
   static __device__ __forceinline__ float one(uint32_t x) { return __uint_as_float(x); }
   static __device__ __forceinline__ void widen(u32x4 r, float* x) {
 #pragma unroll
@@ -98,7 +140,7 @@ template <typename T>
 struct Logits16 {
   using Elem = uint16_t;
   static constexpr int kVec = 8;
-  static constexpr uint16_t kNone = T::kCode == W4A16_F16 ? 0xFC00u : 0xFF80u;
+  static constexpr uint32_t kNoneWord = T::kCode == W4A16_F16 ? 0xFC00FC00u : 0xFF80FF80u;
   static __device__ __forceinline__ float one(uint16_t x) { return widen1<T>(x); }
   static __device__ __forceinline__ void widen(u32x4 r, float* x) {
     const f32x8 y = widen8<T>(r);
@@ -112,45 +154,107 @@ template <>
 struct Logits<BF16> : Logits16<BF16> {};
 
 // A chunk of a row: kEach logits a lane, -infinity in the places outside the row. Lane
-// l's are first .. first + kEach - 1 (`packed`) or the kVec from first + 64 kVec v, v < 4.
+// l's are the kVec from first + 64 kVec v on, v < 4.
 template <typename E>
 struct Chunk {
   using L = Logits<E>;
   using Elem = typename L::Elem;
   static constexpr int kVecs = 4, kEach = kVecs * L::kVec, kSize = 64 * kEach;
+  u32x4 raw[kVecs];
+  f32x4 draft[kEach / 4];
   float x[kEach];
   int first;
 
   __device__ __forceinline__ static int lead(const Elem* row) { return (int)(((uintptr_t)row & 15) / sizeof(Elem)); }
 
-  template <bool PACKED>
-  __device__ __forceinline__ void load(const Elem* row, int vocab, int chunk, int lane) {
+  // fetch() starts the loads of a chunk, widen() takes them all.
+  __device__ __forceinline__ void fetch(const Elem* row, int vocab, int chunk, int lane) {
     const int at = chunk * kSize - lead(row);
-    first = at + lane * (PACKED ? kEach : L::kVec);
-    u32x4 raw[kVecs];
+    first = at + lane * L::kVec;
     if (at >= 0 && at + kSize <= vocab) {
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) raw[v] = load16(row + index(PACKED, v, 0));
-    } else {
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const int i = index(PACKED, v, 0);
-        if (i >= 0 && i + L::kVec <= vocab) {
-          raw[v] = load16(row + i);
-        } else {
-          Elem e[L::kVec];
-#pragma unroll
-          for (int j = 0; j < L::kVec; ++j) e[j] = i + j >= 0 && i + j < vocab ? row[i + j] : L::kNone;
-          raw[v] = __builtin_bit_cast(u32x4, e);
-        }
-      }
+      for (int v = 0; v < kVecs; ++v) raw[v] = load16(row + index(v, 0));
+      return;
     }
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      raw[v] = u32x4{L::kNoneWord, L::kNoneWord, L::kNoneWord, L::kNoneWord};
+      const int i = index(v, 0);
+      if (i >= 0 && i + L::kVec <= vocab) raw[v] = load16(row + i);
+    }
+    // a vector across an end of the row: one logit a lane, gathered into the vector's lane
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const int i0 = across(row, vocab, end);
+      if (i0 < at || i0 >= at + kSize) continue;
+      const int i = i0 + lane;
+      uint32_t bits = L::kNoneWord;
+      if (lane < L::kVec && i >= 0 && i < vocab) bits = row[i];
+      u32x4 whole;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (sizeof(Elem) == 4)
+          whole[w] = __builtin_amdgcn_readlane(bits, w);
+        else
+          whole[w] = (__builtin_amdgcn_readlane(bits, 2 * w) & 0xFFFFu) | __builtin_amdgcn_readlane(bits, 2 * w + 1) << 16;
+      }
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        if (index(v, 0) == i0) raw[v] = whole;
+    }
+  }
+  // First index of the vector that lies across the row's start or end (past both: none does).
+  __device__ __forceinline__ static int across(const Elem* row, int vocab, int end) {
+    const int before = lead(row);
+    if (end == 0) return before > 0 ? -before : INT_MAX;
+    const int rest = (vocab + before) % L::kVec;
+    return rest > 0 && vocab - rest >= 0 ? vocab - rest : INT_MAX;
+  }
+  __device__ __forceinline__ void widen() {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) L::widen(raw[v], x + v * L::kVec);
   }
+  // The same places of an fp32 row: 0 outside it.
+  __device__ __forceinline__ void fetch_draft(const float* q, int vocab, const Elem* row, int lane) {
+    typedef f32x4 Loose __attribute__((aligned(4)));
+    const int at = first - lane * L::kVec;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = index(v, 0);
+#pragma unroll
+      for (int j = 0; j < L::kVec / 4; ++j) {
+        draft[v * (L::kVec / 4) + j] = f32x4{0, 0, 0, 0};
+        if (i >= 0 && i + L::kVec <= vocab) draft[v * (L::kVec / 4) + j] = *(const Loose*)(q + i + 4 * j);
+      }
+    }
+    if (at >= 0 && at + kSize <= vocab) return;
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const int i0 = across(row, vocab, end);
+      if (i0 < at || i0 >= at + kSize) continue;
+      const int i = i0 + lane;
+      float mine = 0.0f;
+      if (lane < L::kVec && i >= 0 && i < vocab) mine = q[i];
+#pragma unroll
+      for (int j = 0; j < L::kVec; ++j) {
+        const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+          if (index(v, 0) == i0) draft[v * (L::kVec / 4) + j / 4][j % 4] = y;
+      }
+    }
+  }
+  // The next vector to the front, for loops that are not unrolled.
+  __device__ __forceinline__ void rotate() {
+    constexpr int kDraft = L::kVec / 4;
+#pragma unroll
+    for (int v = 0; v + 1 < kVecs; ++v) raw[v] = raw[v + 1];
+#pragma unroll
+    for (int v = 0; v + kDraft < kVecs * kDraft; ++v) draft[v] = draft[v + kDraft];
+  }
   // Index in the row of logit j of vector v.
-  __device__ __forceinline__ int index(bool packed, int v, int j) const {
-    return first + v * (packed ? L::kVec : 64 * L::kVec) + j;
+  __device__ __forceinline__ int index(int v, int j) const {
+    return first + v * (64 * L::kVec) + j;
   }
 };
 
@@ -169,74 +273,109 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& p, int row, int l
   return lo;
 }
 
+// Logits' weights in fp32 where the scale is an ordinary one; others (infinite and
+// vanishing temperatures) in fp64.
 template <typename E>
 __global__ __launch_bounds__(kVerifyThreads) void weigh_kernel(VerifyParams p) {
   using C = Chunk<E>;
   const int lane = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * (kVerifyThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (unit >= (int64_t)p.tokens * p.chunks) return;
   const int row = (int)(unit / p.chunks), chunk = (int)(unit - (int64_t)row * p.chunks);
+  if (row >= p.tokens) return;
   C c;
-  c.template load<false>((const typename C::Elem*)p.logits + row * p.row_stride, p.vocab, chunk, lane);
-  bool greedy = false;
-  double scale = kLog2e;
-  if (p.temperatures) {
-    const int b = sequence_of(p, row, lane);
-    greedy = is_greedy(p, b);
-    scale = exponent_of(p, b);
-  }
+  c.fetch((const typename C::Elem*)p.logits + row * p.row_stride, p.vocab, chunk, lane);
+  const Scale scale = scale_of(p, p.temperatures ? sequence_of(p, row, lane) : 0);
+  c.widen();
   float m = c.x[0];
 #pragma unroll
   for (int e = 1; e < C::kEach; ++e) m = __builtin_elementwise_maximum(m, c.x[e]);
   m = wave_max(m);
   VerifyChunk out{0.0, m, p.vocab};
-  if (greedy) {
+  if (scale.greedy) {
     int at = p.vocab;
 #pragma unroll
     for (int e = C::kEach - 1; e >= 0; --e)
-      if (c.x[e] == m) at = c.index(false, e / C::L::kVec, e % C::L::kVec);
+      if (c.x[e] == m) at = c.index(e / C::L::kVec, e % C::L::kVec);
     out.first = wave_min(at);
     out.s = 1.0;
   } else if (m > -kInf && m < kInf) {
-    double s = 0.0;
+    if (scale.c > 1e-30 && scale.c < 1e30) {
+      const float rate = (float)scale.c;
+      float s = 0.0f;
 #pragma unroll
-    for (int e = 0; e < C::kEach; ++e) s += weigh(c.x[e], (double)m, scale);
-    out.s = wave_sum(s);
+      for (int e = 0; e < C::kEach; ++e) s += __builtin_amdgcn_exp2f((c.x[e] - m) * rate);
+      out.s = wave_sum((double)s);
+    } else {
+      double s = 0.0;
+#pragma unroll
+      for (int e = 0; e < C::kEach; ++e) s += weigh(c.x[e], (double)m, scale);
+      out.s = wave_sum(s);
+    }
   }
   if (lane == 0) p.parts[unit] = out;
 }
 
+// A sequence's nodes in LDS, for as many as a call may have.
 struct Walk {
-  double weight[kVerifyMaxNodes];        // of a node's token at its parent
-  double sum[kVerifyMaxNodes];           // of the weights of a node's row
-  float most[kVerifyMaxNodes];           // its largest logit; not finite: no softmax
-  float uniform[kVerifyMaxNodes], prob[kVerifyMaxNodes];
-  int parent[kVerifyMaxNodes], token[kVerifyMaxNodes], first[kVerifyMaxNodes], path[kVerifyMaxNodes];
-  int gone[kVerifyMaxNodes];             // tokens rejected at the last node
-  double mass[kVerifyMaxChunks];
-  int len, dropped, last_token, arrived;
-  bool drawn;                            // a drawn token was rejected
+  double* weight;                        // of a node's token at its parent
+  double* sum;                           // of the weights of a node's row
+  double* mass;                          // of a row's chunks
+  float* most;                           // a row's largest logit; not finite: no softmax
+  float* uniform;
+  float* prob;
+  int* parent;
+  int* token;
+  int* first;                            // greedy: where the row's largest logit stands; else -1: an fp64 sum
+  int* path;
+  int* gone;                             // tokens rejected at the last node, each once
 };
+constexpr int kNodeBytes = 2 * 8 + 8 * 4;
+__host__ __device__ constexpr int walk_bytes(int nodes, int chunks) { return nodes * kNodeBytes + chunks * 8; }
 
-// r of the residual: what the model gives above the draft.
-__device__ __forceinline__ double above(double weight, double sum, float q) {
-  return __builtin_fmax(weight / sum - (double)q, 0.0);
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ void store_shared(double* to, double x) {
+  __hip_atomic_store((uint64_t*)to, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double load_shared(const double* from) {
+  return __builtin_bit_cast(double, __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
 template <typename E>
-__global__ __launch_bounds__(kWalkThreads) void walk_kernel(VerifyParams p) {
+__global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   using C = Chunk<E>;
   using L = typename C::L;
   using Elem = typename L::Elem;
-  __shared__ Walk w;
   constexpr int kWaves = kWalkThreads / 64;
+  extern __shared__ double lds[];
+  __shared__ double sums_[kWaves], before_, target_;
+  __shared__ int node_, len_, need_, dropped_, token_, arrived, chunk_, who_, last_[kWaves];
+  __shared__ bool drawn_;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.x / p.groups, group = blockIdx.x - b * p.groups;
+  Walk w;
+  {
+    const int most = max(p.max_q, 1);
+    w.weight = lds;
+    w.sum = w.weight + most;
+    w.mass = w.sum + most;
+    w.most = (float*)(w.mass + p.chunks);
+    w.uniform = w.most + most;
+    w.prob = w.uniform + most;
+    w.parent = (int*)(w.prob + most);
+    w.token = w.parent + most;
+    w.first = w.token + most;
+    w.path = w.first + most;
+    w.gone = w.path + most;
+  }
   const int64_t lo = min(max(p.q_starts[b], 0), p.tokens), hi = min(max(p.q_starts[b + 1], (int)lo), p.tokens);
   const int n = (int)min(hi - lo, (int64_t)p.max_q);
-  const double scale = exponent_of(p, b);
-  const bool greedy = is_greedy(p, b);
+  const Scale scale = scale_of(p, b);
+  const bool greedy = scale.greedy;
+  const double border = (double)p.finals[b];
   const Elem* logits = (const Elem*)p.logits + lo * p.row_stride;
   int64_t* out_tokens = p.out_tokens + (int64_t)b * p.max_q;
   int32_t* out_path = p.path + (int64_t)b * p.max_q;
@@ -250,268 +389,391 @@ __global__ __launch_bounds__(kWalkThreads) void walk_kernel(VerifyParams p) {
     return;
   }
 
-  // Nodes: what judges them. The weight is taken below, when the rows' largest are known.
-  float x_node = 0.0f;
-  if (tid > 0 && tid < n) {
-    int parent = tid - 1;
-    if (p.parents) {
-      parent = p.parents[lo + tid];
-      if (parent < 0 || parent >= tid) parent = -1;
+  // Nodes: what judges them. Their weights are taken below, when the rows' largest are known.
+  constexpr int kEachNode = kVerifyMaxNodes / kWalkThreads;
+  float x_node[kEachNode];
+#pragma unroll
+  for (int e = 0; e < kEachNode; ++e) {
+    const int i = tid + e * kWalkThreads;
+    x_node[e] = -kInf;
+    if (i >= n) continue;
+    int parent = i - 1;
+    if (p.parents && i > 0) {
+      parent = p.parents[lo + i];
+      if (parent < 0 || parent >= i) parent = -1;
     }
-    const int64_t id = p.ids[lo + tid];
+    const int64_t id = p.ids[lo + i];
     const bool known = id >= 0 && id < p.vocab;
-    w.parent[tid] = parent;
-    w.token[tid] = known ? (int)id : -1;
-    w.uniform[tid] = p.uniforms[lo + tid];
     const bool reads = known && parent >= 0;
-    x_node = reads ? L::one(logits[parent * p.row_stride + id]) : -kInf;
-    w.prob[tid] = reads && p.probs ? p.probs[(lo + parent) * p.probs_stride + id] : 0.0f;
-  } else if (tid == 0) {
-    w.parent[0] = -1;
-    w.token[0] = -1;
+    if (reads) x_node[e] = L::one(logits[parent * p.row_stride + id]);
+    w.parent[i] = parent;
+    w.token[i] = known ? (int)id : -1;
+    w.uniform[i] = p.uniforms[lo + i];
+    w.prob[i] = reads && p.probs ? p.probs[(lo + parent) * p.probs_stride + id] : 0.0f;
   }
-  // Rows: their chunks joined.
-  for (int i = wave; i < n; i += kWaves) {
-    const VerifyChunk* part = p.parts + (lo + i) * p.chunks;
-    float m = -kInf;
-    for (int k = lane; k < p.chunks; k += 64) m = __builtin_elementwise_maximum(m, part[k].m);
-    m = wave_max(m);
-    double s = 0.0;
-    int first = p.vocab;
-    if (m > -kInf && m < kInf) {
-      for (int k = lane; k < p.chunks; k += 64) {
-        const VerifyChunk c = part[k];
-        if (greedy) {
-          if (c.m == m) first = min(first, c.first);
-        } else if (c.m > -kInf) {
-          s += c.s * weigh(c.m, (double)m, scale);
+  // Rows: their chunks joined, 16 lanes a row.
+  {
+    const int part_lane = lane & 15;
+    for (int base = wave * 4; base < n; base += kWaves * 4) {
+      const int i = base + (lane >> 4);
+      const VerifyChunk* part = p.parts + (lo + min(i, n - 1)) * p.chunks;
+      float m = -kInf;
+      double s = 0.0;
+      int first = p.vocab;
+      constexpr int kAhead = 5;
+      for (int k0 = part_lane; k0 < p.chunks; k0 += 16 * kAhead) {
+        VerifyChunk c[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          c[j] = part[min(k0 + 16 * j, p.chunks - 1)];
+          if (k0 + 16 * j >= p.chunks) c[j].m = -kInf;
         }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) top = __builtin_elementwise_maximum(top, c[j].m);
+        if (top > m) first = p.vocab;
+        if (greedy) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (c[j].m == top) first = min(first, c[j].first);
+        } else if (top > -kInf && top < kInf) {
+          s = m > -kInf ? s * weigh(m, (double)top, scale) : 0.0;
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (c[j].m > -kInf) s += c[j].s * weigh(c[j].m, (double)top, scale);
+        }
+        m = top;
       }
-      s = greedy ? 1.0 : wave_sum(s);
+      const float top = row_max(m);
+      const bool finite = top > -kInf && top < kInf;
+      s = finite && m > -kInf ? s * weigh(m, (double)top, scale) : 0.0;
+      if (m != top) first = p.vocab;
+      s = row_sum(s);
+      first = row_min(first);
+      if (part_lane == 0 && i < n) {
+        w.most[i] = top;
+        w.sum[i] = !finite ? 0.0 : greedy ? 1.0 : s;
+        w.first[i] = first;
+      }
     }
-    first = wave_min(first);
-    if (lane == 0) {
-      w.most[i] = m;
-      w.sum[i] = s;
-      w.first[i] = first;
-    }
+  }
+  if (tid == 0) {
+    w.path[0] = 0;
+    node_ = 0;
+    len_ = 1;
+    token_ = -1;
   }
   __syncthreads();
-  if (tid > 0 && tid < n) {
-    const int parent = w.parent[tid];
-    double e = 0.0;
+#pragma unroll
+  for (int e = 0; e < kEachNode; ++e) {
+    const int i = tid + e * kWalkThreads;
+    if (i >= n) continue;
+    const int parent = w.parent[i];
+    double weight = 0.0;
     if (parent >= 0) {
       const float m = w.most[parent];
       if (m > -kInf && m < kInf)
-        e = greedy ? (w.token[tid] == w.first[parent] ? 1.0 : 0.0) : weigh(x_node, (double)m, scale);
+        weight = greedy ? (w.token[i] == w.first[parent] ? 1.0 : 0.0) : weigh(x_node[e], (double)m, scale);
     }
-    w.weight[tid] = e;
+    w.weight[i] = weight;
   }
   __syncthreads();
 
-  if (wave == 0) {
-    int node = 0, len = 1, dropped = 0;
-    bool drawn = false;
-    if (lane == 0) w.path[0] = 0;
-    for (;;) {
-      const double total = w.sum[node];
-      double removed = 0.0;
-      int found = -1;
-      dropped = 0;
-      drawn = false;
-      for (int base = (node + 1) & ~63; base < n && found < 0; base += 64) {
-        const int i = base + lane;
-        uint64_t kids = __ballot(i > node && i < n && w.parent[min(i, n - 1)] == node);
-        while (kids != 0) {
-          const int c = base + __builtin_ctzll(kids);
-          kids &= kids - 1;
-          const double weight = w.weight[c];
-          const int token = w.token[c];
-          if (p.probs) {
-            if ((double)w.uniform[c] * (double)w.prob[c] * total < weight) {
-              found = c;
-              break;
+  // Sum of mass[0..chunks), by one wave, in all its lanes; the lanes' own and what is before.
+  auto sum_mass = [&](double* mine, double* upto) {
+    const int each = (p.chunks + 63) / 64;
+    *mine = 0.0;
+    for (int k = lane * each; k < min(p.chunks, (lane + 1) * each); ++k) *mine += w.mass[k];
+    *upto = wave_prefix(*mine, lane);
+    return __shfl(*upto, 63);
+  };
+
+  // Stages that end in chunks' sums, of which there is one copy of code (as it runs once, it
+  // is as long as its instructions take to arrive): the walk up to a row whose sum is too
+  // near to tell; the last row; that row again with all its weights, where the remainder is empty.
+  enum { kWalking, kDrawing, kDrawingAll };
+  int stage = kWalking, len = 1, last = 0;
+  for (;;) {
+    int node = 0, from = wave, step = kWaves, dropped = 0;
+    const float* q = nullptr;
+    if (stage == kWalking) {
+      if (wave == 0) {
+        int at = node_, count = len_, gone = 0, need = -1;
+        bool drawn = false;
+        for (;;) {
+          const double total = w.sum[at];
+          const bool rough = !greedy && w.first[at] >= 0;
+          double removed = 0.0;
+          int found = -1;
+          gone = 0;
+          drawn = false;
+          for (int base = (at + 1) & ~63; base < n && found < 0 && need < 0; base += 64) {
+            const int i = base + lane;
+            uint64_t kids = __ballot(i > at && i < n && w.parent[min(i, n - 1)] == at);
+            while (kids != 0) {
+              const int c = base + __builtin_ctzll(kids);
+              kids &= kids - 1;
+              const double weight = w.weight[c], u = (double)w.uniform[c];
+              const int token = w.token[c];
+              if (!p.probs) {
+                bool before = token < 0;
+                for (int j = 0; j < gone; j += 64)
+                  before |= __ballot(j + lane < gone && w.gone[min(j + lane, gone - 1)] == token) != 0;
+                if (before) continue;
+              }
+              const double rate = p.probs ? u * (double)w.prob[c] : u;
+              const double least = rate * (total - removed);
+              if (rough && __builtin_fabs(least - weight) <= 0x1p-16 * rate * total) {
+                need = at;
+                break;
+              }
+              if (least < weight) {
+                found = c;
+                break;
+              }
+              drawn = p.probs != nullptr;
+              if (!drawn) {
+                if (lane == 0) w.gone[gone] = token;
+                ++gone;
+                removed += weight;
+                wave_sync();
+              }
             }
-            drawn = true;
-          } else {
-            bool before = token < 0;
-            for (int j = 0; j < dropped; j += 64)
-              before |= __ballot(j + lane < dropped && w.gone[min(j + lane, dropped - 1)] == token) != 0;
-            if (before) continue;
-            if ((double)w.uniform[c] * (total - removed) < weight) {
-              found = c;
-              break;
-            }
-            if (lane == 0) w.gone[dropped] = token;
-            ++dropped;
-            removed += weight;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            if (p.probs) break;          // a chain: there are no others
           }
+          if (found < 0) break;
+          if (lane == 0) w.path[count] = found;
+          ++count;
+          at = found;
+          wave_sync();
+        }
+        if (lane == 0) {
+          node_ = at;
+          len_ = count;
+          need_ = need;
+          dropped_ = gone;
+          drawn_ = drawn;
         }
       }
-      if (found < 0) break;
-      if (lane == 0) w.path[len] = found;
-      ++len;
-      node = found;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    if (lane == 0) {
-      w.len = len;
-      w.dropped = dropped;
-      w.drawn = drawn;
-    }
-  }
-  __syncthreads();
-  const int len = w.len, last = w.path[len - 1];
-  const float m = w.most[last];
-  const double total = w.sum[last];
-  const bool sound = m > -kInf && m < kInf;
-  bool residual = w.drawn && sound && !greedy;
-  if (!residual && group > 0) return;
-
-  const Elem* row = logits + last * p.row_stride;
-  const float* q = p.probs ? p.probs + (lo + last) * p.probs_stride : nullptr;
-  const VerifyChunk* part = p.parts + (lo + last) * p.chunks;
-  int dropped = w.dropped;
-
-  // Weights of a chunk's logits, kEach consecutive ones a lane.
-  auto chunk_weights = [&](int chunk, bool over, int drop, double* r) {
-    C c;
-    c.template load<true>(row, p.vocab, chunk, lane);
-#pragma unroll
-    for (int e = 0; e < C::kEach; ++e) {
-      r[e] = weigh(c.x[e], (double)m, scale);
-      const int i = c.first + e;
-      if (over && i >= 0 && i < p.vocab) r[e] = above(r[e], total, q[i]);
-    }
-    for (int j = 0; j < drop; ++j) {
-      const int at = w.gone[j] - c.first;
-#pragma unroll
-      for (int e = 0; e < C::kEach; ++e)
-        if (e == at) r[e] = 0.0;
-    }
-    return c.first;
-  };
-  auto lane_sum = [&](const double* r) {
-    double s = 0.0;
-#pragma unroll
-    for (int e = 0; e < C::kEach; ++e) s += r[e];
-    return s;
-  };
-
-  if (residual && p.groups > 1) {
-    for (int k = group * kWaves + wave; k < p.chunks; k += p.groups * kWaves) {
-      double r[C::kEach];
-      chunk_weights(k, true, 0, r);
-      const double s = wave_sum(lane_sum(r));
-      if (lane == 0) p.over[(int64_t)b * p.chunks + k] = s;
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      w.arrived = atomicAdd(p.counters + b, 1);
-      if (w.arrived == p.groups - 1) p.counters[b] = 0;
-    }
-    __syncthreads();
-    if (w.arrived != p.groups - 1) return;
-    __threadfence();
-  }
-  if (tid == 0) w.last_token = -1;
-  if (sound && greedy) {
-    if (tid == 0) w.last_token = w.first[last];
-  } else if (sound) {
-    const double border = (double)p.finals[b];
-    // a second time over all weights where the remainder is empty
-    for (int turn = 0; turn < 2; ++turn) {
       __syncthreads();
-      if (residual && p.groups > 1) {
-        for (int k = tid; k < p.chunks; k += kWalkThreads) w.mass[k] = p.over[(int64_t)b * p.chunks + k];
-      } else if (residual) {
-        for (int k = wave; k < p.chunks; k += kWaves) {
-          double r[C::kEach];
-          chunk_weights(k, true, 0, r);
-          const double s = wave_sum(lane_sum(r));
-          if (lane == 0) w.mass[k] = s;
+      node = need_;
+      if (node < 0) {
+        len = len_;
+        last = w.path[len - 1];
+        const bool sound = w.most[last] > -kInf && w.most[last] < kInf;
+        if (greedy || !sound) {
+          if (group > 0) return;
+          if (tid == 0 && sound) token_ = w.first[last];
+          break;
         }
-      } else {
-        for (int k = tid; k < p.chunks; k += kWalkThreads) {
-          const VerifyChunk c = part[k];
-          w.mass[k] = c.m > -kInf ? c.s * weigh(c.m, (double)m, scale) : 0.0;
+        stage = kDrawing;
+      }
+    }
+    if (stage != kWalking) node = last;
+    const Elem* row = logits + node * p.row_stride;
+    const double m = (double)w.most[node], near = w.sum[node];
+    if (stage == kDrawing) {
+      from = group * kWaves + wave;
+      step = p.groups * kWaves;
+      dropped = dropped_;
+      q = drawn_ ? p.probs + (lo + last) * p.probs_stride : nullptr;
+    }
+    double* shared = p.over + (int64_t)b * 3 * p.chunks;
+
+    // Of each chunk, by a wave: the sum of the weights without the rejected tokens, and, over
+    // a draft, the sum of max(w - near q, 0) and of the q under w.
+    for (int k = from; k < p.chunks; k += step) {
+      C c;
+      c.fetch(row, p.vocab, k, lane);
+      if (q) c.fetch_draft(q, p.vocab, row, lane);
+      double s = 0.0, over = 0.0;
+      float under = 0.0f;                // only meets the difference of two sums of the row
+#pragma unroll 1
+      for (int v = 0; v < C::kVecs; ++v) {
+        float x[L::kVec];
+        L::widen(c.raw[0], x);
+        const int first = c.index(v, 0);
+        for (int j = 0; j < dropped; ++j) {
+          const int at = w.gone[j] - first;
+#pragma unroll
+          for (int e = 0; e < L::kVec; ++e)
+            if (e == at) x[e] = -kInf;
+        }
+#pragma unroll
+        for (int e = 0; e < L::kVec; ++e) {
+          const double y = weigh_near(x[e], m, scale);
+          s += y;
+          if (q) {
+            const float d = c.draft[e / 4][e % 4];
+            const double r = __builtin_fma(-near, (double)d, y);
+            over += __builtin_fmax(r, 0.0);
+            under += r > 0.0 ? d : 0.0f;
+          }
+        }
+        c.rotate();
+      }
+      s = wave_sum(s);
+      s = s > kNothing ? s : 0.0;
+      double below = 0.0;
+      if (q) {
+        over = wave_sum(over);
+        over = over > kNothing ? over : 0.0;
+        below = wave_sum((double)under);
+      }
+      if (lane == 0) {
+        if (stage == kDrawing) {
+          store_shared(shared + k, s);
+          if (q) {
+            store_shared(shared + p.chunks + k, over);
+            store_shared(shared + 2 * p.chunks + k, below);
+          }
+        } else {
+          w.mass[k] = s;
+        }
+      }
+    }
+    double total = 0.0;
+    if (stage == kDrawing) {
+      // stores at the device's point of coherence, complete before this workgroup arrives
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __syncthreads();
+      if (p.groups > 1) {
+        if (tid == 0) {
+          arrived = __hip_atomic_fetch_add(p.counters + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          if (arrived == p.groups - 1)
+            __hip_atomic_store(p.counters + b, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         __syncthreads();
-        // chunks that lost tokens: summed again without them
-        for (int j = wave; j < dropped; j += kWaves) {
-          const int k = (w.gone[j] + C::lead(row)) / C::kSize;
-          double r[C::kEach];
-          chunk_weights(k, false, dropped, r);
-          const double s = wave_sum(lane_sum(r));
-          if (lane == 0) w.mass[k] = s;
-        }
+        if (arrived != p.groups - 1) return;
       }
-      __syncthreads();
-      if (wave == 0) {
-        const int each = (p.chunks + 63) / 64;
-        double mine = 0.0;
-        for (int k = lane * each; k < min(p.chunks, (lane + 1) * each); ++k) mine += w.mass[k];
-        const double upto = wave_prefix(mine, lane);
-        const double all = __shfl(upto, 63);
-        if (all > 0.0) {
-          const double target = border * all;
-          // the chunk whose sum passes the border; by rounding none may: the last with any
-          uint64_t passing = __ballot(upto > target && mine > 0.0);
-          const bool none = passing == 0;
-          if (none) passing = __ballot(mine > 0.0);
-          const int owner = none ? 63 - __builtin_clzll(passing) : __builtin_ctzll(passing);
-          double before = __shfl(upto - mine, owner);
-          int chunk = 0;
-          {
-            double run = before, at = before;
-            bool found = false;
-            for (int k = owner * each; k < min(p.chunks, (owner + 1) * each); ++k) {
-              if (!found && w.mass[k] > 0.0) {
-                chunk = k;
-                at = run;
-                run += w.mass[k];
-                found = !none && run > target;
-              }
-            }
-            before = at;
-          }
-          double r[C::kEach];
-          const int first = chunk_weights(chunk, residual, residual ? 0 : dropped, r);
-          const double sum = lane_sum(r);
-          const double end = before + wave_prefix(sum, lane);
-          uint64_t lanes = __ballot(end > target && sum > 0.0);
-          const bool past = lanes == 0;
-          if (past) lanes = __ballot(sum > 0.0);
-          if (lanes != 0) {
-            const int who = past ? 63 - __builtin_clzll(lanes) : __builtin_ctzll(lanes);
-            double run = end - sum;
-            int token = -1;
-            bool found = false;
+      constexpr int kEachChunk = (kVerifyMaxChunks + kWalkThreads - 1) / kWalkThreads;
+      double over[kEachChunk], under[kEachChunk];
 #pragma unroll
-            for (int e = 0; e < C::kEach; ++e) {
-              if (!found && r[e] > 0.0) {
-                token = first + e;
-                run += r[e];
-                found = !past && run > target;
-              }
-            }
-            if (lane == who) w.last_token = token;
-          }
+      for (int e = 0; e < kEachChunk; ++e) {
+        const int k = tid + e * kWalkThreads;
+        over[e] = under[e] = 0.0;
+        if (k >= p.chunks) continue;
+        w.mass[k] = load_shared(shared + k);
+        if (q) {
+          over[e] = load_shared(shared + p.chunks + k);
+          under[e] = load_shared(shared + 2 * p.chunks + k);
         }
       }
       __syncthreads();
-      if (w.last_token >= 0) break;
-      residual = false;
-      dropped = 0;
+      if (q) {
+        if (wave == 0) {
+          double mine, upto;
+          const double all = sum_mass(&mine, &upto);
+          if (lane == 0) target_ = all;
+        }
+        __syncthreads();
+        total = target_;
+#pragma unroll
+        for (int e = 0; e < kEachChunk; ++e) {
+          const int k = tid + e * kWalkThreads;
+          if (k < p.chunks) w.mass[k] = __builtin_fmax(__builtin_fma(near - total, under[e], over[e]), 0.0);
+        }
+      }
     }
+    __syncthreads();
+    if (wave == 0) {
+      // the chunk whose sum passes the border; by rounding none may: the last with any
+      double mine, upto;
+      const double all = sum_mass(&mine, &upto), target = border * all;
+      if (stage == kWalking) {
+        if (lane == 0) {
+          w.sum[node] = all;
+          w.first[node] = -1;
+        }
+      } else {
+        const int each = (p.chunks + 63) / 64;
+        uint64_t passing = __ballot(upto > target && mine > 0.0);
+        const bool none = passing == 0;
+        if (none) passing = __ballot(mine > 0.0);
+        int chunk = -1;
+        double before = 0.0;
+        if (all > 0.0 && passing != 0) {
+          const int owner = none ? 63 - __builtin_clzll(passing) : __builtin_ctzll(passing);
+          double run = __shfl(upto - mine, owner);
+          bool found = false;
+          for (int k = owner * each; k < min(p.chunks, (owner + 1) * each) && !found; ++k) {
+            if (w.mass[k] > 0.0) {
+              chunk = k;
+              before = run;
+              run += w.mass[k];
+              found = !none && run > target;
+            }
+          }
+        }
+        if (lane == 0) {
+          chunk_ = chunk;
+          before_ = before;
+          target_ = target;
+        }
+      }
+    }
+    __syncthreads();
+    if (stage == kWalking) continue;
+    if (chunk_ >= 0) {
+      // that chunk by the whole workgroup, kFew consecutive logits a thread
+      constexpr int kFew = C::kSize / kWalkThreads;
+      const int first = chunk_ * C::kSize - C::lead(row) + tid * kFew;
+      double r[kFew], sum = 0.0;
+#pragma unroll
+      for (int e = 0; e < kFew; ++e) {
+        const int i = first + e, at = min(max(i, 0), p.vocab - 1);
+        const float x = L::one(row[at]), draft = q ? q[at] : 0.0f;
+        r[e] = weigh(i == at ? x : -kInf, m, scale);
+        if (q) r[e] = i == at ? __builtin_fmax(__builtin_fma(-total, (double)draft, r[e]), 0.0) : 0.0;
+      }
+      for (int j = 0; j < dropped; ++j) {
+        const int at = w.gone[j] - first;
+#pragma unroll
+        for (int e = 0; e < kFew; ++e)
+          if (e == at) r[e] = 0.0;
+      }
+#pragma unroll
+      for (int e = 0; e < kFew; ++e) sum += r[e];
+      const double target = target_;
+      const double upto = wave_prefix(sum, lane);
+      if (lane == 63) sums_[wave] = upto;
+      if (tid == 0) who_ = kWalkThreads;
+      __syncthreads();
+      double before = before_;
+      for (int i = 0; i < wave; ++i) before += sums_[i];
+      // the first thread that passes the border, or, by rounding, the last with anything
+      const uint64_t lanes = __ballot(sum > 0.0 && before + upto > target), any = __ballot(sum > 0.0);
+      if (lane == 0 && lanes != 0) atomicMin(&who_, tid + __builtin_ctzll(lanes));
+      if (lane == 0) last_[wave] = any != 0 ? tid + 63 - __builtin_clzll(any) : -1;
+      __syncthreads();
+      int who = who_;
+      const bool past = who == kWalkThreads;
+      if (past)
+        for (int i = 0; i < kWaves; ++i) who = last_[i] >= 0 ? last_[i] : who;
+      if (tid == who) {
+        double run = before + upto - sum;
+        int token = -1;
+        bool found = false;
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) {
+          if (!found && r[e] > 0.0) {
+            token = first + e;
+            run += r[e];
+            found = !past && run > target;
+          }
+        }
+        token_ = token;
+      }
+    }
+    __syncthreads();
+    if (token_ >= 0 || stage == kDrawingAll) break;
+    stage = kDrawingAll;
   }
   __syncthreads();
   for (int i = tid; i < p.max_q; i += kWalkThreads) {
-    out_tokens[i] = i + 1 < len ? (int64_t)w.token[w.path[i + 1]] : i + 1 == len ? (int64_t)w.last_token : -1;
+    out_tokens[i] = i + 1 < len ? (int64_t)w.token[w.path[i + 1]] : i + 1 == len ? (int64_t)token_ : -1;
     out_path[i] = i < len ? w.path[i] : -1;
   }
   if (tid == 0) p.counts[b] = len;
@@ -526,7 +788,8 @@ hipError_t launch(const VerifyParams& p, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  walk_kernel<E><<<(unsigned)p.sequences * (unsigned)p.groups, kWalkThreads, 0, stream>>>(p);
+  walk_kernel<E><<<(unsigned)p.sequences * (unsigned)p.groups, kWalkThreads,
+                   walk_bytes(p.max_q > 0 ? p.max_q : 1, p.chunks), stream>>>(p);
   return hipGetLastError();
 }
 
