@@ -136,11 +136,15 @@ int64_t plan_tokens_at(int64_t tokens, int32_t adapters) {
 }
 
 // Splits of k over workgroups: as many as make one a CU, each with a step for every wave.
-int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int num_cus, int32_t* steps) {
+// us of the first kernel with 1, 3, this rule's and 8 splits: 64 tokens, k 5120, rank 16 6.9,
+// 6.8, (5) 6.1, 7.0; 384, 2112, 64 8.6, 7.9, (5) 7.6, 7.9; 8192, 5120, 64 (1) 32.2, 3 42.0.
+int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int32_t rank, int num_cus, int32_t* steps) {
   const int64_t all = div_up(k, kLoraStep);
-  const int64_t tiles = std::max<int64_t>(div_up(tokens, lora_tile_rows(tokens, adapters)), 1);
+  const int parts = lora_tile_rows(tokens, adapters) == 64 ? kLoraDownParts : 1;
+  const int64_t groups = std::max<int64_t>(div_up(tokens, 16 * parts), 1);
+  const int64_t step = lora_step(parts, lora_rank_block(rank));
   const int64_t want = std::max<int64_t>(
-      1, std::min<int64_t>({num_cus / tiles, all * kLoraStep / (64 * (kLoraDownThreads / 64)), kLoraMaxSplits}));
+      1, std::min<int64_t>({num_cus / groups, div_up(k, step * (kLoraDownThreads / 64)), kLoraMaxSplits}));
   *steps = (int32_t)div_up(all, want);
   return (int32_t)div_up(all, *steps);
 }
@@ -153,7 +157,7 @@ w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t adapters, int32_t
   if (k < 8 || k > (1 << 24) || k % 8 != 0)
     return report(W4A16_ERR_SHAPE, "k=%d must be a multiple of 8 in 8..2^24", (int)k);
   int32_t steps;
-  const int64_t splits = lora_splits(tokens, adapters, k, num_cus, &steps);
+  const int64_t splits = lora_splits(tokens, adapters, k, rank, num_cus, &steps);
   // counters, the splits' sums, v's two parts and a factor for each row
   const int64_t rows = lora_max_tiles(tokens, adapters) * lora_tile_rows(tokens, adapters);
   *bytes = tokens == 0 ? 0 : kCounterBytes + rows * (((splits > 1 ? splits : 0) + 1) * lora_rank_block(rank) + 1) * 4;
@@ -393,7 +397,7 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   p.adapters = a->adapters;
   p.rank = a->rank;
   p.tiles_most = (int32_t)lora_max_tiles(a->tokens, a->adapters);
-  p.splits = lora_splits(a->tokens, a->adapters, a->k, cus, &p.steps);
+  p.splits = lora_splits(a->tokens, a->adapters, a->k, a->rank, cus, &p.steps);
   const int rows = lora_tile_rows(a->tokens, a->adapters);
   const int64_t values = (int64_t)p.tiles_most * rows * lora_rank_block(a->rank);
   p.counters = (int32_t*)workspace;
@@ -401,9 +405,9 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   p.low = p.high + values;
   p.parts = (float*)(p.low + values);
   p.factor = p.parts + (p.splits > 1 ? p.splits : 0) * values;
-  // columns of a workgroup of the second kernel: the 256 of a step until there are 2048 of them
-  const int64_t blocks = p.tiles_most * div_up(a->n, 256);
-  p.columns = (int32_t)(256 * std::min(div_up(blocks, 2048), div_up(a->n, 256)));
+  // columns of a workgroup of the second kernel: those of a step until there are 2048 of them
+  const int64_t steps = div_up(a->n, kUpColumns);
+  p.columns = (int32_t)(kUpColumns * std::min(div_up(p.tiles_most * steps, 2048), steps));
   if ((int64_t)p.tiles_most * div_up(a->n, p.columns) > kMaxGrid)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %d columns are too many for one launch", (long long)a->tokens,
                   (int)a->n);

@@ -110,6 +110,7 @@ constexpr int kLoraMaxTokens = 1 << 24;
 constexpr int kLoraPlanThreads = 512;
 constexpr int kLoraDownThreads = 512;
 constexpr int kLoraThreads = 256;
+constexpr int kUpColumns = 256;           // of n that a workgroup of the second kernel takes at a time
 constexpr int kLoraMaxSplits = 16;
 constexpr int kLoraStep = 128;            // of k: splits are multiples
 // Rows of a tile: tokens of one adapter that are multiplied at a time.
@@ -122,6 +123,15 @@ inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
 }
 // Rank that the kernels are built for.
 __host__ __device__ constexpr int lora_rank_block(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+// Parts of 16 tokens that a workgroup of the first kernel takes of a tile of 64: fewer read a
+// again, more leave CUs idle or split k (8192 tokens, k 5120, rank 64: 1 part 43.5 us, 2 32.2,
+// 4 42.1).
+constexpr int kLoraDownParts = 2;
+// k that a wave of the first kernel takes at a time, with `tiles` of 16 tokens.
+__host__ __device__ constexpr int lora_step(int tiles, int rank_block) {
+  return tiles * (rank_block / 16) <= 2 ? 128 : 64;
+}
 
 // A plan: each tile's adapter, and each tile's tokens in ascending order, -1 behind them.
 // Rows lie where their tile is, so that a workgroup knows its rows without having seen the

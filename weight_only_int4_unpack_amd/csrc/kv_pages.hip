@@ -17,59 +17,67 @@ using namespace serve;
 // from `entry` on. Pages are handed out in the order of the list, lowest first, from those
 // that nobody held at the start: what this call takes back is for later calls, so that no
 // page that is to be read (src) is one that is to be written (dst).
+constexpr int kPagesWaves = kPagesThreads / 64;
+constexpr int kPagesFound = 2048;        // free pages that are kept from the first look
 struct PagesLds {
   int32_t row[kPagesMaxList];
   int32_t entry[kPagesMaxList];
-  int32_t upto[kPagesMaxList + 1];       // pages that the changes before i need
-  int32_t wave[kPagesThreads / 64];
-  int32_t sum;
+  uint32_t upto[kPagesMaxList + 1];      // pages that the changes before i need
+  int32_t found[kPagesFound];
+  uint32_t wave[kPagesWaves];
 };
 
-// Sum of `x` over the threads before this one; the whole in l.sum.
-__device__ __forceinline__ int block_prefix(PagesLds& l, int x, int tid) {
+// Sums stop at one more than any pool has pages: nothing behind that is served.
+constexpr uint32_t kPagesLimit = (1u << 30) + 1;
+__device__ __forceinline__ uint32_t add_pages(uint32_t x, uint32_t y) { return min(x + y, kPagesLimit); }
+
+// Sum of `x` over the threads before this one; *all: over all of them.
+__device__ __forceinline__ uint32_t block_prefix(PagesLds& l, uint32_t x, int tid, uint32_t* all) {
   const int lane = tid & 63, wave = tid >> 6;
-  int upto = x;
+  uint32_t upto = x;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
-    const int y = __shfl_up(upto, s);
-    if (lane >= s) upto += y;
+    const uint32_t y = __shfl_up(upto, s);
+    if (lane >= s) upto = add_pages(upto, y);
   }
+  const uint32_t here = __shfl_up(upto, 1);
+  __syncthreads();                       // the sums of the call before are read
   if (lane == 63) l.wave[wave] = upto;
   __syncthreads();
-  int before = 0, all = 0;
+  uint32_t before = 0, sum = 0;
 #pragma unroll
-  for (int i = 0; i < kPagesThreads / 64; ++i) {
-    const int v = l.wave[i];
-    before += i < wave ? v : 0;
-    all += v;
+  for (int i = 0; i < kPagesWaves; ++i) {
+    const uint32_t v = l.wave[i];
+    before = i < wave ? add_pages(before, v) : before;
+    sum = add_pages(sum, v);
   }
-  if (tid == 0) l.sum = all;
-  __syncthreads();
-  return before + upto - x;
+  *all = sum;
+  return lane == 0 ? before : add_pages(before, here);
 }
 
 // Calls take(k, page) with the k-th free page, k < want, in ascending order; returns how
 // many there are (stops looking when there are enough).
 template <typename Take>
-__device__ __forceinline__ int free_pages(PagesLds& l, const int32_t* refs, int pages, int want, int tid, Take take) {
+__device__ __forceinline__ uint32_t free_pages(PagesLds& l, const int32_t* refs, int pages, uint32_t want, int tid,
+                                               Take take) {
   constexpr int kEach = 8;
-  int found = 0;
-  for (int base = 0; base < pages && found < want; base += kPagesThreads * kEach) {
-    const int first = base + tid * kEach;
-    int held[kEach], mine = 0;
+  uint32_t found = 0;
+  for (int64_t base = 0; base < pages && found < want; base += kPagesThreads * kEach) {
+    const int64_t first = base + tid * kEach;
+    int held[kEach];
+    uint32_t mine = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) held[e] = first + e < pages ? refs[first + e] : 1;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) mine += held[e] == 0;
-    int k = found + block_prefix(l, mine, tid);
+    uint32_t all, k = found + block_prefix(l, mine, tid, &all);
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
       if (held[e] == 0) {
-        if (k < want) take(k, first + e);
+        if (k < want) take(k, (int)(first + e));
         ++k;
       }
-    found += l.sum;
-    __syncthreads();
+    found += all;
   }
   return found;
 }
@@ -77,10 +85,10 @@ __device__ __forceinline__ int free_pages(PagesLds& l, const int32_t* refs, int 
 template <bool FORK>
 __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
   __shared__ PagesLds l;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int size = 1 << p.page_shift;
   const int64_t room = (int64_t)p.table_pages << p.page_shift;
-  constexpr int kEach = kPagesMaxList / kPagesThreads;
+  constexpr int kEach = kPagesMaxList / kPagesThreads;   // changes of a thread: tid, tid + kPagesThreads, ...
   auto pages_of = [&](int tokens) { return (tokens >> p.page_shift) + ((tokens & (size - 1)) != 0); };
   auto length_of = [&](int row) { return (int)min((int64_t)max(p.lens[row], 0), room); };
   auto entry_of = [&](int row, int k) -> int32_t& { return p.table[row * p.table_stride + k]; };
@@ -89,114 +97,120 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     if (known(page) && atomicSub(p.refs + page, 1) <= 0) atomicAdd(p.refs + page, 1);
   };
 
-  // the rows that change: each once
+  // the rows that change, each once: a wave looks for one among those before it
   for (int i = tid; i < p.count; i += kPagesThreads) l.row[i] = FORK ? p.to[i] : p.from[i];
   __syncthreads();
-  int need[kEach], old_len[kEach], new_len[kEach];
+  for (int i = wave; i < p.count; i += kPagesWaves) {
+    const int row = l.row[i];
+    bool before = false;
+    for (int j = lane; j < i; j += 64) before |= l.row[j] == row;
+    const bool twice = __ballot(before) != 0;
+    if (lane == 0) l.entry[i] = twice;
+  }
+  __syncthreads();
+  uint32_t need[kEach], carry = 0;
+  int old_len[kEach], new_len[kEach], src[kEach], entry[kEach];
   bool good[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int i = tid * kEach + e;
+    if (e * kPagesThreads >= p.count) break;
+    const int i = tid + e * kPagesThreads;
     need[e] = 0;
+    old_len[e] = new_len[e] = entry[e] = 0;
+    src[e] = -1;
     good[e] = false;
-    old_len[e] = new_len[e] = 0;
-    if (i >= p.count) continue;
-    const int row = l.row[i];
-    bool ok = row >= 0 && row < p.rows;
-    for (int j = 0; j < i && ok; ++j) ok = l.row[j] != row;
-    int src = -1, entry = 0;
-    if constexpr (FORK) {
-      const int parent = p.from[i];
-      ok = ok && parent >= 0 && parent < p.rows && parent != row && p.lens[row] <= 0;
-      if (ok) {
-        new_len[e] = length_of(parent);
-        entry = new_len[e] >> p.page_shift;
-        if (new_len[e] & (size - 1)) {
-          need[e] = 1;
-          src = entry_of(parent, entry);
+    if (i < p.count) {
+      const int row = l.row[i];
+      bool ok = row >= 0 && row < p.rows && l.entry[i] == 0;
+      if constexpr (FORK) {
+        const int parent = p.from[i];
+        ok = ok && parent >= 0 && parent < p.rows && parent != row;
+        if (ok) {
+          const int held = p.lens[row];
+          new_len[e] = length_of(parent);
+          entry[e] = new_len[e] >> p.page_shift;
+          ok = held <= 0;
+          if (ok && (new_len[e] & (size - 1))) {
+            need[e] = 1;
+            src[e] = entry_of(parent, entry[e]);
+          }
         }
-      }
-    } else {
-      const int want = p.to[i];
-      ok = ok && want >= 0 && want <= room;
-      if (ok) {
-        old_len[e] = length_of(row);
-        new_len[e] = want;
-        const int kept = min(old_len[e], want);
-        entry = pages_of(old_len[e]);
-        need[e] = max(pages_of(want) - entry, 0);
-        if (kept & (size - 1)) {
-          const int last = kept >> p.page_shift;
-          const int page = entry_of(row, last);
-          if (known(page) && p.refs[page] > 1) {
-            src = page;
-            entry = last;
-            ++need[e];
+      } else {
+        const int want = p.to[i];
+        ok = ok && want >= 0 && want <= room;
+        if (ok) {
+          old_len[e] = length_of(row);
+          new_len[e] = want;
+          const int kept = min(old_len[e], want);
+          entry[e] = pages_of(old_len[e]);
+          need[e] = max(pages_of(want) - entry[e], 0);
+          if (kept & (size - 1)) {
+            const int last = kept >> p.page_shift;
+            const int page = entry_of(row, last);
+            if (known(page) && p.refs[page] > 1) {
+              src[e] = page;
+              entry[e] = last;
+              ++need[e];
+            }
           }
         }
       }
+      good[e] = ok;
+      src[e] = known(src[e]) ? src[e] : -1;
+      p.dst[i] = -1;
     }
-    good[e] = ok;
-    l.entry[i] = entry;
-    p.src[i] = known(src) ? src : -1;
-    p.dst[i] = -1;
+    uint32_t all;
+    const uint32_t before = add_pages(carry, block_prefix(l, need[e], tid, &all));
+    carry = add_pages(carry, all);
+    if (i < p.count) {
+      l.upto[i] = before;
+      l.entry[i] = FORK || src[e] >= 0 ? entry[e] : -1 - entry[e];   // negative: its first page is no copy
+    }
   }
-  // what the changes before each need: saturated, as nothing past the pages is served
-  {
-    int64_t mine = 0;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) mine += need[e];
-    const int lane = tid & 63, wave = tid >> 6;
-    int64_t upto = mine;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int64_t y = __shfl_up(upto, s);
-      if (lane >= s) upto += y;
-    }
-    if (lane == 63) l.wave[wave] = (int)min(upto, (int64_t)p.pages + 1);
-    __syncthreads();
-    int64_t before = upto - mine;
-    for (int i = 0; i < wave; ++i) before += l.wave[i];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = tid * kEach + e;
-      if (i <= p.count) l.upto[i] = (int)min(before, (int64_t)p.pages + 1);
-      before += need[e];
-      if (i == kPagesMaxList - 1) l.upto[i + 1] = (int)min(before, (int64_t)p.pages + 1);
-    }
-    __syncthreads();
-  }
-  const int want = l.upto[p.count];
-  const int free = want == 0 ? 0 : free_pages(l, p.refs, p.pages, want, tid, [](int, int) {});
+  if (tid == 0) l.upto[p.count] = carry;
+  __syncthreads();
+  const uint32_t want = carry;
   if (want > 0) {
-    free_pages(l, p.refs, p.pages, min(want, free), tid, [&](int k, int page) {
+    const uint32_t free = free_pages(l, p.refs, p.pages, want, tid, [&](uint32_t k, int page) {
+      if (k < kPagesFound) l.found[k] = page;
+    });
+    __syncthreads();
+    auto give = [&](uint32_t k, int page) {
       int lo = 0, hi = p.count;          // the last change with upto <= k
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (l.upto[mid] <= k) lo = mid; else hi = mid;
       }
       if (l.upto[lo + 1] > free) return;  // not served
-      entry_of(l.row[lo], l.entry[lo] + k - l.upto[lo]) = page;
+      const int at = l.entry[lo], in = k - l.upto[lo];
+      entry_of(l.row[lo], (at < 0 ? -1 - at : at) + in) = page;
       p.refs[page] = 1;
-      if (k == l.upto[lo] && (FORK || p.src[lo] >= 0)) p.dst[lo] = page;
-    });
-  }
-  __syncthreads();
+      if (in == 0 && at >= 0) p.dst[lo] = page;
+    };
+    const uint32_t given = min(want, free);
+    if (given <= kPagesFound) {
+      for (uint32_t k = tid; k < given; k += kPagesThreads) give(k, l.found[k]);
+    } else {
+      free_pages(l, p.refs, p.pages, given, tid, give);
+    }
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = tid * kEach + e;
-    if (i < p.count) good[e] = good[e] && (need[e] == 0 || l.upto[i + 1] <= free);
+    for (int e = 0; e < kEach; ++e) {
+      if (e * kPagesThreads >= p.count) break;
+      const int i = tid + e * kPagesThreads;
+      if (i < p.count && need[e] > 0 && l.upto[i + 1] > free) good[e] = false;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   // Lengths; and what is left to do for each change, which whole waves take below.
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int i = tid * kEach + e;
+    if (e * kPagesThreads >= p.count) break;
+    const int i = tid + e * kPagesThreads;
     if (i >= p.count) continue;
     const bool ok = good[e];
     p.served[i] = ok;
-    if (!ok) p.src[i] = -1;
-    if (!FORK && ok && p.src[i] >= 0) release(p.src[i]);
+    p.src[i] = ok ? src[e] : -1;
+    if (!FORK && ok && src[e] >= 0) release(src[e]);
     if (ok) p.lens[l.row[i]] = new_len[e];
     // pages: [first, last) of this row are taken back, or of the parent's row shared
     if (FORK) {
@@ -208,8 +222,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     if (!ok) l.row[i] = -1;
   }
   __syncthreads();
-  const int lane = tid & 63;
-  for (int i = tid >> 6; i < p.count; i += kPagesThreads / 64) {
+  for (int i = wave; i < p.count; i += kPagesWaves) {
     const int row = l.row[i];
     if (row < 0) continue;
     if constexpr (FORK) {
@@ -220,8 +233,9 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
         if (known(page)) atomicAdd(p.refs + page, 1);
       }
     } else {
-      for (int k = l.entry[i] + lane; k < l.upto[i]; k += 64) {
-        release(entry_of(row, k));
+      for (int k = l.entry[i] + lane; k < (int)l.upto[i]; k += 64) {
+        const int page = entry_of(row, k);
+        release(page);
         entry_of(row, k) = -1;
       }
     }

@@ -158,6 +158,12 @@ __device__ __forceinline__ int rank_of(const LoraParams& p, int adapter) {
   return p.ranks ? min(max(p.ranks[adapter], 0), p.rank) : p.rank;
 }
 
+// A wave's LDS accesses take effect in order; this holds the compiler to it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // v as two 16-bit parts; what is not finite has no second one.
 template <typename T>
 __device__ __forceinline__ void halves(const f32x8& v, u32x4* high, u32x4* low) {
@@ -191,39 +197,46 @@ __device__ __forceinline__ void wait_stores() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// ---- down: MT tiles of 16 tokens, RB ranks (padded). Where k is split over workgroups, the
+// ---- down: MT parts of 16 tokens, of SUBS that a tile has, RB ranks (padded). Where k is split over workgroups, the
 // last one to arrive adds the splits, in their order: their sums are stored and loaded at the
 // device's point of coherence (a release and acquire by fences writes back and invalidates
 // a whole L2: 64 tokens, 10 splits 48 us instead of 7).
-template <typename T, int MT, int RB>
+template <typename T, int MT, int SUBS, int RB>
 __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
   constexpr int kWaves = kLoraDownThreads / 64;
   constexpr int RT = RB / 16, kRows = 16 * MT;
-  constexpr int PIECES = MT * RT <= 2 ? 4 : 2;
-  constexpr int kStep = 32 * PIECES;
+  constexpr int kStep = lora_step(MT, RB), PIECES = kStep / 32;
   constexpr int kMeet = MT * RT < 4 ? MT * RT : 4;          // results that meet at a time
-  __shared__ f32x4 meet[kWaves][kMeet][64];
+  constexpr int kTurnA = RB < 64 ? RB : 64;                  // ranks that are turned at a time
+  constexpr int kWaveScratch = (kRows > kTurnA ? kRows : kTurnA) * (kStep + 8);
+  constexpr int kMeetBytes = kWaves * kMeet * 64 * 16, kTurnBytes = kWaves * kWaveScratch * 2;
+  __shared__ alignas(16) char shared[kMeetBytes > kTurnBytes ? kMeetBytes : kTurnBytes];
   __shared__ float whole[kRows][RB];
+  uint16_t* scratch = (uint16_t*)shared;
+  f32x4 (*meet)[kMeet][64] = (f32x4 (*)[kMeet][64])shared;
   __shared__ int arrived;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, group = lane >> 4;
   const int64_t rows = (int64_t)blockIdx.x * kRows;
-  int token[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) token[m] = token_of(p, rows + 16 * m + col);
-  const int adapter = adapter_of(p, blockIdx.x);
+  const int adapter = adapter_of(p, blockIdx.x / SUBS);
   if (adapter < 0) return;
   const int split = blockIdx.y;
   const int rank = rank_of(p, adapter);
+  // Memory is read as whole lines, kLanes lanes a row, and turned in LDS into what the matrix
+  // instructions take (read straight into their layout, where neighbouring lanes hold
+  // different rows, the first kernel took 45 us for 8192 tokens of 5120 and 64 ranks).
+  constexpr int kLanes = kStep / 8, kRowsAt = 64 / kLanes;   // lanes of a row, rows of a load
+  constexpr int kStride = kStep + 8;                         // of a row in LDS
+  constexpr int kLoadsX = kRows / kRowsAt, kLoadsA = RB / kRowsAt;
+  uint16_t* turn = scratch + wave * kWaveScratch;
+  const int line = lane / kLanes, piece = lane % kLanes;
   // rows without a token take part with another's x: each row's sums are its own
-  const uint16_t* x[MT];
-  const uint16_t* a[RT];
+  const uint16_t* x[kLoadsX];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = p.x + (int64_t)max(token[m], 0) * p.x_stride;
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    a[r] = p.a + ((int64_t)adapter * p.rank + min(16 * r + col, p.rank - 1)) * p.k;
+  for (int i = 0; i < kLoadsX; ++i)
+    x[i] = p.x + (int64_t)max(token_of(p, rows + i * kRowsAt + line), 0) * p.x_stride + piece * 8;
+  const uint16_t* a = p.a + (int64_t)adapter * p.rank * p.k + piece * 8;
   f32x4 sum[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -235,55 +248,66 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
   const int each = ((k_hi - k_lo + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
   const int from = k_lo + wave * each, to = min(k_hi, from + each);
   struct Stage {
-    u32x4 x[MT][PIECES], a[RT][PIECES];
+    u32x4 x[kLoadsX], a[kLoadsA];
   };
   auto load = [&](int k0, Stage& s) {
-    const int k = k0 + group * 8;
+    const int k = k0 + piece * 8 < to ? k0 : 0;
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) {
-      const int at = k + 32 * j < to ? k + 32 * j : 0;
+    for (int i = 0; i < kLoadsX; ++i) s.x[i] = load16(x[i] + k);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) s.x[m][j] = load16(x[m] + at);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) s.a[r][j] = load16(a[r] + at);
-    }
+    for (int i = 0; i < kLoadsA; ++i)
+      s.a[i] = load16(a + (int64_t)min(i * kRowsAt + line, p.rank - 1) * p.k + k);
   };
   auto multiply = [&](int k0, Stage& s) {
-    const int k = k0 + group * 8;
-    if (k0 + kStep > to) {
-      // past the end: zeros on both sides, as 0 x NaN is NaN
+    const bool in = k0 + piece * 8 < to;   // past the end: zeros on both sides, as 0 x NaN is NaN
+    u32x4 xs[MT][PIECES], as[RT][PIECES];
 #pragma unroll
-      for (int j = 0; j < PIECES; ++j) {
-        const bool in = k + 32 * j < to;
+    for (int i = 0; i < kLoadsX; ++i)
+      *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.x[i] : u32x4{0, 0, 0, 0};
+    wave_sync();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (!in) s.x[m][j] = u32x4{0, 0, 0, 0};
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          if (!in) s.a[r][j] = u32x4{0, 0, 0, 0};
-      }
+      for (int j = 0; j < PIECES; ++j) xs[m][j] = *(const u32x4*)&turn[(16 * m + col) * kStride + 32 * j + group * 8];
+    wave_sync();
+#pragma unroll
+    for (int h = 0; h < RB; h += kTurnA) {
+#pragma unroll
+      for (int i = 0; i < kTurnA / kRowsAt; ++i)
+        *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.a[h / kRowsAt + i] : u32x4{0, 0, 0, 0};
+      wave_sync();
+#pragma unroll
+      for (int r = 0; r < kTurnA / 16; ++r)
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j)
+          as[h / 16 + r][j] = *(const u32x4*)&turn[(16 * r + col) * kStride + 32 * j + group * 8];
+      wave_sync();
     }
 #pragma unroll
     for (int j = 0; j < PIECES; ++j)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) sum[m][r] = mfma<T>(s.a[r][j], s.x[m][j], sum[m][r]);
+        for (int r = 0; r < RT; ++r) sum[m][r] = mfma<T>(as[r][j], xs[m][j], sum[m][r]);
   };
-  // the next step's loads are on their way while one is multiplied (a step past the range
-  // loads its first values again)
+  // the next step's loads are on their way while one is multiplied
   if (from < to) {
     Stage s0, s1;
-    load(from, s0);
-    for (int k0 = from; k0 < to; k0 += 2 * kStep) {
+    int k0 = from;
+    load(k0, s0);
+    for (; k0 + 2 * kStep < to; k0 += 2 * kStep) {
       load(k0 + kStep, s1);
       multiply(k0, s0);
       load(k0 + 2 * kStep, s0);
-      if (k0 + kStep < to) multiply(k0 + kStep, s1);
+      multiply(k0 + kStep, s1);
     }
+    if (k0 + kStep < to) load(k0 + kStep, s1);
+    multiply(k0, s0);
+    if (k0 + kStep < to) multiply(k0 + kStep, s1);
   }
+  __syncthreads();                         // the scratch is the waves' sums from here on
   // The waves' sums: a lane holds ranks 16 r + 4 group .. + 3 of token 16 m + col.
-  const int64_t all_rows = (int64_t)p.tiles_most * kRows;
+  const int64_t all_rows = (int64_t)p.tiles_most * SUBS * kRows;
   float* parts = p.parts + (split * all_rows + rows) * RB;
 #pragma unroll
   for (int first = 0; first < MT * RT; first += kMeet) {
@@ -321,10 +345,10 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
     __syncthreads();
   }
   // 8 ranks of a row a thread; the RB / 8 lanes of a row are neighbours
-  constexpr int kLanes = RB / 8;
+  constexpr int kLanesV = RB / 8;
   const float scale = p.scales ? p.scales[adapter] : 1.0f;
-  for (int i = tid; i < kRows * kLanes; i += kLoraDownThreads) {
-    const int row = i / kLanes, r0 = i % kLanes * 8;
+  for (int i = tid; i < kRows * kLanesV; i += kLoraDownThreads) {
+    const int row = i / kLanesV, r0 = i % kLanesV * 8;
     f32x8 v;
     if (p.splits > 1) {
       const float* at = p.parts + (rows + row) * RB + r0;
@@ -348,7 +372,7 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int s = 1; s < kLanes; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
+      for (int s = 1; s < kLanesV; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
       const int exponent = (int)(most >> 23);
       if (exponent > 0 && exponent < 255) {
         const int lift = 127 + 14 - exponent;
@@ -370,70 +394,46 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
   }
 }
 
-#ifndef LORA_OCC
-#define LORA_OCC 2
-#endif
-#ifndef LORA_D
-#define LORA_D 4
-#endif
-// ---- up: a wave takes 64 columns of a tile at a time, one step for each of its MT parts of
-// 16 tokens. b of the columns stays in registers for the steps, v of the steps in LDS (one
-// step: in registers too). Rank blocks of 16 are one matrix instruction of depth 32, v's high
+// ---- up, small tiles and ranks: a wave takes 64 columns of a tile of 16 tokens at a time, b
+// and base a step ahead. Rank blocks of 16 are one matrix instruction of depth 32, v's high
 // parts in the first half and its low ones in the second; larger ones two for each 32 ranks.
 // b is the left operand, its rows in the order that gives a lane 8 consecutive columns of its
-// token.
-// Loads return in the order in which they were issued: base is loaded kAhead steps ahead, and
-// b of the next columns before the base that is needed after it.
-template <typename T, int MT, int RB>
-__global__ __launch_bounds__(kLoraThreads, LORA_OCC) void up_kernel(LoraParams p) {
+// token. 64 tokens of 32 adapters, 17408 columns, rank 16: 5.6 us (3.6 TB/s of b, base and out).
+template <typename T, int RB>
+__global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
   constexpr int KS = RB <= 16 ? 1 : RB / 32;
   constexpr bool kPacked = RB <= 16;
-  constexpr int kRows = 16 * MT, kColumns = 256;
-  constexpr int kAhead = MT == 1 ? 1 : LORA_D;
   constexpr int kParts = kPacked ? 1 : 2;              // loads of v for 32 ranks
-  constexpr int kStride = (kPacked ? 32 : 2 * RB) + 8; // of a row in LDS: 16 bytes apart from the banks' period
-  __shared__ uint16_t vs[MT > 1 ? kRows * kStride : 8];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, group = lane >> 4;
-  const int64_t rows = (int64_t)blockIdx.x * kRows;
-  int token[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) token[m] = token_of(p, rows + 16 * m + col);
+  const int64_t row0 = (int64_t)blockIdx.x * 16 + col;
+  const int token = token_of(p, row0);
   const int adapter = adapter_of(p, blockIdx.x);
   if (adapter == kLoraUnused) return;
   const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
-  const uint16_t* base[MT];
-  uint16_t* out[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    base[m] = p.base + (int64_t)max(token[m], 0) * p.base_stride + group * 8;
-    out[m] = p.out + (int64_t)max(token[m], 0) * p.out_stride + group * 8;
-  }
   struct Held {
     u32x4 x[2];
   };
-  auto load_base = [&](int n0, int m) {
+  const uint16_t* base = p.base + (int64_t)max(token, 0) * p.base_stride + group * 8;
+  uint16_t* out = p.out + (int64_t)max(token, 0) * p.out_stride + group * 8;
+  auto load_base = [&](int n0) {
     Held h;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       h.x[i] = u32x4{0, 0, 0, 0};
-      if (p.base && token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) h.x[i] = load16(base[m] + n0 + 32 * i);
+      if (p.base && token >= 0 && n0 + 32 * i + group * 8 < n_hi) h.x[i] = load16(base + n0 + 32 * i);
     }
     return h;
   };
+  auto store_out = [&](int n0, const Held& h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (token >= 0 && n0 + 32 * i + group * 8 < n_hi) *(u32x4*)(out + n0 + 32 * i) = h.x[i];
+  };
   if (adapter < 0) {
     if (p.base == p.out) return;
-    for (int n0 = n_lo; n0 < n_hi; n0 += kColumns) {
-      Held h[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) h[m] = load_base(n0, m);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) *(u32x4*)(out[m] + n0 + 32 * i) = h[m].x[i];
-    }
+    for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) store_out(n0, load_base(n0));
     return;
   }
   const int rank = rank_of(p, adapter);
@@ -469,37 +469,171 @@ __global__ __launch_bounds__(kLoraThreads, LORA_OCC) void up_kernel(LoraParams p
           if (r0 + e >= rank) c.x[s][j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
     }
   };
-  float factor[MT];
-  u32x4 v1[KS][kParts];                  // of the only step
-  if constexpr (MT > 1) {
-    constexpr int kLanes = RB / 8;       // 16-byte pieces of a row's high (or low) parts
-    for (int i = tid; i < 2 * kRows * kLanes; i += kLoraThreads) {
-      const int part = i / (kRows * kLanes), at = i % (kRows * kLanes);
-      *(u32x4*)&vs[at / kLanes * kStride + part * RB + at % kLanes * 8] = load16((part ? p.low : p.high) + rows * RB + at * 8);
-    }
-  } else {
+  u32x4 v[KS][kParts];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int64_t at = (rows + col) * RB + (kPacked ? (group & 1) * 8 : 32 * s + group * 8);
-      if constexpr (kPacked) {
-        v1[s][0] = load16((group < 2 ? p.high : p.low) + at);
-      } else {
-        v1[s][0] = load16(p.high + at);
-        v1[s][1] = load16(p.low + at);
-      }
+  for (int s = 0; s < KS; ++s) {
+    const int64_t at = row0 * RB + (kPacked ? (group & 1) * 8 : 32 * s + group * 8);
+    if constexpr (kPacked) {
+      v[s][0] = load16((group < 2 ? p.high : p.low) + at);
+    } else {
+      v[s][0] = load16(p.high + at);
+      v[s][1] = load16(p.low + at);
     }
   }
+  const float factor = p.factor[row0];
+  Columns next = load_b(n_lo);
+  Held held = load_base(n_lo);
+  for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) {
+    Columns c = next;
+    cut_b(c);
+    f32x4 sum[4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) factor[m] = p.factor[rows + 16 * m + col];
+    for (int j = 0; j < 4; ++j) sum[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v[s][i], sum[j]);
+    next = load_b(n0 + kUpColumns);
+    Held now = held;
+    held = load_base(n0 + kUpColumns);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x8 y = widen8<T>(now.x[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(sum[2 * i + e / 4][e % 4], factor, y[e]);
+      now.x[i] = narrow8<T>(y);
+    }
+    store_out(n0, now);
+  }
+}
+
+// ---- up, tiles of 64 tokens, or ranks above 32: as above, in MT steps of 16 tokens with b of
+// the columns in registers and v of the steps in LDS, and memory is read and written as
+// whole lines, 8 lanes a row of 64 columns; b and the products are turned in LDS, each wave
+// in a place of its own. Loads return in the order in which they were issued: base is loaded
+// kAhead steps ahead, and b of the next columns before the base that is needed after it.
+// 8192 tokens, 17408 columns, rank 64: 117 us, 4.9 TB/s of base and out (a copy: 5.2); with
+// operands read straight from memory, whose neighbouring lanes hold different rows, 162 us.
+// A third wave a SIMD has no registers for it (spills: 157 us).
+template <typename T, int MT, int RB>
+__global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p) {
+  constexpr int KS = RB <= 16 ? 1 : RB / 32;
+  constexpr bool kPacked = RB <= 16;
+  constexpr int kRows = 16 * MT, kAhead = MT == 1 ? 1 : RB > 64 ? 4 : 8;
+  constexpr int kParts = kPacked ? 1 : 2;              // loads of v for 32 ranks
+  constexpr int kStride = 2 * RB + 8;                  // of v's rows in LDS: 16 bytes off the banks' period
+  constexpr int kTurnB = RB < 64 ? RB : 64;            // ranks of b that are turned at a time
+  constexpr int kStrideB = kTurnB + 8;                 // of b's rows
+  constexpr int kStrideY = 64 + 4;                     // of the products', floats
+  constexpr int kLanesB = kTurnB / 8, kRowsB = 64 / kLanesB, kLoadsB = 64 / kRowsB, kTurns = RB / kTurnB;
+  constexpr int kBytes = 64 * kStrideB * 2 > 16 * kStrideY * 4 ? 64 * kStrideB * 2 : 16 * kStrideY * 4;
+  __shared__ alignas(16) uint16_t vs[kRows * kStride];
+  __shared__ float factors[kRows];
+  __shared__ alignas(16) char turns[4][kBytes];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, group = lane >> 4, line = lane >> 3, piece = lane & 7;
+  const int64_t rows = (int64_t)blockIdx.x * kRows;
+  int token[2 * MT];                       // of the lane's two rows of a step
+#pragma unroll
+  for (int m = 0; m < 2 * MT; ++m) token[m] = token_of(p, rows + 8 * m + line);
+  const int adapter = adapter_of(p, blockIdx.x);
+  if (adapter == kLoraUnused) return;
+  const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
+  struct Held {
+    u32x4 x[2];
+  };
+  auto load_base = [&](int n0, int m) {
+    Held h;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      h.x[i] = u32x4{0, 0, 0, 0};
+      const int64_t at = (int64_t)token[2 * m + i] * p.base_stride + n0 + piece * 8;
+      if (p.base && token[2 * m + i] >= 0 && n0 + piece * 8 < n_hi) h.x[i] = load16(p.base + at);
+    }
+    return h;
+  };
+  auto store_out = [&](int n0, int m, const Held& h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = (int64_t)token[2 * m + i] * p.out_stride + n0 + piece * 8;
+      if (token[2 * m + i] >= 0 && n0 + piece * 8 < n_hi) *(u32x4*)(p.out + at) = h.x[i];
+    }
+  };
+  if (adapter < 0) {
+    if (p.base == p.out) return;
+    for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) {
+      Held h[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) h[m] = load_base(n0, m);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) store_out(n0, m, h[m]);
+    }
+    return;
+  }
+  const int rank = rank_of(p, adapter);
+  const uint16_t* b = p.b + (int64_t)adapter * p.n * p.rank;
+  const int b_line = lane / kLanesB, b_piece = lane % kLanesB;
+  struct Columns {
+    u32x4 x[kTurns][kLoadsB];
+  };
+  // past the columns and the adapter's own rank: zeros, as 0 x NaN is NaN
+  auto load_b = [&](int n0) {
+    Columns c;
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h)
+#pragma unroll
+      for (int i = 0; i < kLoadsB; ++i) {
+        const int n = n0 + i * kRowsB + b_line, r0 = h * kTurnB + b_piece * 8;
+        c.x[h][i] = u32x4{0, 0, 0, 0};
+        if (n < n_hi && r0 < rank) c.x[h][i] = load16(b + (int64_t)n * p.rank + r0);
+      }
+    return c;
+  };
+  auto cut_b = [&](Columns& c) {
+    if ((rank & 7) == 0) return;
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h)
+#pragma unroll
+      for (int i = 0; i < kLoadsB; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (h * kTurnB + b_piece * 8 + e >= rank) c.x[h][i][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  };
+  constexpr int kLanesV = RB / 8;          // 16-byte pieces of a row's high (or low) parts
+  for (int i = tid; i < 2 * kRows * kLanesV; i += kLoraThreads) {
+    const int part = i / (kRows * kLanesV), at = i % (kRows * kLanesV);
+    *(u32x4*)&vs[at / kLanesV * kStride + part * RB + at % kLanesV * 8] = load16((part ? p.low : p.high) + rows * RB + at * 8);
+  }
+  if (tid < kRows) factors[tid] = p.factor[rows + tid];
   Columns next = load_b(n_lo);
   Held held[kAhead];
 #pragma unroll
-  for (int m = 0; m < kAhead; ++m) held[m] = load_base(n_lo + m / MT * kColumns, m % MT);
-  if constexpr (MT > 1) __syncthreads();
+  for (int m = 0; m < kAhead; ++m) held[m] = load_base(n_lo + m / MT * kUpColumns, m % MT);
+  __syncthreads();
+  uint16_t* turn_b = (uint16_t*)turns[wave];
+  float* turn_y = (float*)turns[wave];
 
-  for (int n0 = n_lo; n0 < n_hi; n0 += kColumns) {
-    Columns c = next;
-    cut_b(c);
+  for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) {
+    cut_b(next);
+    u32x4 bs[KS][4];
+    constexpr int kDeep = KS / kTurns;     // of 32 ranks, a turn
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h) {
+#pragma unroll
+      for (int i = 0; i < kLoadsB; ++i) *(u32x4*)&turn_b[(i * kRowsB + b_line) * kStrideB + b_piece * 8] = next.x[h][i];
+      wave_sync();
+#pragma unroll
+      for (int s = 0; s < kDeep; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          bs[h * kDeep + s][j] =
+              *(const u32x4*)&turn_b[(16 * j + col) * kStrideB + (kPacked ? (group & 1) * 8 : 32 * s + group * 8)];
+      wave_sync();
+    }
+    next = load_b(n0 + kUpColumns);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       f32x4 sum[4];
@@ -509,35 +643,43 @@ __global__ __launch_bounds__(kLoraThreads, LORA_OCC) void up_kernel(LoraParams p
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          u32x4 v;
-          if constexpr (MT > 1)
-            v = *(const u32x4*)&vs[(16 * m + col) * kStride + (kPacked ? group * 8 : i * RB + 32 * s + group * 8)];
-          else
-            v = v1[s][i];
+          const u32x4 v = *(const u32x4*)&vs[(16 * m + col) * kStride + (kPacked ? group * 8 : i * RB + 32 * s + group * 8)];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v, sum[j]);
+          for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(bs[s][j], v, sum[j]);
         }
-      if (m == 0) next = load_b(n0 + kColumns);
-      const Held now = held[m % kAhead];
-      held[m % kAhead] = load_base(n0 + (m + kAhead) / MT * kColumns, (m + kAhead) % MT);
+      // a lane holds columns 16 j + 4 group .. + 3 of token 16 m + col
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (token[m] >= 0 && n0 + 32 * i + group * 8 < n_hi) {
-          f32x8 y = widen8<T>(now.x[i]);
+      for (int j = 0; j < 4; ++j) *(f32x4*)&turn_y[col * kStrideY + 16 * j + 4 * group] = sum[j];
+      wave_sync();
+      Held now = held[m % kAhead];
+      held[m % kAhead] = load_base(n0 + (m + kAhead) / MT * kUpColumns, (m + kAhead) % MT);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = fmaf(sum[2 * i + e / 4][e % 4], factor[m], y[e]);
-          *(u32x4*)(out[m] + n0 + 32 * i) = narrow8<T>(y);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const f32x4 lo = *(const f32x4*)&turn_y[(8 * i + line) * kStrideY + piece * 8];
+        const f32x4 hi = *(const f32x4*)&turn_y[(8 * i + line) * kStrideY + piece * 8 + 4];
+        const float factor = factors[16 * m + 8 * i + line];
+        f32x8 y = widen8<T>(now.x[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(e < 4 ? lo[e & 3] : hi[e & 3], factor, y[e]);
+        now.x[i] = narrow8<T>(y);
+      }
+      wave_sync();
+      store_out(n0, m, now);
     }
   }
 }
 
 template <typename T, int MT, int RB>
 hipError_t launch(const LoraParams& p, hipStream_t stream) {
-  down_kernel<T, MT, RB><<<dim3(p.tiles_most, p.splits), kLoraDownThreads, 0, stream>>>(p);
+  constexpr int DOWN = MT == 4 ? kLoraDownParts : MT;
+  down_kernel<T, DOWN, MT / DOWN, RB><<<dim3(p.tiles_most * (MT / DOWN), p.splits), kLoraDownThreads, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  up_kernel<T, MT, RB><<<dim3(p.tiles_most, (p.n + p.columns - 1) / p.columns), kLoraThreads, 0, stream>>>(p);
+  const dim3 grid(p.tiles_most, (p.n + p.columns - 1) / p.columns);
+  if constexpr (MT > 1 || RB > 32)
+    up_lines_kernel<T, MT, RB><<<grid, kLoraThreads, 0, stream>>>(p);
+  else
+    up_kernel<T, RB><<<grid, kLoraThreads, 0, stream>>>(p);
   return hipGetLastError();
 }
 template <typename T, int MT>
