@@ -777,7 +777,7 @@ typedef struct {
 w4a16_status w4a16_lora(const w4a16_lora_t* args, void* workspace, int64_t ws_bytes, void* stream);
 
 /* Scratch of w4a16_lora (host only; num_cus as for w4a16_workspace_bytes). Errors: NULL, SHAPE. */
-w4a16_status w4a16_lora_workspace_bytes(int64_t tokens, int32_t k, int32_t adapters, int32_t rank,
+w4a16_status w4a16_lora_workspace_bytes(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank,
                                         int32_t num_cus, int64_t* bytes);
 
 /*

@@ -60,7 +60,7 @@ def _compact(group=None, **kw):
 
 
 def _lora(ws=P, nb=1 << 40, **kw):
-    f = dict(x=P, a=P, b=P, base=P, out=P, scales=P, ranks=P, plan=P, T=4, xs=512, bs=1024, os=1024, k=512, n=1024,
+    f = dict(x=2 * P, a=P, b=P, base=P, out=P, scales=P, ranks=P, plan=P, T=4, xs=16384, bs=1024, os=1024, k=16384, n=1024,
              R=4, rank=16, dt=1, r=0)
     f.update(kw)
     return W.lib().w4a16_lora(adapters._ARGS.pack(*f.values()), ws, nb, None)
@@ -163,7 +163,9 @@ def test_compact_refusals(kw, status):
     (dict(bs=1 << 40), W.ERR_SHAPE), (dict(x=0), W.ERR_NULL), (dict(a=0), W.ERR_NULL), (dict(b=0), W.ERR_NULL),
     (dict(out=0), W.ERR_NULL), (dict(plan=0), W.ERR_NULL), (dict(x=P + 2), W.ERR_ALIGN), (dict(plan=P + 8), W.ERR_ALIGN),
     (dict(scales=P + 2), W.ERR_ALIGN), (dict(bs=2048), W.ERR_SHAPE),   # base is out, at another stride
+    (dict(x=P), W.ERR_SHAPE),                         # out would be read as x
     (dict(nb=0), W.ERR_WORKSPACE), (dict(ws=0), W.ERR_NULL), (dict(T=0, x=0), W.OK),
+    (dict(nb=0, ws=0, xs=512, k=512), W.ERR_DEVICE),  # one kernel does both
 ])
 def test_lora_refusals(kw, status):
     assert _lora(**kw) == status
@@ -198,12 +200,15 @@ def test_scratch_and_plan_sizes():
     assert adapters.plan_bytes(1, 4) == 16 + 64 and adapters.plan_bytes(0, 4) == 0
     assert adapters.plan_bytes(64, 32) == 4 * 36 + 4 * 16 * 36
     assert adapters.plan_bytes(640, 2) == 48 + 4 * 64 * 12
-    # counters; for each of 16 rows 16 ranks in two parts and a factor, and 16 sums for each split
-    assert adapters.workspace_bytes(1, 128, 4, 8) == 65536 + 16 * (16 + 1) * 4
-    assert adapters.workspace_bytes(1, 5120, 4, 8) > 65536 + 16 * (2 * 16 + 16 + 1) * 4
-    for bad in (dict(rank=7), dict(k=4), dict(tokens=-1), dict(adapters=0)):
+    # counters; for each of 16 rows the ranks (128 or 16 here) in two parts and a factor, and the sums of each split
+    assert adapters.workspace_bytes(1, 128, 256, 4, 128) == 65536 + 16 * (128 + 1) * 4
+    assert adapters.workspace_bytes(1, 20480, 256, 4, 8) > 65536 + 16 * (2 * 16 + 16 + 1) * 4
+    # none where one kernel does both: 256 KiB of an adapter's a, a workgroup for each 512 columns
+    assert adapters.workspace_bytes(1, 16384, 256, 4, 8) == 0 != adapters.workspace_bytes(1, 16392, 256, 4, 8)
+    assert adapters.workspace_bytes(16, 512, 8192, 64, 16) == 0 != adapters.workspace_bytes(16, 512, 8200, 64, 16)
+    for bad in (dict(rank=7), dict(k=4), dict(tokens=-1), dict(adapters=0), dict(n=12)):
         with pytest.raises(W.W4A16Error):
-            adapters.workspace_bytes(**{**dict(tokens=1, k=128, adapters=4, rank=8), **bad})
+            adapters.workspace_bytes(**{**dict(tokens=1, k=128, n=256, adapters=4, rank=8), **bad})
 
 
 def test_cpu_tensors_are_refused():

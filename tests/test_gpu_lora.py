@@ -73,6 +73,25 @@ def test_against_the_oracle(T, K, N, R, rank, dtype):
     check(run(c), c)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("T,K,N,R,rank", [(1, 16384, 136, 2, 8), (1, 16392, 136, 2, 8), (40, 8192, 1032, 4, 16),
+                                          (40, 8200, 1032, 4, 16), (5, 4096, 520, 1, 32), (5, 4104, 520, 1, 32),
+                                          (3, 2048, 4104, 2, 64), (3, 2056, 4104, 2, 64), (100, 264, 8192, 30, 16),
+                                          (200, 264, 8192, 30, 64), (9, 40000, 72, 9, 48)])
+def test_one_kernel_or_two(T, K, N, R, rank, dtype):
+    # around the sizes from which on the two products are launched apart
+    c = make(K, T, K, N, R, rank, dtype)
+    check(run(c), c)
+
+
+@pytest.mark.parametrize("rank", [8, 32, 64, 128])
+@pytest.mark.parametrize("T,R,N", [(64, 64, 8200), (64, 64, 16392), (64, 64, 33000), (128, 2, 131080), (128, 2, 262152)])
+def test_workgroups_with_several_steps_of_columns(T, R, N, rank):
+    # a workgroup takes 2, 3 or 4 times 256 columns from 2048 workgroups on
+    c = make(N, T, 8, N, R, rank, "fp16" if rank == 32 else "bf16")
+    check(run(c), c)
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 511, 512, 513, 1000])
 @pytest.mark.parametrize("R", [1, 2, 7])
 def test_tile_borders(tokens, R):

@@ -12,6 +12,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import NamedTuple
 
@@ -39,11 +40,12 @@ def plan_bytes(tokens: int, adapters: int) -> int:
     return n.value
 
 
-def workspace_bytes(tokens: int, k: int, adapters: int, rank: int, num_cus: int = 256) -> int:
+@functools.lru_cache(maxsize=4096)
+def workspace_bytes(tokens: int, k: int, n: int, adapters: int, rank: int, num_cus: int = 256) -> int:
     """Scratch bytes of ``lora`` (host only)."""
-    n = ctypes.c_int64(0)
-    _W._check(_W.lib().w4a16_lora_workspace_bytes(tokens, k, adapters, rank, num_cus, ctypes.byref(n)))
-    return n.value
+    need = ctypes.c_int64(0)
+    _W._check(_W.lib().w4a16_lora_workspace_bytes(tokens, k, n, adapters, rank, num_cus, ctypes.byref(need)))
+    return need.value
 
 
 def lora_plan(index: torch.Tensor, adapters: int) -> LoraPlan:
@@ -112,7 +114,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan,
     outp, os = _rows(out, "out", code, dev, T, N)
     sp = 0 if scales is None else _array(scales, "scales", torch.float32, dev, R)
     rp = 0 if ranks is None else _array(ranks, "ranks", torch.int32, dev, R)
-    need = workspace_bytes(T, K, R, rank, _W._num_cus(dev))
+    need = workspace_bytes(T, K, N, R, rank, _W._num_cus(dev))
     ws = _W.stream_workspace(dev, need)
     _call(_W.lib().w4a16_lora, dev,
           _ARGS.pack(xp, ap, bp, basep, outp, sp, rp, plan.data.data_ptr(), T, xs, bs, os, K, N, R, rank,

@@ -149,18 +149,33 @@ int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int32_t rank, i
   return (int32_t)div_up(all, *steps);
 }
 
-w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t adapters, int32_t rank, int num_cus, int64_t* bytes) {
+// Whether one kernel does both: while all its workgroups are resident and each reads little
+// of a. us of a call replayed from a graph, with two kernels (and their scratch cleared) and
+// with one: k 1024, rank 8 (16 KiB of a) 7.2 and 3.9; 4096, 16 (128 KiB) 9.1 and 6.5; 8192, 16
+// (256 KiB) 9.5 and 9.2; 17408, 16 (544 KiB) 10.6 and 15.5; 5120, 64 (640 KiB) 11.9 and 14.0.
+constexpr int64_t kOnceBytes = 256 << 10;
+bool lora_once(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus) {
+  return lora_tile_rows(tokens, adapters) == 16 && lora_rank_block(rank) <= 64 && (int64_t)rank * k * 2 <= kOnceBytes &&
+         lora_max_tiles(tokens, adapters) * div_up(n, kOnceColumns) <= num_cus;
+}
+
+w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus,
+                            int64_t* bytes) {
   w4a16_status st = check_lora_counts(tokens, adapters);
   if (st != W4A16_OK) return st;
   if (rank < 8 || rank > 128 || rank % 8 != 0)
     return report(W4A16_ERR_SHAPE, "rank=%d must be a multiple of 8 in 8..128", (int)rank);
   if (k < 8 || k > (1 << 24) || k % 8 != 0)
     return report(W4A16_ERR_SHAPE, "k=%d must be a multiple of 8 in 8..2^24", (int)k);
+  if (n < 8 || n > (1 << 22) || n % 8 != 0)
+    return report(W4A16_ERR_SHAPE, "n=%d must be a multiple of 8 in 8..2^22", (int)n);
+  *bytes = 0;
+  if (tokens == 0 || lora_once(tokens, k, n, adapters, rank, num_cus)) return W4A16_OK;
   int32_t steps;
   const int64_t splits = lora_splits(tokens, adapters, k, rank, num_cus, &steps);
   // counters, the splits' sums, v's two parts and a factor for each row
   const int64_t rows = lora_max_tiles(tokens, adapters) * lora_tile_rows(tokens, adapters);
-  *bytes = tokens == 0 ? 0 : kCounterBytes + rows * (((splits > 1 ? splits : 0) + 1) * lora_rank_block(rank) + 1) * 4;
+  *bytes = kCounterBytes + rows * (((splits > 1 ? splits : 0) + 1) * lora_rank_block(rank) + 1) * 4;
   return W4A16_OK;
 }
 
@@ -349,19 +364,17 @@ w4a16_status w4a16_lora_plan(const int32_t* index, int64_t tokens, int32_t adapt
   return launched(launch_lora_plan(p, (hipStream_t)stream));
 }
 
-w4a16_status w4a16_lora_workspace_bytes(int64_t tokens, int32_t k, int32_t adapters, int32_t rank, int32_t num_cus,
-                                        int64_t* bytes) {
+w4a16_status w4a16_lora_workspace_bytes(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank,
+                                        int32_t num_cus, int64_t* bytes) {
   if (!bytes) return report(W4A16_ERR_NULL, "bytes must be non-NULL");
-  return lora_workspace(tokens, k, adapters, rank, num_cus > 0 ? num_cus : kWholeDevice, bytes);
+  return lora_workspace(tokens, k, n, adapters, rank, num_cus > 0 ? num_cus : kWholeDevice, bytes);
 }
 
 w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes, void* stream) {
   if (!a) return report(W4A16_ERR_NULL, "args must be non-NULL");
   CHECK(check_dtype(a->dtype));
   int64_t need;
-  CHECK(lora_workspace(a->tokens, a->k, a->adapters, a->rank, kWholeDevice, &need));
-  if (a->n < 8 || a->n > (1 << 22) || a->n % 8 != 0)
-    return report(W4A16_ERR_SHAPE, "n=%d must be a multiple of 8 in 8..2^22", (int)a->n);
+  CHECK(lora_workspace(a->tokens, a->k, a->n, a->adapters, a->rank, kWholeDevice, &need));
   CHECK(check_rows("x", a->x_stride, a->tokens, a->k, false));
   CHECK(check_rows("base", a->base ? a->base_stride : 0, a->tokens, a->n, false));
   CHECK(check_rows("out", a->out_stride, a->tokens, a->n, true));
@@ -373,9 +386,10 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
     return report(W4A16_ERR_ALIGN, "x, a, b, base, out and the plan must be 16-byte aligned, the rest to its elements");
   if (a->base == a->out && a->base_stride != a->out_stride)
     return report(W4A16_ERR_SHAPE, "in place, out needs base's stride");
+  if (a->x == a->out) return report(W4A16_ERR_SHAPE, "x must not be out: it is read while out is written");
   int cus = kWholeDevice;
   const w4a16_status device = current_device(&cus);
-  CHECK(lora_workspace(a->tokens, a->k, a->adapters, a->rank, cus, &need));
+  CHECK(lora_workspace(a->tokens, a->k, a->n, a->adapters, a->rank, cus, &need));
   CHECK(check_workspace(workspace, ws_bytes, need));
   if (device != W4A16_OK) return device;
   LoraParams p{};
@@ -408,6 +422,7 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   // columns of a workgroup of the second kernel: those of a step until there are 2048 of them
   const int64_t steps = div_up(a->n, kUpColumns);
   p.columns = (int32_t)(kUpColumns * std::min(div_up(p.tiles_most * steps, 2048), steps));
+  if (lora_once(a->tokens, a->k, a->n, a->adapters, a->rank, cus)) p.splits = 0;
   if ((int64_t)p.tiles_most * div_up(a->n, p.columns) > kMaxGrid)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %d columns are too many for one launch", (long long)a->tokens,
                   (int)a->n);

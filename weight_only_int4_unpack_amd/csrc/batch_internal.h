@@ -111,6 +111,7 @@ constexpr int kLoraPlanThreads = 512;
 constexpr int kLoraDownThreads = 512;
 constexpr int kLoraThreads = 256;
 constexpr int kUpColumns = 256;           // of n that a workgroup of the second kernel takes at a time
+constexpr int kOnceColumns = 512;         // of n that a workgroup takes that does both
 constexpr int kLoraMaxSplits = 16;
 constexpr int kLoraStep = 128;            // of k: splits are multiples
 // Rows of a tile: tokens of one adapter that are multiplied at a time.
@@ -130,7 +131,7 @@ __host__ __device__ constexpr int lora_rank_block(int rank) { return rank <= 16 
 constexpr int kLoraDownParts = 2;
 // k that a wave of the first kernel takes at a time, with `tiles` of 16 tokens.
 __host__ __device__ constexpr int lora_step(int tiles, int rank_block) {
-  return tiles * (rank_block / 16) <= 2 ? 128 : 64;
+  return tiles * (rank_block / 16) <= 2 ? 128 : tiles * (rank_block / 16) <= 8 && rank_block <= 64 ? 64 : 32;
 }
 
 // A plan: each tile's adapter, and each tile's tokens in ascending order, -1 behind them.
@@ -161,7 +162,7 @@ struct LoraParams {
   int32_t* counters;        // [tiles], zero between launches (splits > 1)
   int64_t x_stride, base_stride, out_stride;
   int32_t tokens, k, n, adapters, rank, tiles_most;
-  int32_t splits;           // of k over workgroups
+  int32_t splits;           // of k over workgroups; 0: one kernel for both
   int32_t steps;            // of kLoraStep that a split takes
   int32_t columns;          // of n that a workgroup of the second kernel takes
 };

@@ -4,10 +4,11 @@
 // A plan orders the tokens by adapter and cuts each adapter's into tiles of 16 or 64
 // tokens. Two kernels follow it. The first (down) forms v: a workgroup takes a tile and a
 // range of k, its waves parts of that range, and their sums meet in LDS; the ranges' sums
-// go to scratch in fp32. The second (up) takes a tile and a range of columns, adds the
-// ranges of v in order, and multiplies it with b as two 16-bit parts, v = high + low:
-// 16 bits of v in bf16 and 22 in fp16, each row scaled by a power of two in front of fp16
-// so that it stays in range. The products are small beside the bytes: what bounds both is
+// go to scratch in fp32, where the last workgroup of a tile adds them in their order. It
+// leaves v as two 16-bit parts, v = high + low: 16 bits of v in bf16 and 22 in fp16, each
+// row scaled by a power of two in front of fp16 so that it stays in range. The second (up)
+// takes a tile and a range of columns and multiplies both parts with b. For a few tokens
+// one kernel does both. The products are small beside the bytes: what bounds them is
 // reading x, a and b once and base and out.
 #include "batch_internal.h"
 #include "serve_device.h"
@@ -164,18 +165,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// v as two 16-bit parts; what is not finite has no second one.
-template <typename T>
-__device__ __forceinline__ void halves(const f32x8& v, u32x4* high, u32x4* low) {
-  const u32x4 h = narrow8<T>(v);
-  const f32x8 wide = widen8<T>(h);
-  f32x8 rest;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) rest[e] = __builtin_isfinite(wide[e]) ? v[e] - wide[e] : 0.0f;
-  *high = h;
-  *low = narrow8<T>(rest);
-}
-
 // Values that other workgroups read: 8 bytes at a time, past the caches that are not shared.
 __device__ __forceinline__ void store_shared(float* to, const f32x4& v) {
   typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
@@ -197,140 +186,188 @@ __device__ __forceinline__ void wait_stores() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// ---- down: MT parts of 16 tokens, of SUBS that a tile has, RB ranks (padded). Where k is split over workgroups, the
-// last one to arrive adds the splits, in their order: their sums are stored and loaded at the
-// device's point of coherence (a release and acquire by fences writes back and invalidates
-// a whole L2: 64 tokens, 10 splits 48 us instead of 7).
+// ---- down: the sums v of MT parts of 16 tokens, RB ranks (padded), over a range of k, by a
+// workgroup. Each wave takes a part of the range, and the waves' sums meet in LDS.
+// Memory is read as whole lines, kLanes lanes a row, and turned in LDS into what the matrix
+// instructions take (read straight into their layout, where neighbouring lanes hold different
+// rows, 8192 tokens of 5120 with rank 64 took 45 us instead of 32).
+template <typename T, int MT, int RB>
+struct Down {
+  static constexpr int kWaves = kLoraDownThreads / 64, kRows = 16 * MT, RT = RB / 16;
+  static constexpr int kStep = lora_step(MT, RB), kPieces = kStep / 32;
+  static constexpr int kMeet = MT * RT < 4 ? MT * RT : 4;          // results that meet at a time
+  static constexpr int kTurnA = RB < 64 ? RB : 64;                 // ranks that are turned at a time
+  static constexpr int kStride = kStep + 8;                        // of a row in LDS
+  static constexpr int kWaveTurn = (kRows > kTurnA ? kRows : kTurnA) * kStride;
+  static constexpr int kMeetBytes = kWaves * kMeet * 64 * 16, kTurnBytes = kWaves * kWaveTurn * 2;
+  static constexpr int kLdsBytes = kMeetBytes > kTurnBytes ? kMeetBytes : kTurnBytes;
+  static constexpr int kLanes = kStep / 8, kRowsAt = 64 / kLanes;  // lanes of a row, rows of a load
+  static constexpr int kLoadsX = kRows / kRowsAt, kLoadsA = RB / kRowsAt;
+  struct Stage {
+    u32x4 x[kLoadsX], a[kLoadsA];
+  };
+
+  // put(row, r, v): ranks r .. r + 3 of a row's sums (0 from the adapter's own rank on).
+  template <typename Put>
+  static __device__ __forceinline__ void sums(const LoraParams& p, char* lds, int64_t rows, int adapter, int rank,
+                                              int k_lo, int k_hi, Put put) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, group = lane >> 4, line = lane / kLanes, piece = lane % kLanes;
+    uint16_t* turn = (uint16_t*)lds + wave * kWaveTurn;
+    // rows without a token take part with another's x: each row's sums are its own
+    const uint16_t* x[kLoadsX];
+#pragma unroll
+    for (int i = 0; i < kLoadsX; ++i)
+      x[i] = p.x + (int64_t)max(token_of(p, rows + i * kRowsAt + line), 0) * p.x_stride;
+    const uint16_t* a = p.a + (int64_t)adapter * p.rank * p.k;
+    f32x4 sum[MT][RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0, 0, 0, 0};
+
+    const int each = ((k_hi - k_lo + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
+    const int from = k_lo + wave * each, to = min(k_hi, from + each);
+    auto load = [&](int k0, Stage& s) {
+      const int k = k0 + piece * 8 < to ? k0 + piece * 8 : 0;
+#pragma unroll
+      for (int i = 0; i < kLoadsX; ++i) s.x[i] = load16(x[i] + k);
+#pragma unroll
+      for (int i = 0; i < kLoadsA; ++i) s.a[i] = load16(a + (int64_t)min(i * kRowsAt + line, p.rank - 1) * p.k + k);
+    };
+    auto multiply = [&](int k0, const Stage& s) {
+      const bool in = k0 + piece * 8 < to;   // past the end: zeros on both sides, as 0 x NaN is NaN
+      u32x4 xs[MT][kPieces];
+#pragma unroll
+      for (int i = 0; i < kLoadsX; ++i)
+        *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.x[i] : u32x4{0, 0, 0, 0};
+      wave_sync();
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) xs[m][j] = *(const u32x4*)&turn[(16 * m + col) * kStride + 32 * j + group * 8];
+      wave_sync();
+#pragma unroll
+      for (int h = 0; h < RB; h += kTurnA) {
+#pragma unroll
+        for (int i = 0; i < kTurnA / kRowsAt; ++i)
+          *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.a[h / kRowsAt + i] : u32x4{0, 0, 0, 0};
+        wave_sync();
+        u32x4 as[kTurnA / 16][kPieces];
+#pragma unroll
+        for (int r = 0; r < kTurnA / 16; ++r)
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j)
+            as[r][j] = *(const u32x4*)&turn[(16 * r + col) * kStride + 32 * j + group * 8];
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < kTurnA / 16; ++r)
+              sum[m][h / 16 + r] = mfma<T>(as[r][j], xs[m][j], sum[m][h / 16 + r]);
+      }
+    };
+    // the next step's loads are on their way while one is multiplied
+    if (from < to) {
+      Stage s0, s1;
+      int k0 = from;
+      load(k0, s0);
+      for (; k0 + 2 * kStep < to; k0 += 2 * kStep) {
+        load(k0 + kStep, s1);
+        multiply(k0, s0);
+        load(k0 + 2 * kStep, s0);
+        multiply(k0 + kStep, s1);
+      }
+      if (k0 + kStep < to) load(k0 + kStep, s1);
+      multiply(k0, s0);
+      if (k0 + kStep < to) multiply(k0 + kStep, s1);
+    }
+    // the scratch holds the waves' sums from here on: a lane has ranks 16 r + 4 group .. + 3
+    // of token 16 m + col
+    f32x4 (*meet)[kMeet][64] = (f32x4 (*)[kMeet][64])lds;
+#pragma unroll
+    for (int first = 0; first < MT * RT; first += kMeet) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kMeet; ++i) meet[wave][i][lane] = sum[(first + i) / RT][(first + i) % RT];
+      __syncthreads();
+      for (int i = wave; i < kMeet; i += kWaves) {
+        f32x4 v = meet[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += meet[w][i][lane];
+        const int m = (first + i) / RT, r = (first + i) % RT;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * r + 4 * group + e >= rank) v[e] = 0.0f;
+        put(16 * m + col, 16 * r + 4 * group, v);
+      }
+    }
+  }
+};
+
+// 8 ranks of a row's v as two 16-bit parts; what is not finite has no second one. The RB / 8
+// lanes of a row are neighbours. Returns what the products are scaled by: `scale`, and in
+// fp16 a power of two that brought the row's largest magnitude to 2^14..2^15.
+template <typename T, int RB>
+__device__ __forceinline__ float in_parts(f32x8 v, float scale, u32x4* high, u32x4* low) {
+  if constexpr (T::kCode == W4A16_F16) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int s = 1; s < RB / 8; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
+    const int exponent = (int)(most >> 23);
+    if (exponent > 0 && exponent < 255) {
+      const int lift = 127 + 14 - exponent;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], lift);
+      scale = __builtin_ldexpf(scale, -lift);
+    } else if (exponent == 255) {
+      // beside what is not finite the others only must not become infinite
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (__builtin_isfinite(v[e])) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
+    }
+  }
+  const u32x4 h = narrow8<T>(v);
+  const f32x8 wide = widen8<T>(h);
+  f32x8 rest;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rest[e] = __builtin_isfinite(wide[e]) ? v[e] - wide[e] : 0.0f;
+  *high = h;
+  *low = narrow8<T>(rest);
+  return scale;
+}
+
+// SUBS workgroups a tile and split. Where k is split over workgroups, the last one to arrive
+// adds the splits, in their order: their sums are stored and loaded at the device's point of
+// coherence (a release and acquire by fences writes back and invalidates a whole L2: 64
+// tokens, 10 splits 48 us instead of 7).
 template <typename T, int MT, int SUBS, int RB>
 __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
-  constexpr int kWaves = kLoraDownThreads / 64;
-  constexpr int RT = RB / 16, kRows = 16 * MT;
-  constexpr int kStep = lora_step(MT, RB), PIECES = kStep / 32;
-  constexpr int kMeet = MT * RT < 4 ? MT * RT : 4;          // results that meet at a time
-  constexpr int kTurnA = RB < 64 ? RB : 64;                  // ranks that are turned at a time
-  constexpr int kWaveScratch = (kRows > kTurnA ? kRows : kTurnA) * (kStep + 8);
-  constexpr int kMeetBytes = kWaves * kMeet * 64 * 16, kTurnBytes = kWaves * kWaveScratch * 2;
-  __shared__ alignas(16) char shared[kMeetBytes > kTurnBytes ? kMeetBytes : kTurnBytes];
-  __shared__ float whole[kRows][RB];
-  uint16_t* scratch = (uint16_t*)shared;
-  f32x4 (*meet)[kMeet][64] = (f32x4 (*)[kMeet][64])shared;
+  using D = Down<T, MT, RB>;
+  constexpr int kRows = 16 * MT;
+  __shared__ alignas(16) char lds[D::kLdsBytes];
+  __shared__ alignas(16) float whole[kRows][RB];
   __shared__ int arrived;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, group = lane >> 4;
+  const int tid = threadIdx.x;
   const int64_t rows = (int64_t)blockIdx.x * kRows;
   const int adapter = adapter_of(p, blockIdx.x / SUBS);
   if (adapter < 0) return;
   const int split = blockIdx.y;
-  const int rank = rank_of(p, adapter);
-  // Memory is read as whole lines, kLanes lanes a row, and turned in LDS into what the matrix
-  // instructions take (read straight into their layout, where neighbouring lanes hold
-  // different rows, the first kernel took 45 us for 8192 tokens of 5120 and 64 ranks).
-  constexpr int kLanes = kStep / 8, kRowsAt = 64 / kLanes;   // lanes of a row, rows of a load
-  constexpr int kStride = kStep + 8;                         // of a row in LDS
-  constexpr int kLoadsX = kRows / kRowsAt, kLoadsA = RB / kRowsAt;
-  uint16_t* turn = scratch + wave * kWaveScratch;
-  const int line = lane / kLanes, piece = lane % kLanes;
-  // rows without a token take part with another's x: each row's sums are its own
-  const uint16_t* x[kLoadsX];
-#pragma unroll
-  for (int i = 0; i < kLoadsX; ++i)
-    x[i] = p.x + (int64_t)max(token_of(p, rows + i * kRowsAt + line), 0) * p.x_stride + piece * 8;
-  const uint16_t* a = p.a + (int64_t)adapter * p.rank * p.k + piece * 8;
-  f32x4 sum[MT][RT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0, 0, 0, 0};
-
-  // this wave's range of the split's
-  const int k_lo = split * p.steps * kLoraStep, k_hi = min(p.k, k_lo + p.steps * kLoraStep);
-  const int each = ((k_hi - k_lo + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
-  const int from = k_lo + wave * each, to = min(k_hi, from + each);
-  struct Stage {
-    u32x4 x[kLoadsX], a[kLoadsA];
-  };
-  auto load = [&](int k0, Stage& s) {
-    const int k = k0 + piece * 8 < to ? k0 : 0;
-#pragma unroll
-    for (int i = 0; i < kLoadsX; ++i) s.x[i] = load16(x[i] + k);
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i)
-      s.a[i] = load16(a + (int64_t)min(i * kRowsAt + line, p.rank - 1) * p.k + k);
-  };
-  auto multiply = [&](int k0, Stage& s) {
-    const bool in = k0 + piece * 8 < to;   // past the end: zeros on both sides, as 0 x NaN is NaN
-    u32x4 xs[MT][PIECES], as[RT][PIECES];
-#pragma unroll
-    for (int i = 0; i < kLoadsX; ++i)
-      *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.x[i] : u32x4{0, 0, 0, 0};
-    wave_sync();
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < PIECES; ++j) xs[m][j] = *(const u32x4*)&turn[(16 * m + col) * kStride + 32 * j + group * 8];
-    wave_sync();
-#pragma unroll
-    for (int h = 0; h < RB; h += kTurnA) {
-#pragma unroll
-      for (int i = 0; i < kTurnA / kRowsAt; ++i)
-        *(u32x4*)&turn[(i * kRowsAt + line) * kStride + piece * 8] = in ? s.a[h / kRowsAt + i] : u32x4{0, 0, 0, 0};
-      wave_sync();
-#pragma unroll
-      for (int r = 0; r < kTurnA / 16; ++r)
-#pragma unroll
-        for (int j = 0; j < PIECES; ++j)
-          as[h / 16 + r][j] = *(const u32x4*)&turn[(16 * r + col) * kStride + 32 * j + group * 8];
-      wave_sync();
-    }
-#pragma unroll
-    for (int j = 0; j < PIECES; ++j)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) sum[m][r] = mfma<T>(as[r][j], xs[m][j], sum[m][r]);
-  };
-  // the next step's loads are on their way while one is multiplied
-  if (from < to) {
-    Stage s0, s1;
-    int k0 = from;
-    load(k0, s0);
-    for (; k0 + 2 * kStep < to; k0 += 2 * kStep) {
-      load(k0 + kStep, s1);
-      multiply(k0, s0);
-      load(k0 + 2 * kStep, s0);
-      multiply(k0 + kStep, s1);
-    }
-    if (k0 + kStep < to) load(k0 + kStep, s1);
-    multiply(k0, s0);
-    if (k0 + kStep < to) multiply(k0 + kStep, s1);
-  }
-  __syncthreads();                         // the scratch is the waves' sums from here on
-  // The waves' sums: a lane holds ranks 16 r + 4 group .. + 3 of token 16 m + col.
   const int64_t all_rows = (int64_t)p.tiles_most * SUBS * kRows;
   float* parts = p.parts + (split * all_rows + rows) * RB;
-#pragma unroll
-  for (int first = 0; first < MT * RT; first += kMeet) {
-    if (first > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMeet; ++i) meet[wave][i][lane] = sum[(first + i) / RT][(first + i) % RT];
-    __syncthreads();
-    for (int i = wave; i < kMeet; i += kWaves) {
-      f32x4 v = meet[0][i][lane];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += meet[w][i][lane];
-      const int m = (first + i) / RT, r = (first + i) % RT;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * r + 4 * group + e >= rank) v[e] = 0.0f;
-      const int row = 16 * m + col, at = 16 * r + 4 * group;
-      if (p.splits > 1) {
-        store_shared(parts + row * RB + at, v);
-      } else {
-        *(f32x4*)&whole[row][at] = v;
-      }
-    }
-  }
+  const int k_lo = split * p.steps * kLoraStep;
+  D::sums(p, lds, rows, adapter, rank_of(p, adapter), k_lo, min(p.k, k_lo + p.steps * kLoraStep),
+          [&](int row, int r, const f32x4& v) {
+            if (p.splits > 1)
+              store_shared(parts + row * RB + r, v);
+            else
+              *(f32x4*)&whole[row][r] = v;
+          });
   if (p.splits > 1) {
     wait_stores();
     __syncthreads();
@@ -344,11 +381,10 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
   } else {
     __syncthreads();
   }
-  // 8 ranks of a row a thread; the RB / 8 lanes of a row are neighbours
-  constexpr int kLanesV = RB / 8;
+  constexpr int kLanes = RB / 8;
   const float scale = p.scales ? p.scales[adapter] : 1.0f;
-  for (int i = tid; i < kRows * kLanesV; i += kLoraDownThreads) {
-    const int row = i / kLanesV, r0 = i % kLanesV * 8;
+  for (int i = tid; i < kRows * kLanes; i += kLoraDownThreads) {
+    const int row = i / kLanes, r0 = i % kLanes * 8;
     f32x8 v;
     if (p.splits > 1) {
       const float* at = p.parts + (rows + row) * RB + r0;
@@ -365,127 +401,98 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
     } else {
       v = *(const f32x8*)&whole[row][r0];
     }
-    float factor = scale;
-    if constexpr (T::kCode == W4A16_F16) {
-      // the row's largest magnitude to 2^14..2^15, if it is finite and not 0
-      uint32_t most = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int s = 1; s < kLanesV; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
-      const int exponent = (int)(most >> 23);
-      if (exponent > 0 && exponent < 255) {
-        const int lift = 127 + 14 - exponent;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], lift);
-        factor = __builtin_ldexpf(scale, -lift);
-      } else if (exponent == 255) {
-        // beside what is not finite the others only must not become infinite
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (__builtin_isfinite(v[e])) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
-      }
-    }
     u32x4 high, low;
-    halves<T>(v, &high, &low);
+    const float factor = in_parts<T, RB>(v, scale, &high, &low);
     *(u32x4*)(p.high + (rows + row) * RB + r0) = high;
     *(u32x4*)(p.low + (rows + row) * RB + r0) = low;
     if (r0 == 0) p.factor[rows + row] = factor;
   }
 }
 
-// ---- up, small tiles and ranks: a wave takes 64 columns of a tile of 16 tokens at a time, b
-// and base a step ahead. Rank blocks of 16 are one matrix instruction of depth 32, v's high
-// parts in the first half and its low ones in the second; larger ones two for each 32 ranks.
-// b is the left operand, its rows in the order that gives a lane 8 consecutive columns of its
-// token. 64 tokens of 32 adapters, 17408 columns, rank 16: 5.6 us (3.6 TB/s of b, base and out).
+// ---- up, small tiles and ranks: a wave takes 64 columns of a tile of 16 tokens at a time. Rank
+// blocks of 16 are one matrix instruction of depth 32, v's high parts in the first half and
+// its low ones in the second; larger ones two for each 32 ranks. b is the left operand, its
+// rows in the order that gives a lane 8 consecutive columns of its token.
 template <typename T, int RB>
-__global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
-  constexpr int KS = RB <= 16 ? 1 : RB / 32;
-  constexpr bool kPacked = RB <= 16;
-  constexpr int kParts = kPacked ? 1 : 2;              // loads of v for 32 ranks
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, group = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.x * 16 + col;
-  const int token = token_of(p, row0);
-  const int adapter = adapter_of(p, blockIdx.x);
-  if (adapter == kLoraUnused) return;
-  const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
+struct Few {
+  static constexpr int KS = RB <= 16 ? 1 : RB / 32;
+  static constexpr bool kPacked = RB <= 16;
+  static constexpr int kParts = kPacked ? 1 : 2;       // operands of v for 32 ranks
   struct Held {
     u32x4 x[2];
   };
-  const uint16_t* base = p.base + (int64_t)max(token, 0) * p.base_stride + group * 8;
-  uint16_t* out = p.out + (int64_t)max(token, 0) * p.out_stride + group * 8;
-  auto load_base = [&](int n0) {
+  struct Columns {
+    u32x4 x[KS][4];
+  };
+  const uint16_t* base;                  // of the lane's token, at its first columns; null: 0
+  uint16_t* out;
+  const uint16_t* b;
+  int token, group, row, rank, n_hi, rank_all;
+
+  __device__ __forceinline__ Few(const LoraParams& p, int64_t row0, int adapter, int n_end) {
+    const int lane = threadIdx.x & 63, col = lane & 15;
+    token = token_of(p, row0 + col);
+    group = lane >> 4;
+    row = (col >> 2) * 8 + (col & 3);
+    n_hi = n_end;
+    rank_all = p.rank;
+    rank = adapter >= 0 ? rank_of(p, adapter) : 0;
+    base = p.base ? p.base + (int64_t)max(token, 0) * p.base_stride + group * 8 : nullptr;
+    out = p.out + (int64_t)max(token, 0) * p.out_stride + group * 8;
+    b = p.b + (int64_t)max(adapter, 0) * p.n * p.rank;
+  }
+  // First of the 8 ranks of the lane's operands of 32 ranks.
+  __device__ __forceinline__ int rank_at(int s) const { return kPacked ? (group & 1) * 8 : 32 * s + group * 8; }
+  __device__ __forceinline__ Held load_base(int n0) const {
     Held h;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       h.x[i] = u32x4{0, 0, 0, 0};
-      if (p.base && token >= 0 && n0 + 32 * i + group * 8 < n_hi) h.x[i] = load16(base + n0 + 32 * i);
+      if (base && token >= 0 && n0 + 32 * i + group * 8 < n_hi) h.x[i] = load16(base + n0 + 32 * i);
     }
     return h;
-  };
-  auto store_out = [&](int n0, const Held& h) {
+  }
+  __device__ __forceinline__ void store_out(int n0, const Held& h) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (token >= 0 && n0 + 32 * i + group * 8 < n_hi) *(u32x4*)(out + n0 + 32 * i) = h.x[i];
-  };
-  if (adapter < 0) {
-    if (p.base == p.out) return;
-    for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) store_out(n0, load_base(n0));
-    return;
   }
-  const int rank = rank_of(p, adapter);
-  const uint16_t* b = p.b + (int64_t)adapter * p.n * p.rank;
-  const int row = (col >> 2) * 8 + (col & 3);
-  struct Columns {
-    u32x4 x[KS][4];
-  };
-  auto load_b = [&](int n0) {
+  // past the adapter's own rank: zeros, as 0 x NaN is NaN
+  __device__ __forceinline__ Columns load_b(int n0) const {
     Columns c;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = n0 + (j >> 1) * 32 + (j & 1) * 4 + row;
         c.x[s][j] = u32x4{0, 0, 0, 0};
-        if (n < n_hi && r0 < rank) c.x[s][j] = load16(b + (int64_t)n * p.rank + r0);
+        if (n < n_hi && rank_at(s) < rank) c.x[s][j] = load16(b + (int64_t)n * rank_all + rank_at(s));
       }
-    }
     return c;
-  };
-  // past the adapter's own rank: zeros, as 0 x NaN is NaN
-  auto cut_b = [&](Columns& c) {
+  }
+  __device__ __forceinline__ void cut_b(Columns& c) const {
     if ((rank & 7) == 0) return;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int r0 = kPacked ? (group & 1) * 8 : 32 * s + group * 8;
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (r0 + e >= rank) c.x[s][j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-    }
-  };
-  u32x4 v[KS][kParts];
+          if (rank_at(s) + e >= rank) c.x[s][j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  }
+  // The lane's operands of v, from rows of RB high and RB low parts.
+  __device__ __forceinline__ void load_v(const uint16_t* high, const uint16_t* low, u32x4 (&v)[KS][kParts]) const {
 #pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const int64_t at = row0 * RB + (kPacked ? (group & 1) * 8 : 32 * s + group * 8);
-    if constexpr (kPacked) {
-      v[s][0] = load16((group < 2 ? p.high : p.low) + at);
-    } else {
-      v[s][0] = load16(p.high + at);
-      v[s][1] = load16(p.low + at);
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (kPacked) {
+        v[s][0] = load16((group < 2 ? high : low) + rank_at(s));
+      } else {
+        v[s][0] = load16(high + rank_at(s));
+        v[s][1] = load16(low + rank_at(s));
+      }
     }
   }
-  const float factor = p.factor[row0];
-  Columns next = load_b(n_lo);
-  Held held = load_base(n_lo);
-  for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) {
-    Columns c = next;
-    cut_b(c);
+  __device__ __forceinline__ Held add(Held h, const Columns& c, const u32x4 (&v)[KS][kParts], float factor) const {
     f32x4 sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = f32x4{0, 0, 0, 0};
@@ -495,33 +502,105 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
       for (int i = 0; i < kParts; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v[s][i], sum[j]);
-    next = load_b(n0 + kUpColumns);
-    Held now = held;
-    held = load_base(n0 + kUpColumns);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f32x8 y = widen8<T>(now.x[i]);
+      f32x8 y = widen8<T>(h.x[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = fmaf(sum[2 * i + e / 4][e % 4], factor, y[e]);
-      now.x[i] = narrow8<T>(y);
+      h.x[i] = narrow8<T>(y);
     }
-    store_out(n0, now);
+    return h;
   }
+};
+
+// b and base a step ahead. 64 tokens of 32 adapters, 17408 columns, rank 16: 5.6 us (3.6 TB/s
+// of b, base and out).
+template <typename T, int RB>
+__global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
+  using F = Few<T, RB>;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int adapter = adapter_of(p, blockIdx.x);
+  if (adapter == kLoraUnused) return;
+  const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
+  const F f(p, row0, adapter, n_hi);
+  if (adapter < 0) {
+    if (p.base == p.out) return;
+    for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) f.store_out(n0, f.load_base(n0));
+    return;
+  }
+  const int64_t row = row0 + (threadIdx.x & 15);
+  u32x4 v[F::KS][F::kParts];
+  f.load_v(p.high + row * RB, p.low + row * RB, v);
+  const float factor = p.factor[row];
+  typename F::Columns next = f.load_b(n_lo);
+  typename F::Held held = f.load_base(n_lo);
+  for (int n0 = n_lo; n0 < n_hi; n0 += kUpColumns) {
+    typename F::Columns c = next;
+    const typename F::Held now = held;
+    f.cut_b(c);
+    next = f.load_b(n0 + kUpColumns);
+    held = f.load_base(n0 + kUpColumns);
+    f.store_out(n0, f.add(now, c, v, factor));
+  }
+}
+
+// ---- both for a few tokens: every workgroup forms v for itself and multiplies it with its own
+// columns, whose b and base are on their way meanwhile. One launch in place of two, no
+// scratch; a is read by each workgroup (the host's rule says how much of it).
+template <typename T, int RB>
+__global__ __launch_bounds__(kLoraDownThreads) void once_kernel(LoraParams p) {
+  using D = Down<T, 1, RB>;
+  using F = Few<T, RB>;
+  __shared__ alignas(16) char lds[D::kLdsBytes];
+  __shared__ alignas(16) float whole[16][RB];
+  __shared__ alignas(16) uint16_t high[16][RB], low[16][RB];
+  __shared__ float factors[16];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int adapter = adapter_of(p, blockIdx.x);
+  if (adapter == kLoraUnused) return;
+  const int n0 = blockIdx.y * kOnceColumns + wave * 64;
+  const F f(p, row0, adapter, p.n);
+  const typename F::Held held = f.load_base(n0);
+  if (adapter < 0) {
+    if (p.base != p.out) f.store_out(n0, held);
+    return;
+  }
+  typename F::Columns c = f.load_b(n0);
+  D::sums(p, lds, row0, adapter, f.rank, 0, p.k, [&](int row, int r, const f32x4& v) { *(f32x4*)&whole[row][r] = v; });
+  __syncthreads();
+  constexpr int kLanes = RB / 8;
+  if (tid < 16 * kLanes) {
+    const int row = tid / kLanes, r0 = tid % kLanes * 8;
+    u32x4 h, l;
+    const float factor = in_parts<T, RB>(*(const f32x8*)&whole[row][r0], p.scales ? p.scales[adapter] : 1.0f, &h, &l);
+    *(u32x4*)&high[row][r0] = h;
+    *(u32x4*)&low[row][r0] = l;
+    if (r0 == 0) factors[row] = factor;
+  }
+  __syncthreads();
+  f.cut_b(c);
+  const int row = tid & 15;
+  u32x4 v[F::KS][F::kParts];
+  f.load_v(high[row], low[row], v);
+  f.store_out(n0, f.add(held, c, v, factors[row]));
 }
 
 // ---- up, tiles of 64 tokens, or ranks above 32: as above, in MT steps of 16 tokens with b of
 // the columns in registers and v of the steps in LDS, and memory is read and written as
 // whole lines, 8 lanes a row of 64 columns; b and the products are turned in LDS, each wave
 // in a place of its own. Loads return in the order in which they were issued: base is loaded
-// kAhead steps ahead, and b of the next columns before the base that is needed after it.
-// 8192 tokens, 17408 columns, rank 64: 117 us, 4.9 TB/s of base and out (a copy: 5.2); with
-// operands read straight from memory, whose neighbouring lanes hold different rows, 162 us.
-// A third wave a SIMD has no registers for it (spills: 157 us).
+// a step of columns ahead, and b of the next columns before the base that is needed after it.
+// 8192 tokens, 17408 columns, rank 64: 122-125 us, 4.6 TB/s of base and out (a copy: 5.2); with
+// operands read straight from memory, whose neighbouring lanes hold different rows, 162 us;
+// with base two steps ahead 127-131. A third wave a SIMD has no registers for it (spills: 157).
 template <typename T, int MT, int RB>
 __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p) {
   constexpr int KS = RB <= 16 ? 1 : RB / 32;
   constexpr bool kPacked = RB <= 16;
-  constexpr int kRows = 16 * MT, kAhead = MT == 1 ? 1 : RB > 64 ? 4 : 8;
+  constexpr int kRows = 16 * MT;
   constexpr int kParts = kPacked ? 1 : 2;              // loads of v for 32 ranks
   constexpr int kStride = 2 * RB + 8;                  // of v's rows in LDS: 16 bytes off the banks' period
   constexpr int kTurnB = RB < 64 ? RB : 64;            // ranks of b that are turned at a time
@@ -609,9 +688,9 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p)
   }
   if (tid < kRows) factors[tid] = p.factor[rows + tid];
   Columns next = load_b(n_lo);
-  Held held[kAhead];
+  Held held[MT];
 #pragma unroll
-  for (int m = 0; m < kAhead; ++m) held[m] = load_base(n_lo + m / MT * kUpColumns, m % MT);
+  for (int m = 0; m < MT; ++m) held[m] = load_base(n_lo, m);
   __syncthreads();
   uint16_t* turn_b = (uint16_t*)turns[wave];
   float* turn_y = (float*)turns[wave];
@@ -651,8 +730,8 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p)
 #pragma unroll
       for (int j = 0; j < 4; ++j) *(f32x4*)&turn_y[col * kStrideY + 16 * j + 4 * group] = sum[j];
       wave_sync();
-      Held now = held[m % kAhead];
-      held[m % kAhead] = load_base(n0 + (m + kAhead) / MT * kUpColumns, (m + kAhead) % MT);
+      Held now = held[m];
+      held[m] = load_base(n0 + kUpColumns, m);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const f32x4 lo = *(const f32x4*)&turn_y[(8 * i + line) * kStrideY + piece * 8];
@@ -671,6 +750,12 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p)
 
 template <typename T, int MT, int RB>
 hipError_t launch(const LoraParams& p, hipStream_t stream) {
+  if constexpr (MT == 1 && RB <= 64) {
+    if (p.splits == 0) {
+      once_kernel<T, RB><<<dim3(p.tiles_most, (p.n + kOnceColumns - 1) / kOnceColumns), kLoraDownThreads, 0, stream>>>(p);
+      return hipGetLastError();
+    }
+  }
   constexpr int DOWN = MT == 4 ? kLoraDownParts : MT;
   down_kernel<T, DOWN, MT / DOWN, RB><<<dim3(p.tiles_most * (MT / DOWN), p.splits), kLoraDownThreads, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();

@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
     L.w4a16_lora_plan.argtypes = [vp, i64, i32, vp, vp]
     L.w4a16_lora_plan_bytes.argtypes = [i64, i32, ctypes.POINTER(i64)]
     L.w4a16_lora.argtypes = [args, vp, i64, vp]
-    L.w4a16_lora_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, ctypes.POINTER(i64)]
+    L.w4a16_lora_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, ctypes.POINTER(i64)]
     for f in ("w4a16_gemm", "w4a16_gemm_bias", "w4a16_gemm_planned", "w4a16_gemm_ws",
               "w4a16_workspace_bytes", "w4a16_gemm_noalloc", "w4a16_plan", "w4a16_plan_route",
               "w4a16_dequant", "w4a16_pack_int4", "w4a16_unpack_int4", "w4a16_gemm_kpacked",
