@@ -12,3 +12,4 @@ from . import scoring  # noqa: F401  (token log probabilities, verification of d
 from . import paging  # noqa: F401  (pages of the cache: forks, copies, compaction)
 from . import adapters  # noqa: F401  (low-rank adapters beside a shared product)
 from . import serve_op  # noqa: F401  (registers torch.ops.w4a16.rope, kv_write, ...)
+from . import batch_op  # noqa: F401  (registers torch.ops.w4a16.verify_drafts, lora, ...)

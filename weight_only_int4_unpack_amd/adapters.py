@@ -33,6 +33,7 @@ class LoraPlan(NamedTuple):
     adapters: int
 
 
+@functools.lru_cache(maxsize=4096)
 def plan_bytes(tokens: int, adapters: int) -> int:
     """Bytes of a plan (host only)."""
     n = ctypes.c_int64(0)
@@ -48,16 +49,17 @@ def workspace_bytes(tokens: int, k: int, n: int, adapters: int, rank: int, num_c
     return need.value
 
 
-def lora_plan(index: torch.Tensor, adapters: int) -> LoraPlan:
+def lora_plan(index: torch.Tensor, adapters: int, nbytes: int = 0) -> LoraPlan:
     """The plan of a step whose token t takes adapter ``index[t]`` (int32
-    ``[tokens]``) of ``adapters`` (1 to 1024); anything outside, such as -1: none."""
+    ``[tokens]``) of ``adapters`` (1 to 1024); anything outside, such as -1: none.
+    Its memory has ``plan_bytes``, or ``nbytes`` if that is more."""
     if index.dim() != 1:
         raise ValueError("index must be int32 [tokens]")
     if not index.is_cuda:
         raise ValueError("all tensors must be on the same GPU")
     T, dev = index.shape[0], index.device
     at = _array(index, "index", torch.int32, dev, T)
-    data = torch.empty(plan_bytes(T, adapters), dtype=torch.uint8, device=dev)
+    data = torch.empty(max(plan_bytes(T, adapters), nbytes), dtype=torch.uint8, device=dev)
     _call(_W.lib().w4a16_lora_plan, dev, at, T, adapters, data.data_ptr())
     return LoraPlan(data, T, adapters)
 
@@ -104,8 +106,11 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan,
     bp = _array(b, "b", x.dtype, dev, R, N, rank)
     if plan.tokens != T or plan.adapters != R:
         raise ValueError(f"the plan is for {plan.tokens} tokens and {plan.adapters} adapters, not {T} and {R}")
-    if plan.data.device != dev:
+    data = plan.data
+    if data.device != dev:
         raise ValueError("all tensors must be on the same GPU")
+    if data.dtype != torch.uint8 or data.dim() != 1 or not data.is_contiguous() or data.shape[0] < plan_bytes(T, R):
+        raise ValueError("plan.data must be lora_plan's")
     basep = bs = 0
     if base is not None:
         basep, bs = _rows(base, "base", code, dev, T, N)
@@ -117,6 +122,6 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan,
     need = workspace_bytes(T, K, N, R, rank, _W._num_cus(dev))
     ws = _W.stream_workspace(dev, need)
     _call(_W.lib().w4a16_lora, dev,
-          _ARGS.pack(xp, ap, bp, basep, outp, sp, rp, plan.data.data_ptr(), T, xs, bs, os, K, N, R, rank,
+          _ARGS.pack(xp, ap, bp, basep, outp, sp, rp, data.data_ptr(), T, xs, bs, os, K, N, R, rank,
                      code, 0), _W._ptr(ws), need)
     return out
