@@ -59,7 +59,7 @@ def lora_plan(index: torch.Tensor, adapters: int, nbytes: int = 0) -> LoraPlan:
         raise ValueError("all tensors must be on the same GPU")
     T, dev = index.shape[0], index.device
     at = _array(index, "index", torch.int32, dev, T)
-    data = torch.empty(max(plan_bytes(T, adapters), nbytes), dtype=torch.uint8, device=dev)
+    data = index.new_empty(max(plan_bytes(T, adapters), nbytes), dtype=torch.uint8)
     _call(_W.lib().w4a16_lora_plan, dev, at, T, adapters, data.data_ptr())
     return LoraPlan(data, T, adapters)
 
@@ -115,7 +115,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan,
     if base is not None:
         basep, bs = _rows(base, "base", code, dev, T, N)
     if out is None:
-        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+        out = x.new_empty((T, N))
     outp, os = _rows(out, "out", code, dev, T, N)
     sp = 0 if scales is None else _array(scales, "scales", torch.float32, dev, R)
     rp = 0 if ranks is None else _array(ranks, "ranks", torch.int32, dev, R)

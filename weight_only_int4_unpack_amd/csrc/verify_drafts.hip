@@ -161,7 +161,6 @@ struct Chunk {
   using Elem = typename L::Elem;
   static constexpr int kVecs = 4, kEach = kVecs * L::kVec, kSize = 64 * kEach;
   u32x4 raw[kVecs];
-  f32x4 draft[kEach / 4];
   float x[kEach];
   int first;
 
@@ -214,47 +213,69 @@ struct Chunk {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) L::widen(raw[v], x + v * L::kVec);
   }
-  // The same places of an fp32 row: 0 outside it.
-  __device__ __forceinline__ void fetch_draft(const float* q, int vocab, const Elem* row, int lane) {
-    typedef f32x4 Loose __attribute__((aligned(4)));
-    const int at = first - lane * L::kVec;
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = index(v, 0);
-#pragma unroll
-      for (int j = 0; j < L::kVec / 4; ++j) {
-        draft[v * (L::kVec / 4) + j] = f32x4{0, 0, 0, 0};
-        if (i >= 0 && i + L::kVec <= vocab) draft[v * (L::kVec / 4) + j] = *(const Loose*)(q + i + 4 * j);
-      }
-    }
-    if (at >= 0 && at + kSize <= vocab) return;
-#pragma unroll 1
-    for (int end = 0; end < 2; ++end) {
-      const int i0 = across(row, vocab, end);
-      if (i0 < at || i0 >= at + kSize) continue;
-      const int i = i0 + lane;
-      float mine = 0.0f;
-      if (lane < L::kVec && i >= 0 && i < vocab) mine = q[i];
-#pragma unroll
-      for (int j = 0; j < L::kVec; ++j) {
-        const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-          if (index(v, 0) == i0) draft[v * (L::kVec / 4) + j / 4][j % 4] = y;
-      }
-    }
-  }
-  // The next vector to the front, for loops that are not unrolled.
-  __device__ __forceinline__ void rotate() {
-    constexpr int kDraft = L::kVec / 4;
-#pragma unroll
-    for (int v = 0; v + 1 < kVecs; ++v) raw[v] = raw[v + 1];
-#pragma unroll
-    for (int v = 0; v + kDraft < kVecs * kDraft; ++v) draft[v] = draft[v + kDraft];
-  }
   // Index in the row of logit j of vector v.
   __device__ __forceinline__ int index(int v, int j) const {
     return first + v * (64 * L::kVec) + j;
+  }
+};
+
+// One vector a lane of a chunk, and of a draft's row in the same places: -infinity, and 0,
+// outside the row.
+template <typename E, bool DRAFT>
+struct Part {
+  using C = Chunk<E>;
+  using L = Logits<E>;
+  static constexpr int kDrafts = DRAFT ? L::kVec / 4 : 1;
+  u32x4 raw;
+  f32x4 draft[kDrafts];
+  int first;
+
+  __device__ __forceinline__ void fetch(const typename L::Elem* row, const float* q, int vocab, int at, int lane) {
+    typedef f32x4 Loose __attribute__((aligned(4)));
+    first = at + lane * L::kVec;
+    if (at >= 0 && at + 64 * L::kVec <= vocab) {
+      raw = load16(row + first);
+      if constexpr (DRAFT) {
+#pragma unroll
+        for (int j = 0; j < kDrafts; ++j) draft[j] = *(const Loose*)(q + first + 4 * j);
+      }
+      return;
+    }
+    raw = u32x4{L::kNoneWord, L::kNoneWord, L::kNoneWord, L::kNoneWord};
+    const bool whole = first >= 0 && first + L::kVec <= vocab;
+    if (whole) raw = load16(row + first);
+#pragma unroll
+    for (int j = 0; j < kDrafts; ++j) {
+      draft[j] = f32x4{0, 0, 0, 0};
+      if (DRAFT && whole) draft[j] = *(const Loose*)(q + first + 4 * j);
+    }
+    // a vector across an end of the row: one logit a lane, gathered into the vector's lane
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+      const int i0 = C::across(row, vocab, end);
+      if (i0 < at || i0 >= at + 64 * L::kVec) continue;
+      const int i = i0 + lane;
+      uint32_t bits = L::kNoneWord;
+      float mine = 0.0f;
+      if (lane < L::kVec && i >= 0 && i < vocab) {
+        bits = row[i];
+        if (DRAFT) mine = q[i];
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t word = __builtin_amdgcn_readlane(bits, w);
+        if constexpr (sizeof(typename L::Elem) == 2)
+          word = (__builtin_amdgcn_readlane(bits, 2 * w) & 0xFFFFu) | __builtin_amdgcn_readlane(bits, 2 * w + 1) << 16;
+        if (first == i0) raw[w] = word;
+      }
+      if constexpr (DRAFT) {
+#pragma unroll
+        for (int j = 0; j < L::kVec; ++j) {
+          const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
+          if (first == i0) draft[j / 4][j % 4] = y;
+        }
+      }
+    }
   }
 };
 
@@ -581,20 +602,23 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     double* shared = p.over + (int64_t)b * 3 * p.chunks;
 
     // Of each chunk, by a wave: the sum of the weights without the rejected tokens, and, over
-    // a draft, the sum of max(w - near q, 0) and of the q under w.
-    for (int k = from; k < p.chunks; k += step) {
-      C c;
-      c.fetch(row, p.vocab, k, lane);
-      if (q) c.fetch_draft(q, p.vocab, row, lane);
+    // a draft, the sum of max(w - near q, 0) and of the q under w. Loads of two vectors are
+    // on their way while one is weighed.
+    auto weigh_chunks = [&](auto drafted) {
+      constexpr bool kDraft = decltype(drafted)::value;
+      using P = Part<E, kDraft>;
+      const int count = from < p.chunks ? (p.chunks - from + step - 1) / step : 0;
       double s = 0.0, over = 0.0;
       float under = 0.0f;                // only meets the difference of two sums of the row
-#pragma unroll 1
-      for (int v = 0; v < C::kVecs; ++v) {
+      auto fetch = [&](P& part, int unit) {
+        const int chunk = from + unit / C::kVecs * step;
+        part.fetch(row, q, p.vocab, chunk * C::kSize - C::lead(row) + unit % C::kVecs * (64 * L::kVec), lane);
+      };
+      auto add = [&](const P& part) {
         float x[L::kVec];
-        L::widen(c.raw[0], x);
-        const int first = c.index(v, 0);
+        L::widen(part.raw, x);
         for (int j = 0; j < dropped; ++j) {
-          const int at = w.gone[j] - first;
+          const int at = w.gone[j] - part.first;
 #pragma unroll
           for (int e = 0; e < L::kVec; ++e)
             if (e == at) x[e] = -kInf;
@@ -603,35 +627,51 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         for (int e = 0; e < L::kVec; ++e) {
           const double y = weigh_near(x[e], m, scale);
           s += y;
-          if (q) {
-            const float d = c.draft[e / 4][e % 4];
+          if constexpr (kDraft) {
+            const float d = part.draft[e / 4][e % 4];
             const double r = __builtin_fma(-near, (double)d, y);
             over += __builtin_fmax(r, 0.0);
             under += r > 0.0 ? d : 0.0f;
           }
         }
-        c.rotate();
-      }
-      s = wave_sum(s);
-      s = s > kNothing ? s : 0.0;
-      double below = 0.0;
-      if (q) {
-        over = wave_sum(over);
-        over = over > kNothing ? over : 0.0;
-        below = wave_sum((double)under);
-      }
-      if (lane == 0) {
-        if (stage == kDrawing) {
-          store_shared(shared + k, s);
-          if (q) {
-            store_shared(shared + p.chunks + k, over);
-            store_shared(shared + 2 * p.chunks + k, below);
-          }
-        } else {
-          w.mass[k] = s;
+      };
+      P part[2];
+#pragma unroll 1
+      for (int unit = -2; unit < count * C::kVecs; unit += 2) {
+        const bool more = unit + 2 < count * C::kVecs;
+        if (unit >= 0) add(part[0]);
+        if (more) fetch(part[0], unit + 2);
+        if (unit >= 0) add(part[1]);
+        if (more) fetch(part[1], unit + 3);
+        if (unit < 0 || (unit + 2) % C::kVecs != 0) continue;
+        const int k = from + unit / C::kVecs * step;
+        s = wave_sum(s);
+        s = s > kNothing ? s : 0.0;
+        double below = 0.0;
+        if constexpr (kDraft) {
+          over = wave_sum(over);
+          over = over > kNothing ? over : 0.0;
+          below = wave_sum((double)under);
         }
+        if (lane == 0) {
+          if (stage == kDrawing) {
+            store_shared(shared + k, s);
+            if constexpr (kDraft) {
+              store_shared(shared + p.chunks + k, over);
+              store_shared(shared + 2 * p.chunks + k, below);
+            }
+          } else {
+            w.mass[k] = s;
+          }
+        }
+        s = over = 0.0;
+        under = 0.0f;
       }
-    }
+    };
+    if (q)
+      weigh_chunks(std::bool_constant<true>{});
+    else
+      weigh_chunks(std::bool_constant<false>{});
     double total = 0.0;
     if (stage == kDrawing) {
       // stores at the device's point of coherence, complete before this workgroup arrives

@@ -90,8 +90,8 @@ def _change(fn, pool, first, second, names):
         raise ValueError(f"{names[0]} must be int32, 1-D")
     n = first.shape[0]
     lists = _array(first, names[0], torch.int32, dev, n), _array(second, names[1], torch.int32, dev, n)
-    out = torch.empty((3, n), dtype=torch.int32, device=dev)
-    served, src, dst = out.unbind(0)
+    out = first.new_empty((3, n))
+    served, src, dst = torch.unbind(out)
     at = out.data_ptr()
     _call(fn, dev, _PAGES.pack(*fields, *lists, at, at + 4 * n, at + 8 * n, n, 0))
     return served, src, dst
