@@ -616,9 +616,11 @@ typedef struct {
  *    r = w_i without the tokens rejected at i, or, where a drawn token was
  *    rejected, max(w_i / S_i - q_i, 0); where r is 0 everywhere, r = w_i.
  * A row that holds NaN or +infinity, or -infinity alone, has no softmax: what
- * follows it is not accepted, and its sequence's last token is -1. Sums and
- * weights are fp64: of the 2^17 borders that a draw falls between, fp32 sums
- * (off by 1e-7) move one under one draw in a hundred.
+ * follows it is not accepted, and its sequence's last token is -1. The rows'
+ * sums are fp32 where that decides an acceptance beyond doubt, and fp64 in the
+ * row that the last token is drawn from and where it does not: of the 2^17
+ * borders that a draw falls between, fp32 sums (off by 1e-7) move one under one
+ * draw in a hundred.
  * Scratch: as for w4a16_tree_attention, of at least
  * w4a16_verify_drafts_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.

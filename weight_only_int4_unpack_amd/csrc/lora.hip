@@ -29,7 +29,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 
 // ---- the plan: a counting sort of the tokens by adapter, by one workgroup. Each wave has
 // a run of consecutive tokens and counts of its own, so that the order is the tokens' own
-// within an adapter.
+// within an adapter. 64 tokens 5 us, 8192 16 us, once for all products of a step.
 constexpr int kPlanWaves = kLoraPlanThreads / 64;
 struct PlanLds {
   int32_t count[kPlanWaves][kLoraMaxAdapters + 1];
@@ -513,8 +513,8 @@ struct Few {
   }
 };
 
-// b and base a step ahead. 64 tokens of 32 adapters, 17408 columns, rank 16: 5.6 us (3.6 TB/s
-// of b, base and out).
+// b and base a step ahead. 64 tokens of 32 adapters, 17408 columns, rank 16: 6.4 us (3.5 TB/s
+// of b, base and out; vector issue 43 %, waits 63 %).
 template <typename T, int RB>
 __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
   using F = Few<T, RB>;
@@ -547,7 +547,8 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
 
 // ---- both for a few tokens: every workgroup forms v for itself and multiplies it with its own
 // columns, whose b and base are on their way meanwhile. One launch in place of two, no
-// scratch; a is read by each workgroup (the host's rule says how much of it).
+// scratch; a is read by each workgroup (the host's rule says how much of it). One token, k
+// and n 4096, rank 8: 7.0 us instead of 4.8 + 3.3, a call 10.8 instead of 15.0.
 template <typename T, int RB>
 __global__ __launch_bounds__(kLoraDownThreads) void once_kernel(LoraParams p) {
   using D = Down<T, 1, RB>;

@@ -295,7 +295,8 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& p, int row, int l
 }
 
 // Logits' weights in fp32 where the scale is an ordinary one; others (infinite and
-// vanishing temperatures) in fp64.
+// vanishing temperatures) in fp64. Bound by HBM and issue together: 288 rows of 151667 in
+// bf16 17.5 us, 5.0 TB/s, vector issue 72 % (weighed in fp64, 40 us).
 template <typename E>
 __global__ __launch_bounds__(kVerifyThreads) void weigh_kernel(VerifyParams p) {
   using C = Chunk<E>;
@@ -364,6 +365,11 @@ __device__ __forceinline__ double load_shared(const double* from) {
   return __builtin_bit_cast(double, __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
+// A chain of loads and barriers: one sequence over 32000 logits 14.6 us, of which its nodes
+// 1.6, the rows' join and the walk 2.6, the chunks 5.2, hand-off, sums and border 3, the last
+// chunk and the outputs 2.5. 64 chains over 151667 with drafts 32 us: the chunks' 58 MB take 15
+// (HBM 11; vector issue is 53 % of all), where a chunk's loads at once, not two vectors
+// ahead, took 20.
 template <typename E>
 __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   using C = Chunk<E>;
