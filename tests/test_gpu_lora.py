@@ -224,6 +224,37 @@ def test_many_adapters_and_many_tokens():
     check(run(c), c)
 
 
+@pytest.mark.parametrize("T", [6, 200])
+def test_offsets_past_32_bits(T):
+    # rows of x, base and out and adapters that lie past 2^31 elements: as those side by side
+    K, N, R, rank = 40000, 264, 1024, 64
+    c = make(20, T, K, N, 2, rank, index=[0, 1, -1] * (T // 3) + [1] * (T % 3))
+    a = torch.empty((R, rank, K), dtype=torch.bfloat16, device="cuda")
+    b = torch.empty((R, 40000, rank), dtype=torch.bfloat16, device="cuda")
+    assert a.numel() > 1 << 31 and b.numel() > 1 << 31
+    a[[0, R - 1]], at = c["a"].cuda(), (1 << 32) // T // 8 * 8
+    wide = torch.empty(at * T, dtype=torch.bfloat16, device="cuda")
+    x, base = wide.as_strided((T, K), (at, 1)), wide.as_strided((T, N), (at, 1), K)
+    x.copy_(c["x"])
+    base.copy_(c["base"])
+    b = b.view(-1)[:R * N * rank].view(R, N, rank) if T == 6 else b
+    full = torch.zeros((2, b.shape[1], rank)).bfloat16()
+    full[:, :N] = c["b"]
+    b[[0, R - 1]] = full.cuda()
+    index = [R - 1 if i == 1 else i for i in c["index"]]
+    scales = torch.ones(R, device="cuda")
+    scales[[0, R - 1]] = c["scales"].cuda()
+    plan = adapters.lora_plan(ints(index), R)
+    if T == 6:
+        out = wide.as_strided((T, N), (at, 1), K + N)
+        got = adapters.lora(x, a, b, plan, base=base, scales=scales, out=out)
+    else:
+        got = adapters.lora(x, a, b, plan, scales=scales)
+        assert not got[:, N:].any()
+        c["base"], got = None, got[:, :N]
+    check(got, c)
+
+
 def test_plan_keeps_the_order_of_tokens():
     g = np.random.default_rng(3)
     for T, R in ((1, 1), (64, 32), (5000, 3), (5000, 1024), (70000, 40)):
@@ -249,8 +280,9 @@ def test_no_tokens():
     assert run(c).shape == (0, 40)
 
 
-def test_captured_and_replayed_with_other_adapters():
-    c = make(17, 48, 520, 264, 6, 16)
+@pytest.mark.parametrize("K,rank", [(520, 16), (12288, 16), (520, 96)])    # one kernel; two, with and without splits
+def test_captured_and_replayed_with_other_adapters(K, rank):
+    c = make(17, 48, K, 264, 6, rank)
     d = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
     index = ints(c["index"])
 
@@ -273,8 +305,9 @@ def test_captured_and_replayed_with_other_adapters():
         assert torch.equal(out, step())
 
 
-def test_two_streams_at_once():
-    cs = [make(s, 64, 2048, 1024, 8, 32) for s in (18, 19)]
+@pytest.mark.parametrize("K,rank", [(2048, 32), (12288, 32)])
+def test_two_streams_at_once(K, rank):
+    cs = [make(s, 64, K, 1024, 8, rank) for s in (18, 19)]
     want = [run(c) for c in cs]
     dev = [{k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)} for c in cs]
     plans = [adapters.lora_plan(ints(c["index"]), 8) for c in cs]

@@ -102,6 +102,21 @@ def test_rows_of_draft_probabilities_that_lie_apart():
     same(call(c, draft_probs=wide[:, 3:3004]), want(c))
 
 
+@pytest.mark.parametrize("mode", ["given", "drawn"])
+def test_offsets_past_32_bits(mode):
+    # the last sequence's rows lie past 2^31 logits (and probabilities): as the same rows alone
+    c = make(7, [4, 4], 151667, "bf16", False, mode == "drawn")
+    T, V = 14400, 151667
+    logits = torch.zeros((T, V), dtype=torch.bfloat16, device="cuda")
+    assert (T - 4) * V > 1 << 31
+    place = lambda x: torch.cat([x[:4], x.new_zeros((T - 8, *x.shape[1:])), x[4:]])                   # noqa: E731
+    logits[:4], logits[-4:] = c["logits"][:4], c["logits"][4:]
+    probs = None if c["q"] is None else place(cuda(c["q"]))
+    got = scoring.verify_drafts(logits, place(cuda(c["ids"], torch.int64)), cuda([0, 4, T - 4, T], torch.int32), 4,
+                                place(cuda(c["u"])), cuda([c["final"][0], 0.5, c["final"][1]]), draft_probs=probs)
+    same([x[[0, 2]] for x in got], want(c))
+
+
 @pytest.mark.parametrize("mode", ["given", "tree", "drawn"])
 def test_many_sequences(mode):
     # more than the second kernel's workgroups of a sequence share, and more than one look at q_starts
