@@ -191,10 +191,10 @@ def test_null_arguments():
 
 
 def test_scratch_and_plan_sizes():
-    # counters, then 16 bytes a chunk and row, 24 a chunk and sequence; the chunks of a row may
-    # start up to 7 logits before it
-    assert scoring.verify_workspace_bytes(6, 2041, 2, 3, torch.bfloat16) == 65536 + 6 * 16 + 2 * 24
-    assert scoring.verify_workspace_bytes(6, 2042, 2, 3, torch.bfloat16) == 65536 + 2 * (6 * 16 + 2 * 24)
+    # counters, then 16 bytes a chunk of 2048 and row, 24 a span of 1024 and sequence; those of a
+    # row may start up to 7 logits before it
+    assert scoring.verify_workspace_bytes(6, 2041, 2, 3, torch.bfloat16) == 65536 + 6 * 16 + 2 * 2 * 24
+    assert scoring.verify_workspace_bytes(6, 2042, 2, 3, torch.bfloat16) == 65536 + 2 * 6 * 16 + 3 * 2 * 24
     assert scoring.verify_workspace_bytes(0, 2042, 2, 3, torch.float32) == 0
     # 4 bytes a tile, in whole 16, and 4 for each of its 16 or 64 rows
     assert adapters.plan_bytes(1, 4) == 16 + 64 and adapters.plan_bytes(0, 4) == 0

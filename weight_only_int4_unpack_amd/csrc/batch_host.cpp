@@ -14,11 +14,11 @@ namespace {
 using namespace checks;
 
 // ---- verification of drafts
-int32_t verify_groups(int64_t sequences, int chunks, int num_cus) {
-  // Workgroups of a sequence that share the last row: a chunk a wave, while all of them are
+int32_t verify_groups(int64_t sequences, int spans, int num_cus) {
+  // Workgroups of a sequence that share the last row: a span a wave, while all of them are
   // resident; counters bound how many sequences may have several.
   if (sequences > kCounterBytes / 4) return 1;
-  const int64_t most = div_up(chunks, kWalkThreads / 64);
+  const int64_t most = div_up(spans, kWalkThreads / 64);
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>(most, 2 * (int64_t)num_cus / std::max<int64_t>(sequences, 1)));
 }
 
@@ -39,7 +39,7 @@ w4a16_status verify_workspace(int64_t tokens, int64_t vocab, int32_t sequences, 
   if (tokens > kMaxGrid * (kVerifyThreads / 64) / chunks)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %lld logits are too many for one launch", (long long)tokens,
                   (long long)vocab);
-  *bytes = tokens == 0 ? 0 : kCounterBytes + tokens * chunks * (int64_t)sizeof(VerifyChunk) + sequences * chunks * 24;
+  *bytes = tokens == 0 ? 0 : kCounterBytes + tokens * chunks * (int64_t)sizeof(VerifyChunk) + sequences * verify_spans(vocab) * (int64_t)24;
   return W4A16_OK;
 }
 
@@ -241,7 +241,8 @@ w4a16_status w4a16_verify_drafts(const w4a16_verify_drafts_t* a, void* workspace
   p.sequences = a->sequences;
   p.max_q = a->max_q;
   p.chunks = verify_chunks(a->vocab, a->dtype);
-  p.groups = a->tokens > 0 ? verify_groups(a->sequences, p.chunks, cus) : 1;
+  p.spans = verify_spans(a->vocab);
+  p.groups = a->tokens > 0 ? verify_groups(a->sequences, p.spans, cus) : 1;
   if (need > 0) {
     p.counters = (int32_t*)workspace;
     p.parts = (VerifyChunk*)((char*)workspace + kCounterBytes);

@@ -5,17 +5,17 @@
 // logits, finds its largest m and sums 2^((x - m) c), c = log2(e) / temperature. It is one
 // pass over the logits. The second has one or more workgroups for a sequence: it joins the
 // chunks' sums of the sequence's rows, weighs the drafted tokens, walks from node to node,
-// and draws the last token from the last node's row, whose chunks it sums again in fp64: the
-// chunk in which the cumulative sum passes the border from those sums, the logit from that
-// chunk alone. All workgroups of a sequence walk alike and share the chunks; whoever is last
-// draws.
+// and draws the last token from the last node's row, which it sums again in fp64, by spans of
+// 1024: the span in which the cumulative sum passes the border from those sums, the logit
+// from that span alone. All workgroups of a sequence walk alike and share the spans; whoever
+// is last draws.
 //
 // What needs fp64: a draw is a border in a cumulative sum over 2^17 terms, and rounding moves
 // one draw in 1 / (terms x rounding), a hundred with fp32 and 10^8 with sums that are right
 // to 2^-46. A token is accepted by one comparison; where the row's fp32 sum is too near to
 // tell (2^-16 of it, some 16 times its error), the row is summed in fp64 and compared again.
 // Where a drawn token was rejected, max(w - S q, 0) is summed with S of the first kernel,
-// together with the sum Q of the q under w: with the exact S, known when all chunks are, the
+// together with the sum Q of the q under w: with the exact S, known when all spans are, the
 // sum is that plus (S_first - S) Q (what changes sides on the way is 2^-24 of 2^-24).
 #include <climits>
 
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(kVerifyThreads) void weigh_kernel(VerifyParams p) {
 struct Walk {
   double* weight;                        // of a node's token at its parent
   double* sum;                           // of the weights of a node's row
-  double* mass;                          // of a row's chunks
+  double* mass;                          // of a row's spans
   float* most;                           // a row's largest logit; not finite: no softmax
   float* uniform;
   float* prob;
@@ -352,7 +352,7 @@ struct Walk {
   int* gone;                             // tokens rejected at the last node, each once
 };
 constexpr int kNodeBytes = 2 * 8 + 8 * 4;
-__host__ __device__ constexpr int walk_bytes(int nodes, int chunks) { return nodes * kNodeBytes + chunks * 8; }
+__host__ __device__ constexpr int walk_bytes(int nodes, int spans) { return nodes * kNodeBytes + spans * 8; }
 
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -365,11 +365,9 @@ __device__ __forceinline__ double load_shared(const double* from) {
   return __builtin_bit_cast(double, __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
-// A chain of loads and barriers: one sequence over 32000 logits 14.6 us, of which its nodes
-// 1.6, the rows' join and the walk 2.6, the chunks 5.2, hand-off, sums and border 3, the last
-// chunk and the outputs 2.5. 64 chains over 151667 with drafts 32 us: the chunks' 58 MB take 15
-// (HBM 11; vector issue is 53 % of all), where a chunk's loads at once, not two vectors
-// ahead, took 20.
+// A chain of loads and barriers: one sequence over 32000 logits 12.9 us. 64 chains over 151667
+// with drafts 27.6, of which 58 MB of rows and drafts take 13 (HBM 11; a row's loads are two
+// vectors ahead of the weighing: a chunk's at once take 3 us more).
 template <typename E>
 __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   using C = Chunk<E>;
@@ -378,7 +376,7 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   constexpr int kWaves = kWalkThreads / 64;
   extern __shared__ double lds[];
   __shared__ double sums_[kWaves], before_, target_;
-  __shared__ int node_, len_, need_, dropped_, token_, arrived, chunk_, who_, last_[kWaves];
+  __shared__ int node_, len_, need_, dropped_, token_, arrived, span_, who_, last_[kWaves];
   __shared__ bool drawn_;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -389,7 +387,7 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     w.weight = lds;
     w.sum = w.weight + most;
     w.mass = w.sum + most;
-    w.most = (float*)(w.mass + p.chunks);
+    w.most = (float*)(w.mass + p.spans);
     w.uniform = w.most + most;
     w.prob = w.uniform + most;
     w.parent = (int*)(w.prob + most);
@@ -416,13 +414,16 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     return;
   }
 
-  // Nodes: what judges them. Their weights are taken below, when the rows' largest are known.
+  // Nodes: what judges them, on its way while the rows are joined.
   constexpr int kEachNode = kVerifyMaxNodes / kWalkThreads;
-  float x_node[kEachNode];
+  float x_node[kEachNode], uniform[kEachNode], prob[kEachNode];
+  int parent_of[kEachNode], token_of[kEachNode];
 #pragma unroll
   for (int e = 0; e < kEachNode; ++e) {
     const int i = tid + e * kWalkThreads;
     x_node[e] = -kInf;
+    uniform[e] = prob[e] = 0.0f;
+    parent_of[e] = token_of[e] = -1;
     if (i >= n) continue;
     int parent = i - 1;
     if (p.parents && i > 0) {
@@ -433,10 +434,10 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     const bool known = id >= 0 && id < p.vocab;
     const bool reads = known && parent >= 0;
     if (reads) x_node[e] = L::one(logits[parent * p.row_stride + id]);
-    w.parent[i] = parent;
-    w.token[i] = known ? (int)id : -1;
-    w.uniform[i] = p.uniforms[lo + i];
-    w.prob[i] = reads && p.probs ? p.probs[(lo + parent) * p.probs_stride + id] : 0.0f;
+    if (reads && p.probs) prob[e] = p.probs[(lo + parent) * p.probs_stride + id];
+    uniform[e] = p.uniforms[lo + i];
+    parent_of[e] = parent;
+    token_of[e] = known ? (int)id : -1;
   }
   // Rows: their chunks joined, 16 lanes a row.
   {
@@ -495,27 +496,31 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   for (int e = 0; e < kEachNode; ++e) {
     const int i = tid + e * kWalkThreads;
     if (i >= n) continue;
-    const int parent = w.parent[i];
+    const int parent = parent_of[e];
     double weight = 0.0;
     if (parent >= 0) {
       const float m = w.most[parent];
       if (m > -kInf && m < kInf)
-        weight = greedy ? (w.token[i] == w.first[parent] ? 1.0 : 0.0) : weigh(x_node[e], (double)m, scale);
+        weight = greedy ? (token_of[e] == w.first[parent] ? 1.0 : 0.0) : weigh(x_node[e], (double)m, scale);
     }
     w.weight[i] = weight;
+    w.parent[i] = parent;
+    w.token[i] = token_of[e];
+    w.uniform[i] = uniform[e];
+    w.prob[i] = prob[e];
   }
   __syncthreads();
 
-  // Sum of mass[0..chunks), by one wave, in all its lanes; the lanes' own and what is before.
+  // Sum of mass[0..spans), by one wave, in all its lanes; the lanes' own and what is before.
   auto sum_mass = [&](double* mine, double* upto) {
-    const int each = (p.chunks + 63) / 64;
+    const int each = (p.spans + 63) / 64;
     *mine = 0.0;
-    for (int k = lane * each; k < min(p.chunks, (lane + 1) * each); ++k) *mine += w.mass[k];
+    for (int k = lane * each; k < min(p.spans, (lane + 1) * each); ++k) *mine += w.mass[k];
     *upto = wave_prefix(*mine, lane);
     return __shfl(*upto, 63);
   };
 
-  // Stages that end in chunks' sums, of which there is one copy of code (as it runs once, it
+  // Stages that end in spans' sums, of which there is one copy of code (as it runs once, it
   // is as long as its instructions take to arrive): the walk up to a row whose sum is too
   // near to tell; the last row; that row again with all its weights, where the remainder is empty.
   enum { kWalking, kDrawing, kDrawingAll };
@@ -605,20 +610,21 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
       dropped = dropped_;
       q = drawn_ ? p.probs + (lo + last) * p.probs_stride : nullptr;
     }
-    double* shared = p.over + (int64_t)b * 3 * p.chunks;
+    double* shared = p.over + (int64_t)b * 3 * p.spans;
 
-    // Of each chunk, by a wave: the sum of the weights without the rejected tokens, and, over
+    // Of each span, by a wave: the sum of the weights without the rejected tokens, and, over
     // a draft, the sum of max(w - near q, 0) and of the q under w. Loads of two vectors are
     // on their way while one is weighed.
-    auto weigh_chunks = [&](auto drafted) {
+    auto weigh_spans = [&](auto drafted) {
       constexpr bool kDraft = decltype(drafted)::value;
       using P = Part<E, kDraft>;
-      const int count = from < p.chunks ? (p.chunks - from + step - 1) / step : 0;
+      constexpr int kVecs = kVerifySpan / (64 * L::kVec);
+      const int count = from < p.spans ? (p.spans - from + step - 1) / step : 0;
       double s = 0.0, over = 0.0;
       float under = 0.0f;                // only meets the difference of two sums of the row
       auto fetch = [&](P& part, int unit) {
-        const int chunk = from + unit / C::kVecs * step;
-        part.fetch(row, q, p.vocab, chunk * C::kSize - C::lead(row) + unit % C::kVecs * (64 * L::kVec), lane);
+        const int span = from + unit / kVecs * step;
+        part.fetch(row, q, p.vocab, span * kVerifySpan - C::lead(row) + unit % kVecs * (64 * L::kVec), lane);
       };
       auto add = [&](const P& part) {
         float x[L::kVec];
@@ -641,16 +647,9 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
           }
         }
       };
-      P part[2];
-#pragma unroll 1
-      for (int unit = -2; unit < count * C::kVecs; unit += 2) {
-        const bool more = unit + 2 < count * C::kVecs;
-        if (unit >= 0) add(part[0]);
-        if (more) fetch(part[0], unit + 2);
-        if (unit >= 0) add(part[1]);
-        if (more) fetch(part[1], unit + 3);
-        if (unit < 0 || (unit + 2) % C::kVecs != 0) continue;
-        const int k = from + unit / C::kVecs * step;
+      auto finish = [&](int unit) {
+        const int k = from + unit / kVecs * step;
+        if (k >= p.spans) return;
         s = wave_sum(s);
         s = s > kNothing ? s : 0.0;
         double below = 0.0;
@@ -663,8 +662,8 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
           if (stage == kDrawing) {
             store_shared(shared + k, s);
             if constexpr (kDraft) {
-              store_shared(shared + p.chunks + k, over);
-              store_shared(shared + 2 * p.chunks + k, below);
+              store_shared(shared + p.spans + k, over);
+              store_shared(shared + 2 * p.spans + k, below);
             }
           } else {
             w.mass[k] = s;
@@ -672,12 +671,23 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         }
         s = over = 0.0;
         under = 0.0f;
+      };
+      P part[2];
+#pragma unroll 1
+      for (int unit = -2; unit < count * kVecs; unit += 2) {
+        const bool more = unit + 2 < count * kVecs;
+        if (unit >= 0) add(part[0]);
+        if (more) fetch(part[0], unit + 2);
+        if (kVecs == 1 && unit >= 0) finish(unit);
+        if (unit >= 0) add(part[1]);
+        if (more) fetch(part[1], unit + 3);
+        if (unit >= 0 && (unit + 2) % kVecs == 0) finish(unit + 1);
       }
     };
     if (q)
-      weigh_chunks(std::bool_constant<true>{});
+      weigh_spans(std::bool_constant<true>{});
     else
-      weigh_chunks(std::bool_constant<false>{});
+      weigh_spans(std::bool_constant<false>{});
     double total = 0.0;
     if (stage == kDrawing) {
       // stores at the device's point of coherence, complete before this workgroup arrives
@@ -694,17 +704,17 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         __syncthreads();
         if (arrived != p.groups - 1) return;
       }
-      constexpr int kEachChunk = (kVerifyMaxChunks + kWalkThreads - 1) / kWalkThreads;
-      double over[kEachChunk], under[kEachChunk];
+      constexpr int kEachSpan = (kVerifyMaxSpans + kWalkThreads - 1) / kWalkThreads;
+      double over[kEachSpan], under[kEachSpan];
 #pragma unroll
-      for (int e = 0; e < kEachChunk; ++e) {
+      for (int e = 0; e < kEachSpan; ++e) {
         const int k = tid + e * kWalkThreads;
         over[e] = under[e] = 0.0;
-        if (k >= p.chunks) continue;
+        if (k >= p.spans) continue;
         w.mass[k] = load_shared(shared + k);
         if (q) {
-          over[e] = load_shared(shared + p.chunks + k);
-          under[e] = load_shared(shared + 2 * p.chunks + k);
+          over[e] = load_shared(shared + p.spans + k);
+          under[e] = load_shared(shared + 2 * p.spans + k);
         }
       }
       __syncthreads();
@@ -717,15 +727,15 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         __syncthreads();
         total = target_;
 #pragma unroll
-        for (int e = 0; e < kEachChunk; ++e) {
+        for (int e = 0; e < kEachSpan; ++e) {
           const int k = tid + e * kWalkThreads;
-          if (k < p.chunks) w.mass[k] = __builtin_fmax(__builtin_fma(near - total, under[e], over[e]), 0.0);
+          if (k < p.spans) w.mass[k] = __builtin_fmax(__builtin_fma(near - total, under[e], over[e]), 0.0);
         }
       }
     }
     __syncthreads();
     if (wave == 0) {
-      // the chunk whose sum passes the border; by rounding none may: the last with any
+      // the span whose sum passes the border; by rounding none may: the last with any
       double mine, upto;
       const double all = sum_mass(&mine, &upto), target = border * all;
       if (stage == kWalking) {
@@ -734,19 +744,19 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
           w.first[node] = -1;
         }
       } else {
-        const int each = (p.chunks + 63) / 64;
+        const int each = (p.spans + 63) / 64;
         uint64_t passing = __ballot(upto > target && mine > 0.0);
         const bool none = passing == 0;
         if (none) passing = __ballot(mine > 0.0);
-        int chunk = -1;
+        int span = -1;
         double before = 0.0;
         if (all > 0.0 && passing != 0) {
           const int owner = none ? 63 - __builtin_clzll(passing) : __builtin_ctzll(passing);
           double run = __shfl(upto - mine, owner);
           bool found = false;
-          for (int k = owner * each; k < min(p.chunks, (owner + 1) * each) && !found; ++k) {
+          for (int k = owner * each; k < min(p.spans, (owner + 1) * each) && !found; ++k) {
             if (w.mass[k] > 0.0) {
-              chunk = k;
+              span = k;
               before = run;
               run += w.mass[k];
               found = !none && run > target;
@@ -754,7 +764,7 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
           }
         }
         if (lane == 0) {
-          chunk_ = chunk;
+          span_ = span;
           before_ = before;
           target_ = target;
         }
@@ -762,10 +772,10 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     }
     __syncthreads();
     if (stage == kWalking) continue;
-    if (chunk_ >= 0) {
-      // that chunk by the whole workgroup, kFew consecutive logits a thread
-      constexpr int kFew = C::kSize / kWalkThreads;
-      const int first = chunk_ * C::kSize - C::lead(row) + tid * kFew;
+    if (span_ >= 0) {
+      // that span by the whole workgroup, kFew consecutive logits a thread
+      constexpr int kFew = kVerifySpan / kWalkThreads;
+      const int first = span_ * kVerifySpan - C::lead(row) + tid * kFew;
       double r[kFew], sum = 0.0;
 #pragma unroll
       for (int e = 0; e < kFew; ++e) {
@@ -835,7 +845,7 @@ hipError_t launch(const VerifyParams& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   walk_kernel<E><<<(unsigned)p.sequences * (unsigned)p.groups, kWalkThreads,
-                   walk_bytes(p.max_q > 0 ? p.max_q : 1, p.chunks), stream>>>(p);
+                   walk_bytes(p.max_q > 0 ? p.max_q : 1, p.spans), stream>>>(p);
   return hipGetLastError();
 }
 
