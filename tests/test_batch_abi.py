@@ -203,9 +203,11 @@ def test_scratch_and_plan_sizes():
     # counters; for each of 16 rows the ranks (128 or 16 here) in two parts and a factor, and the sums of each split
     assert adapters.workspace_bytes(1, 128, 256, 4, 128) == 65536 + 16 * (128 + 1) * 4
     assert adapters.workspace_bytes(1, 20480, 256, 4, 8) > 65536 + 16 * (2 * 16 + 16 + 1) * 4
-    # none where one kernel does both: 256 KiB of an adapter's a, a workgroup for each 512 columns
-    assert adapters.workspace_bytes(1, 16384, 256, 4, 8) == 0 != adapters.workspace_bytes(1, 16392, 256, 4, 8)
-    assert adapters.workspace_bytes(16, 512, 8192, 64, 16) == 0 != adapters.workspace_bytes(16, 512, 8200, 64, 16)
+    # none where one kernel does both: 4 steps of k a wave, and up to 4096 columns each of 256 workgroups
+    for rank, k in ((8, 8192), (16, 8192), (24, 4096), (32, 4096), (40, 2048), (64, 2048)):
+        assert adapters.workspace_bytes(1, k, 256, 4, rank) == 0 != adapters.workspace_bytes(1, k + 8, 256, 4, rank)
+    assert adapters.workspace_bytes(16, 512, 65536, 64, 16) == 0 != adapters.workspace_bytes(16, 512, 65544, 64, 16)
+    assert adapters.workspace_bytes(257, 512, 256, 256, 16) != 0 == adapters.workspace_bytes(256, 512, 256, 256, 16)
     for bad in (dict(rank=7), dict(k=4), dict(tokens=-1), dict(adapters=0), dict(n=12)):
         with pytest.raises(W.W4A16Error):
             adapters.workspace_bytes(**{**dict(tokens=1, k=128, n=256, adapters=4, rank=8), **bad})

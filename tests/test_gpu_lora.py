@@ -74,10 +74,12 @@ def test_against_the_oracle(T, K, N, R, rank, dtype):
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))
-@pytest.mark.parametrize("T,K,N,R,rank", [(1, 16384, 136, 2, 8), (1, 16392, 136, 2, 8), (40, 8192, 1032, 4, 16),
+@pytest.mark.parametrize("T,K,N,R,rank", [(1, 8192, 136, 2, 8), (1, 8200, 136, 2, 8), (40, 8192, 1032, 4, 16),
                                           (40, 8200, 1032, 4, 16), (5, 4096, 520, 1, 32), (5, 4104, 520, 1, 32),
-                                          (3, 2048, 4104, 2, 64), (3, 2056, 4104, 2, 64), (100, 264, 8192, 30, 16),
-                                          (200, 264, 8192, 30, 64), (9, 40000, 72, 9, 48)])
+                                          (3, 2048, 4104, 2, 64), (3, 2056, 4104, 2, 64), (100, 264, 8200, 30, 16),
+                                          (200, 264, 12320, 64, 16), (200, 264, 12296, 64, 16), (200, 264, 12320, 64, 32),
+                                          (200, 264, 8192, 64, 64), (300, 72, 264, 255, 24), (255, 72, 264, 255, 24),
+                                          (9, 40000, 72, 9, 48)])
 def test_one_kernel_or_two(T, K, N, R, rank, dtype):
     # around the sizes from which on the two products are launched apart
     c = make(K, T, K, N, R, rank, dtype)

@@ -149,14 +149,25 @@ int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int32_t rank, i
   return (int32_t)div_up(all, *steps);
 }
 
-// Whether one kernel does both: while all its workgroups are resident and each reads little
-// of a. us of a call replayed from a graph, with two kernels (and their scratch cleared) and
-// with one: k 1024, rank 8 (16 KiB of a) 7.2 and 3.9; 4096, 16 (128 KiB) 9.1 and 6.5; 8192, 16
-// (256 KiB) 9.5 and 9.2; 17408, 16 (544 KiB) 10.6 and 15.5; 5120, 64 (640 KiB) 11.9 and 14.0.
-constexpr int64_t kOnceBytes = 256 << 10;
-bool lora_once(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus) {
-  return lora_tile_rows(tokens, adapters) == 16 && lora_rank_block(rank) <= 64 && (int64_t)rank * k * 2 <= kOnceBytes &&
-         lora_max_tiles(tokens, adapters) * div_up(n, kOnceColumns) <= num_cus;
+// Columns that a workgroup takes where one kernel does both products, or 0: two are launched.
+// It wins while all its workgroups are resident, none takes many columns, and each wave has at
+// most 4 steps of k, all of a being read by every workgroup. us of a call replayed from a
+// graph, with two kernels (of which clearing their scratch is 1.8) and with one, n 4096:
+//   1 token, 16 ranks: k 1024 7.1, 4.9; 4096 8.8, 6.9; 8192 9.2, 9.3; 12288 9.8, 11.8
+//   64 tokens, 32 adapters of 16: k 1024 8.2, 5.4; 4096 10.7, 8.1; 8192 12.3, 10.7; 16384 15.4, 16.5
+//   1 token, 32 ranks: k 1024 7.9, 5.2; 4096 9.8, 8.5; 8192 10.2, 12.3
+//   1 token, 64 ranks: k 1024 10.5, 7.8; 2048 11.0, 9.2; 4096 11.9, 12.5
+// 200 tokens, 64 adapters, k 1024, 6144 columns a workgroup: 16 ranks 15.9, 14.2, 64 ranks 37.2, 42.8.
+constexpr int kOnceSteps = 4;
+constexpr int64_t kOnceMaxColumns = 4096;
+int32_t lora_once_columns(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus) {
+  const int block = lora_rank_block(rank), threads = lora_once_threads(block);
+  const int64_t tiles = lora_max_tiles(tokens, adapters);
+  if (lora_tile_rows(tokens, adapters) != 16 || block > 64 || tiles > num_cus ||
+      k > kOnceSteps * (threads / 64) * lora_step(1, block))
+    return 0;
+  const int64_t columns = threads * div_up(div_up(n, threads), num_cus / tiles);
+  return columns <= kOnceMaxColumns ? (int32_t)columns : 0;
 }
 
 w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus,
@@ -170,7 +181,7 @@ w4a16_status lora_workspace(int64_t tokens, int32_t k, int32_t n, int32_t adapte
   if (n < 8 || n > (1 << 22) || n % 8 != 0)
     return report(W4A16_ERR_SHAPE, "n=%d must be a multiple of 8 in 8..2^22", (int)n);
   *bytes = 0;
-  if (tokens == 0 || lora_once(tokens, k, n, adapters, rank, num_cus)) return W4A16_OK;
+  if (tokens == 0 || lora_once_columns(tokens, k, n, adapters, rank, num_cus) > 0) return W4A16_OK;
   int32_t steps;
   const int64_t splits = lora_splits(tokens, adapters, k, rank, num_cus, &steps);
   // counters, the splits' sums, v's two parts and a factor for each row
@@ -423,7 +434,11 @@ w4a16_status w4a16_lora(const w4a16_lora_t* a, void* workspace, int64_t ws_bytes
   // columns of a workgroup of the second kernel: those of a step until there are 2048 of them
   const int64_t steps = div_up(a->n, kUpColumns);
   p.columns = (int32_t)(kUpColumns * std::min(div_up(p.tiles_most * steps, 2048), steps));
-  if (lora_once(a->tokens, a->k, a->n, a->adapters, a->rank, cus)) p.splits = 0;
+  const int32_t once = lora_once_columns(a->tokens, a->k, a->n, a->adapters, a->rank, cus);
+  if (once > 0) {
+    p.splits = 0;
+    p.columns = once;
+  }
   if ((int64_t)p.tiles_most * div_up(a->n, p.columns) > kMaxGrid)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %d columns are too many for one launch", (long long)a->tokens,
                   (int)a->n);

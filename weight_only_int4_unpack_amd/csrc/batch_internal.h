@@ -117,7 +117,9 @@ constexpr int kLoraPlanThreads = 512;
 constexpr int kLoraDownThreads = 512;
 constexpr int kLoraThreads = 256;
 constexpr int kUpColumns = 256;           // of n that a workgroup of the second kernel takes at a time
-constexpr int kOnceColumns = 512;         // of n that a workgroup takes that does both
+// Threads of a workgroup that does both products, and columns that it takes at a time: for
+// 16 ranks more waves with one step's loads each, for more of them fewer with two.
+__host__ __device__ constexpr int lora_once_threads(int rank_block) { return rank_block <= 16 ? 1024 : 512; }
 constexpr int kLoraMaxSplits = 16;
 constexpr int kLoraStep = 128;            // of k: splits are multiples
 // Rows of a tile: tokens of one adapter that are multiplied at a time.
@@ -170,7 +172,7 @@ struct LoraParams {
   int32_t tokens, k, n, adapters, rank, tiles_most;
   int32_t splits;           // of k over workgroups; 0: one kernel for both
   int32_t steps;            // of kLoraStep that a split takes
-  int32_t columns;          // of n that a workgroup of the second kernel takes
+  int32_t columns;          // of n that a workgroup of the second kernel (or of the only one) takes
 };
 
 hipError_t launch_verify(const VerifyParams& p, int dtype, hipStream_t stream);

@@ -191,9 +191,9 @@ __device__ __forceinline__ void wait_stores() {
 // Memory is read as whole lines, kLanes lanes a row, and turned in LDS into what the matrix
 // instructions take (read straight into their layout, where neighbouring lanes hold different
 // rows, 8192 tokens of 5120 with rank 64 took 45 us instead of 32).
-template <typename T, int MT, int RB>
+template <typename T, int MT, int RB, int THREADS = kLoraDownThreads>
 struct Down {
-  static constexpr int kWaves = kLoraDownThreads / 64, kRows = 16 * MT, RT = RB / 16;
+  static constexpr int kWaves = THREADS / 64, kRows = 16 * MT, RT = RB / 16;
   static constexpr int kStep = lora_step(MT, RB), kPieces = kStep / 32;
   static constexpr int kMeet = MT * RT < 4 ? MT * RT : 4;          // results that meet at a time
   static constexpr int kTurnA = RB < 64 ? RB : 64;                 // ranks that are turned at a time
@@ -270,8 +270,15 @@ struct Down {
               sum[m][h / 16 + r] = mfma<T>(as[r][j], xs[m][j], sum[m][h / 16 + r]);
       }
     };
-    // the next step's loads are on their way while one is multiplied
-    if (from < to) {
+    if constexpr (THREADS > 512) {
+#pragma unroll 1
+      for (int k0 = from; k0 < to; k0 += kStep) {
+        Stage s;
+        load(k0, s);
+        multiply(k0, s);
+      }
+    } else if (from < to) {
+      // the next step's loads are on their way while one is multiplied
       Stage s0, s1;
       int k0 = from;
       load(k0, s0);
@@ -546,12 +553,16 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
 }
 
 // ---- both for a few tokens: every workgroup forms v for itself and multiplies it with its own
-// columns, whose b and base are on their way meanwhile. One launch in place of two, no
-// scratch; a is read by each workgroup (the host's rule says how much of it). One token, k
-// and n 4096, rank 8: 7.0 us instead of 4.8 + 3.3, a call 10.8 instead of 15.0.
+// columns, whose first b and base are on their way meanwhile. One launch in place of two, no
+// scratch; a is read by each workgroup (the host's rule says where that pays). As code that
+// runs once takes as long as it is, loads of more steps ahead made it slower (64 tokens of 32 adapters, k
+// 5120, n 17408, rank 16: by 0.5 to 1.1 us with 3, 4 or 5 steps). That case 12.4 us instead of
+// 6.3 + 6.5 and a call 11.5 instead of 14.3; one token, k and n 4096, rank 8: 7.4 us instead of
+// 4.8 + 3.3, a call 10.8 instead of 15.0.
 template <typename T, int RB>
-__global__ __launch_bounds__(kLoraDownThreads) void once_kernel(LoraParams p) {
-  using D = Down<T, 1, RB>;
+__global__ __launch_bounds__(lora_once_threads(RB)) void once_kernel(LoraParams p) {
+  constexpr int kThreads = lora_once_threads(RB);
+  using D = Down<T, 1, RB, kThreads>;
   using F = Few<T, RB>;
   __shared__ alignas(16) char lds[D::kLdsBytes];
   __shared__ alignas(16) float whole[16][RB];
@@ -562,14 +573,15 @@ __global__ __launch_bounds__(kLoraDownThreads) void once_kernel(LoraParams p) {
   const int64_t row0 = (int64_t)blockIdx.x * 16;
   const int adapter = adapter_of(p, blockIdx.x);
   if (adapter == kLoraUnused) return;
-  const int n0 = blockIdx.y * kOnceColumns + wave * 64;
-  const F f(p, row0, adapter, p.n);
-  const typename F::Held held = f.load_base(n0);
+  const int n_lo = blockIdx.y * p.columns + wave * 64, n_hi = min(p.n, (int)(blockIdx.y + 1) * p.columns);
+  const F f(p, row0, adapter, n_hi);
   if (adapter < 0) {
-    if (p.base != p.out) f.store_out(n0, held);
+    if (p.base == p.out) return;
+    for (int n0 = n_lo; n0 < n_hi; n0 += kThreads) f.store_out(n0, f.load_base(n0));
     return;
   }
-  typename F::Columns c = f.load_b(n0);
+  typename F::Held held = f.load_base(n_lo);
+  typename F::Columns next = f.load_b(n_lo);
   D::sums(p, lds, row0, adapter, f.rank, 0, p.k, [&](int row, int r, const f32x4& v) { *(f32x4*)&whole[row][r] = v; });
   __syncthreads();
   constexpr int kLanes = RB / 8;
@@ -582,11 +594,18 @@ __global__ __launch_bounds__(kLoraDownThreads) void once_kernel(LoraParams p) {
     if (r0 == 0) factors[row] = factor;
   }
   __syncthreads();
-  f.cut_b(c);
   const int row = tid & 15;
   u32x4 v[F::KS][F::kParts];
   f.load_v(high[row], low[row], v);
-  f.store_out(n0, f.add(held, c, v, factors[row]));
+  const float factor = factors[row];
+  for (int n0 = n_lo; n0 < n_hi; n0 += kThreads) {
+    typename F::Columns c = next;
+    const typename F::Held now = held;
+    f.cut_b(c);
+    next = f.load_b(n0 + kThreads);
+    held = f.load_base(n0 + kThreads);
+    f.store_out(n0, f.add(now, c, v, factor));
+  }
 }
 
 // ---- up, tiles of 64 tokens, or ranks above 32: as above, in MT steps of 16 tokens with b of
@@ -753,7 +772,7 @@ template <typename T, int MT, int RB>
 hipError_t launch(const LoraParams& p, hipStream_t stream) {
   if constexpr (MT == 1 && RB <= 64) {
     if (p.splits == 0) {
-      once_kernel<T, RB><<<dim3(p.tiles_most, (p.n + kOnceColumns - 1) / kOnceColumns), kLoraDownThreads, 0, stream>>>(p);
+      once_kernel<T, RB><<<dim3(p.tiles_most, (p.n + p.columns - 1) / p.columns), lora_once_threads(RB), 0, stream>>>(p);
       return hipGetLastError();
     }
   }
