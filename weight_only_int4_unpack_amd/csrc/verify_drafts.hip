@@ -520,9 +520,9 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     return __shfl(*upto, 63);
   };
 
-  // Stages that end in spans' sums, of which there is one copy of code (as it runs once, it
-  // is as long as its instructions take to arrive): the walk up to a row whose sum is too
-  // near to tell; the last row; that row again with all its weights, where the remainder is empty.
+  // Stages that end in spans' sums, with one copy of code: the walk up to a row whose sum is
+  // too near to tell; the last row; that row again with all its weights, where the remainder
+  // is empty.
   enum { kWalking, kDrawing, kDrawingAll };
   int stage = kWalking, len = 1, last = 0;
   for (;;) {
