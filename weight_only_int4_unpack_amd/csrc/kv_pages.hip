@@ -13,7 +13,9 @@ namespace {
 using namespace serve;
 
 // ---- forks and resizes
-// One sequence forked in 3 ways 6.2 us, 10 in 4 each 8.5; resized 3.7 and 6.8: waits are 75 %.
+// One sequence forked in 3 ways 6.2 us, 10 in 4 each 7.7; resized 4.0 and 6.0: waits are 75 %.
+// (The first look at the counts only when their number is known, and a wave for each row in
+// turn: 9.1 and 7.2 us for the 40.)
 // Every listed change needs `need` new pages, which go into consecutive entries of its row
 // from `entry` on. Pages are handed out in the order of the list, lowest first, from those
 // that nobody held at the start: what this call takes back is for later calls, so that no
@@ -56,29 +58,39 @@ __device__ __forceinline__ uint32_t block_prefix(PagesLds& l, uint32_t x, int ti
   return lane == 0 ? before : add_pages(before, here);
 }
 
+// Counts of the pages that a thread looks at, at a time; 1 behind the last page.
+constexpr int kPagesLook = 8;
+struct Look {
+  int held[kPagesLook];
+};
+__device__ __forceinline__ Look look(const int32_t* refs, int pages, int64_t base, int tid) {
+  Look x;
+  const int64_t first = base + tid * kPagesLook;
+#pragma unroll
+  for (int e = 0; e < kPagesLook; ++e) x.held[e] = first + e < pages ? refs[first + e] : 1;
+  return x;
+}
 // Calls take(k, page) with the k-th free page, k < want, in ascending order; returns how
-// many there are (stops looking when there are enough).
+// many there are (stops looking when there are enough). `x`: the first look.
 template <typename Take>
 __device__ __forceinline__ uint32_t free_pages(PagesLds& l, const int32_t* refs, int pages, uint32_t want, int tid,
-                                               Take take) {
-  constexpr int kEach = 8;
+                                               Look x, Take take) {
   uint32_t found = 0;
-  for (int64_t base = 0; base < pages && found < want; base += kPagesThreads * kEach) {
-    const int64_t first = base + tid * kEach;
-    int held[kEach];
+  for (int64_t base = 0; base < pages && found < want;) {
+    const int64_t first = base + tid * kPagesLook;
     uint32_t mine = 0;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) held[e] = first + e < pages ? refs[first + e] : 1;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) mine += held[e] == 0;
+    for (int e = 0; e < kPagesLook; ++e) mine += x.held[e] == 0;
     uint32_t all, k = found + block_prefix(l, mine, tid, &all);
 #pragma unroll
-    for (int e = 0; e < kEach; ++e)
-      if (held[e] == 0) {
+    for (int e = 0; e < kPagesLook; ++e)
+      if (x.held[e] == 0) {
         if (k < want) take(k, (int)(first + e));
         ++k;
       }
     found += all;
+    base += kPagesThreads * kPagesLook;
+    x = look(refs, pages, base, tid);
   }
   return found;
 }
@@ -109,6 +121,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     if (lane == 0) l.entry[i] = twice;
   }
   __syncthreads();
+  const Look first_look = look(p.refs, p.pages, 0, tid);   // on its way while the changes are read
   uint32_t need[kEach], carry = 0;
   int old_len[kEach], new_len[kEach], src[kEach], entry[kEach];
   bool good[kEach];
@@ -172,7 +185,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
   __syncthreads();
   const uint32_t want = carry;
   if (want > 0) {
-    const uint32_t free = free_pages(l, p.refs, p.pages, want, tid, [&](uint32_t k, int page) {
+    const uint32_t free = free_pages(l, p.refs, p.pages, want, tid, first_look, [&](uint32_t k, int page) {
       if (k < kPagesFound) l.found[k] = page;
     });
     __syncthreads();
@@ -192,7 +205,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     if (given <= kPagesFound) {
       for (uint32_t k = tid; k < given; k += kPagesThreads) give(k, l.found[k]);
     } else {
-      free_pages(l, p.refs, p.pages, given, tid, give);
+      free_pages(l, p.refs, p.pages, given, tid, look(p.refs, p.pages, 0, tid), give);
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
@@ -202,7 +215,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     }
     __syncthreads();
   }
-  // Lengths; and what is left to do for each change, which whole waves take below.
+  // Lengths; and what is left to do for each change, which many threads take below.
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     if (e * kPagesThreads >= p.count) break;
@@ -223,18 +236,20 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     if (!ok) l.row[i] = -1;
   }
   __syncthreads();
-  for (int i = wave; i < p.count; i += kPagesWaves) {
+  // as many threads a change as there are for all of them, 16 at least
+  const int shift = min(p.count > 1 ? 32 - __builtin_clz(p.count - 1) : 0, 6), lanes = kPagesThreads >> shift;
+  for (int i = tid / lanes; i < p.count; i += 1 << shift) {
     const int row = l.row[i];
     if (row < 0) continue;
     if constexpr (FORK) {
       const int parent = p.from[i];
-      for (int k = lane; k < l.entry[i]; k += 64) {
+      for (int k = tid % lanes; k < l.entry[i]; k += lanes) {
         const int page = entry_of(parent, k);
         entry_of(row, k) = page;
         if (known(page)) atomicAdd(p.refs + page, 1);
       }
     } else {
-      for (int k = l.entry[i] + lane; k < (int)l.upto[i]; k += 64) {
+      for (int k = l.entry[i] + tid % lanes; k < (int)l.upto[i]; k += lanes) {
         const int page = entry_of(row, k);
         release(page);
         entry_of(row, k) = -1;
