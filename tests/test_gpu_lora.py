@@ -83,7 +83,10 @@ def test_against_the_oracle(T, K, N, R, rank, dtype):
 def test_one_kernel_or_two(T, K, N, R, rank, dtype):
     # around the sizes from which on the two products are launched apart
     c = make(K, T, K, N, R, rank, dtype)
-    check(run(c), c)
+    got = run(c)
+    check(got, c)
+    base = c["base"].cuda()
+    assert torch.equal(run(c, base=base, out=base), got) and torch.equal(base, got)
 
 
 @pytest.mark.parametrize("rank", [8, 32, 64, 128])
