@@ -260,6 +260,24 @@ def test_offsets_past_32_bits(T):
     check(got, c)
 
 
+def test_the_most_tokens():
+    # 2^24 of them; one in 2^8 is compared, in fp64, with the tolerance of `check`
+    T, K, N, R, rank = 1 << 24, 8, 8, 1024, 8
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x, a, b = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((T, K), (R, rank, K), (R, N, rank)))
+    index = torch.randint(-1, R, (T,), generator=g, device="cuda", dtype=torch.int32)
+    got = adapters.lora(x, a, b, adapters.lora_plan(index, R))
+    at = torch.arange(0, T, 256, device="cuda") + 7
+    i = index[at].long()
+    xs, aa, bb = x[at].double(), a[i.clamp(min=0)].double(), b[i.clamp(min=0)].double()
+    v, deep = (xs[:, None] * aa).sum(-1), (xs[:, None] * aa).abs().sum(-1)
+    y, vb, deep = ((bb * v[:, None]).sum(-1), (bb * v[:, None]).abs().sum(-1), (bb.abs() * deep[:, None]).sum(-1))
+    y[i < 0] = 0
+    tol = deep * K * 2.0 ** -23 + vb * (2.0 ** -18 + 2 * rank * 2.0 ** -23 + 2.0 ** -23)
+    tol = tol + 2.0 ** -8 * (y.abs() + tol) + 2.0 ** -134
+    assert ((got[at].double() - y).abs() <= tol).all()
+
+
 def test_plan_keeps_the_order_of_tokens():
     g = np.random.default_rng(3)
     for T, R in ((1, 1), (64, 32), (5000, 3), (5000, 1024), (70000, 40)):

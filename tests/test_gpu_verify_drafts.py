@@ -102,6 +102,13 @@ def test_rows_of_draft_probabilities_that_lie_apart():
     same(call(c, draft_probs=wide[:, 3:3004]), want(c))
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("mode", ["given", "drawn"])
+def test_the_largest_vocabulary_and_most_nodes(mode, dtype):
+    c = make(8, [3, 0, 5], 1 << 20, dtype, False, mode == "drawn", temps=[1.0, 1.0, 0.5], pad=3)
+    same(call(c, max_q=1024), want(c, max_q=1024))
+
+
 @pytest.mark.parametrize("mode", ["given", "drawn"])
 def test_offsets_past_32_bits(mode):
     # the last sequence's rows lie past 2^31 logits (and probabilities): as the same rows alone
