@@ -111,11 +111,11 @@ w4a16_status check_caches(const w4a16_kv_cache_t* caches, int32_t count, KvView*
   return W4A16_OK;
 }
 
-int fill_addresses(const w4a16_kv_cache_t* caches, int32_t first, int32_t count, CacheAddresses* to) {
+int fill_addresses(const w4a16_kv_cache_t* caches, int32_t first, int32_t count, CacheList<kGroupCaches>* to) {
   const int n = std::min<int32_t>(kGroupCaches, count - first);
   for (int i = 0; i < n; ++i) {
     const w4a16_kv_cache_t& c = caches[first + i];
-    to[i] = CacheAddresses{(char*)c.k, (char*)c.v, (char*)c.k_scale, (char*)c.v_scale};
+    to->at[i] = CacheAddresses{(char*)c.k, (char*)c.v, (char*)c.k_scale, (char*)c.v_scale};
   }
   return n;
 }
@@ -279,6 +279,7 @@ w4a16_status w4a16_kv_copy_pages(const w4a16_kv_copy_pages_t* a, void* stream) {
   const int32_t format = a->caches[0].format;
   const int64_t tokens = (int64_t)view.heads << view.page_shift;
   CopyPagesParams p{};
+  CacheList<kGroupCaches> caches{};
   p.page_units = (uint32_t)(tokens * view.dim * element_bytes(format) / 16);
   p.scale_units = format == W4A16_KV_SAME ? 0 : (uint32_t)(tokens * 4 / 16);
   p.chunks = (uint32_t)div_up(2 * ((int64_t)p.page_units + p.scale_units), kCopyThreads * kCopyEach);
@@ -291,8 +292,8 @@ w4a16_status w4a16_kv_copy_pages(const w4a16_kv_copy_pages_t* a, void* stream) {
   p.pages = view.pages;
   p.pairs = a->pairs;
   for (int32_t first = 0; first < a->count; first += p.count) {
-    p.count = fill_addresses(a->caches, first, a->count, p.caches);
-    CHECK(launched(launch_copy_pages(p, (hipStream_t)stream)));
+    p.count = fill_addresses(a->caches, first, a->count, &caches);
+    CHECK(launched(launch_copy_pages(p, caches, (hipStream_t)stream)));
   }
   return W4A16_OK;
 }
@@ -316,6 +317,7 @@ w4a16_status w4a16_kv_compact(const w4a16_kv_compact_t* a, void* stream) {
   if (a->new_lens == a->kv_lens) return report(W4A16_ERR_SHAPE, "new_lens must be apart from kv_lens");
   const bool none = a->count == 0 || view.pages == 0;
   CompactParams p{};
+  CacheList<kGroupCaches> caches{};
   p.row_units = none ? 0 : view.dim * element_bytes(a->caches[0].format) / 16;
   p.scaled = !none && a->caches[0].format != W4A16_KV_SAME;
   const int64_t work = (int64_t)view.heads * 2 * (p.row_units + p.scaled);
@@ -340,11 +342,11 @@ w4a16_status w4a16_kv_compact(const w4a16_kv_compact_t* a, void* stream) {
   p.heads = view.heads;
   if (none) {  // lengths alone
     p.count = 1;
-    return launched(launch_compact(p, (hipStream_t)stream));
+    return launched(launch_compact(p, caches, (hipStream_t)stream));
   }
   for (int32_t first = 0; first < a->count; first += p.count) {
-    p.count = fill_addresses(a->caches, first, a->count, p.caches);
-    CHECK(launched(launch_compact(p, (hipStream_t)stream)));
+    p.count = fill_addresses(a->caches, first, a->count, &caches);
+    CHECK(launched(launch_compact(p, caches, (hipStream_t)stream)));
     p.new_lens = nullptr;
   }
   return W4A16_OK;

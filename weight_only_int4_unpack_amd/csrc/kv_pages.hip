@@ -262,14 +262,15 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
 // A workgroup copies kCopyEach * 256 units of 16 bytes of one pair in one cache; k, v and
 // their scales count as one run of units. 40 pages of 64 tokens in 16 caches of 8 bf16 heads
 // of 128: 56 us, 6.0 TB/s read and written.
-__global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyPagesParams p) {
+template <int N>
+__global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyPagesParams p, CacheList<N> caches) {
   uint32_t at = blockIdx.x;
   const uint32_t chunk = at % p.chunks;
   at /= p.chunks;
   const uint32_t cache = at % (uint32_t)p.count, pair = at / (uint32_t)p.count;
   const int64_t src = p.src[pair], dst = p.dst[pair];
   if (src < 0 || src >= p.pages || dst < 0 || dst >= p.pages || src == dst) return;
-  const CacheAddresses& c = p.caches[cache];
+  const CacheAddresses& c = caches.at[cache];
   char* base[kCopyEach];
   u32x4 held[kCopyEach];
   const uint32_t first = chunk * (kCopyThreads * kCopyEach) + threadIdx.x;
@@ -306,7 +307,8 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyPagesParam
 // heads of 128: 8.2 us, 2.3 TB/s; one sequence 4: path, table and tokens follow one another
 // (waits: 72 %).
 constexpr int kCompactList = 64;
-__global__ __launch_bounds__(kCompactThreads) void compact_kernel(CompactParams p) {
+template <int N>
+__global__ __launch_bounds__(kCompactThreads) void compact_kernel(CompactParams p, CacheList<N> caches) {
   __shared__ int64_t from[kCompactList], to[kCompactList];   // token rows of head 0
   __shared__ int kept_total, moves;
   uint32_t at = blockIdx.x;
@@ -332,11 +334,11 @@ __global__ __launch_bounds__(kCompactThreads) void compact_kernel(CompactParams 
   if (moves_unit) {
     const int head = work / p.row_units;
     part = work - head * p.row_units;
-    base = head >= p.heads ? p.caches[cache].v : p.caches[cache].k;
+    base = head >= p.heads ? caches.at[cache].v : caches.at[cache].k;
     head_rows = (int64_t)(head >= p.heads ? head - p.heads : head) << p.page_shift;
   } else if (moves_scale) {
     const int head = work - units;
-    base = head >= p.heads ? p.caches[cache].v_scale : p.caches[cache].k_scale;
+    base = head >= p.heads ? caches.at[cache].v_scale : caches.at[cache].k_scale;
     head_rows = (int64_t)(head >= p.heads ? head - p.heads : head) << p.page_shift;
   }
 
@@ -402,6 +404,12 @@ __global__ __launch_bounds__(kCompactThreads) void compact_kernel(CompactParams 
   if (p.new_lens && block == 0 && cache == 0 && tid == 0) p.new_lens[b] = (int32_t)(any ? first + kept : len);
 }
 
+CacheList<kFewCaches> few(const CacheList<kGroupCaches>& caches) {
+  CacheList<kFewCaches> l;
+  for (int i = 0; i < kFewCaches; ++i) l.at[i] = caches.at[i];
+  return l;
+}
+
 }  // namespace
 
 hipError_t launch_pages(const PagesParams& p, bool fork, hipStream_t stream) {
@@ -412,13 +420,21 @@ hipError_t launch_pages(const PagesParams& p, bool fork, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_copy_pages(const CopyPagesParams& p, hipStream_t stream) {
-  copy_pages_kernel<<<(unsigned)(p.pairs * p.count * p.chunks), kCopyThreads, 0, stream>>>(p);
+hipError_t launch_copy_pages(const CopyPagesParams& p, const CacheList<kGroupCaches>& caches, hipStream_t stream) {
+  const unsigned grid = (unsigned)(p.pairs * p.count * p.chunks);
+  if (p.count <= kFewCaches)
+    copy_pages_kernel<<<grid, kCopyThreads, 0, stream>>>(p, few(caches));
+  else
+    copy_pages_kernel<<<grid, kCopyThreads, 0, stream>>>(p, caches);
   return hipGetLastError();
 }
 
-hipError_t launch_compact(const CompactParams& p, hipStream_t stream) {
-  compact_kernel<<<(unsigned)((int64_t)p.sequences * p.count * p.blocks), kCompactThreads, 0, stream>>>(p);
+hipError_t launch_compact(const CompactParams& p, const CacheList<kGroupCaches>& caches, hipStream_t stream) {
+  const unsigned grid = (unsigned)((int64_t)p.sequences * p.count * p.blocks);
+  if (p.count <= kFewCaches)
+    compact_kernel<<<grid, kCompactThreads, 0, stream>>>(p, few(caches));
+  else
+    compact_kernel<<<grid, kCompactThreads, 0, stream>>>(p, caches);
   return hipGetLastError();
 }
 

@@ -40,8 +40,8 @@ hipError_t attn_bf16_e4m3(const AttnParams&, AttnKind, hipStream_t) { return hip
 hipError_t attn_bf16_int8(const AttnParams&, AttnKind, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_verify(const VerifyParams&, int, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_pages(const PagesParams&, bool, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_copy_pages(const CopyPagesParams&, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_compact(const CompactParams&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_copy_pages(const CopyPagesParams&, const CacheList<kGroupCaches>&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_compact(const CompactParams&, const CacheList<kGroupCaches>&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_lora_plan(const LoraPlanParams&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_lora(const LoraParams&, int, int, hipStream_t) { return hipErrorNoDevice; }
 }  // namespace w4a16
