@@ -227,8 +227,9 @@ struct Down {
 #pragma unroll
       for (int r = 0; r < RT; ++r) sum[m][r] = f32x4{0, 0, 0, 0};
 
-    const int each = ((k_hi - k_lo + kWaves * kStep - 1) / (kWaves * kStep)) * kStep;
-    const int from = k_lo + wave * each, to = min(k_hi, from + each);
+    // the waves' steps lie side by side, so that a row is read in runs of all of them
+    constexpr int kTurn = kWaves * kStep;
+    const int from = k_lo + wave * kStep, to = k_hi;
     auto load = [&](int k0, Stage& s) {
       const int k = k0 + piece * 8 < to ? k0 + piece * 8 : 0;
 #pragma unroll
@@ -272,7 +273,7 @@ struct Down {
     };
     if constexpr (THREADS > 512) {
 #pragma unroll 1
-      for (int k0 = from; k0 < to; k0 += kStep) {
+      for (int k0 = from; k0 < to; k0 += kTurn) {
         Stage s;
         load(k0, s);
         multiply(k0, s);
@@ -282,15 +283,15 @@ struct Down {
       Stage s0, s1;
       int k0 = from;
       load(k0, s0);
-      for (; k0 + 2 * kStep < to; k0 += 2 * kStep) {
-        load(k0 + kStep, s1);
+      for (; k0 + 2 * kTurn < to; k0 += 2 * kTurn) {
+        load(k0 + kTurn, s1);
         multiply(k0, s0);
-        load(k0 + 2 * kStep, s0);
-        multiply(k0 + kStep, s1);
+        load(k0 + 2 * kTurn, s0);
+        multiply(k0 + kTurn, s1);
       }
-      if (k0 + kStep < to) load(k0 + kStep, s1);
+      if (k0 + kTurn < to) load(k0 + kTurn, s1);
       multiply(k0, s0);
-      if (k0 + kStep < to) multiply(k0 + kStep, s1);
+      if (k0 + kTurn < to) multiply(k0 + kTurn, s1);
     }
     // the scratch holds the waves' sums from here on: a lane has ranks 16 r + 4 group .. + 3
     // of token 16 m + col
