@@ -556,7 +556,7 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
 // ---- both for a few tokens: every workgroup forms v for itself and multiplies it with its own
 // columns, whose first b and base are on their way meanwhile. One launch in place of two, no
 // scratch; a is read by each workgroup (the host's rule says where that pays). 64 tokens of 32
-// adapters, k 5120, n 17408, rank 16: 12.4 us instead of 6.3 + 6.5, a call 11.5 instead of 14.3
+// adapters, k 5120, n 17408, rank 16: 12.2 us instead of 6.3 + 6.5, a call 11.5 instead of 14.3
 // (with 512 threads and loads of 2 steps ahead 12.8, of 3 to 5 13.0 to 13.6). One token, k and
 // n 4096, rank 8: 7.4 us instead of 4.8 + 3.3, a call 10.8 instead of 15.0.
 template <typename T, int RB>
