@@ -109,14 +109,17 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan,
     data = plan.data
     if data.device != dev:
         raise ValueError("all tensors must be on the same GPU")
-    if data.dtype != torch.uint8 or data.dim() != 1 or not data.is_contiguous() or data.shape[0] < plan_bytes(T, R):
+    if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() < plan_bytes(T, R):
         raise ValueError("plan.data must be lora_plan's")
     basep = bs = 0
     if base is not None:
         basep, bs = _rows(base, "base", code, dev, T, N)
     if out is None:
-        out = x.new_empty((T, N))
-    outp, os = _rows(out, "out", code, dev, T, N)
+        # like `base` where that is as it should be: 0.9 us, not 1.5
+        out = torch.empty_like(base) if base is not None and base.is_contiguous() else x.new_empty((T, N))
+        outp, os = out.data_ptr(), N
+    else:
+        outp, os = _rows(out, "out", code, dev, T, N)
     sp = 0 if scales is None else _array(scales, "scales", torch.float32, dev, R)
     rp = 0 if ranks is None else _array(ranks, "ranks", torch.int32, dev, R)
     need = workspace_bytes(T, K, N, R, rank, _W._num_cus(dev))

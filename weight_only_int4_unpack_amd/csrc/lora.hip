@@ -558,7 +558,7 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
 // scratch; a is read by each workgroup (the host's rule says where that pays). 64 tokens of 32
 // adapters, k 5120, n 17408, rank 16: 12.2 us instead of 6.3 + 6.5, a call 11.5 instead of 14.3
 // (with 512 threads and loads of 2 steps ahead 12.8, of 3 to 5 13.0 to 13.6). One token, k and
-// n 4096, rank 8: 7.4 us instead of 4.8 + 3.3, a call 10.8 instead of 15.0.
+// n 4096, rank 8: 7.2 us instead of 4.8 + 3.3, a call 9.6 instead of 15.0.
 template <typename T, int RB>
 __global__ __launch_bounds__(lora_once_threads(RB)) void once_kernel(LoraParams p) {
   constexpr int kThreads = lora_once_threads(RB);
