@@ -139,7 +139,7 @@ def _call(fn, dev, *args):
     """One library call on the current stream of `dev`."""
     index = dev.index
     stream = torch._C._cuda_getCurrentRawStream(index)   # without a Stream object: 0.1 us, not 1.9
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():              # 0.1 us, not 0.25
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):

@@ -74,9 +74,11 @@ def _pool(pool: PagePool, dev) -> tuple:
     if refs.dim() != 1 or table.dim() != 2 or lens.dim() != 1:
         raise ValueError("a pool has refs [pages], block_table [rows, table_pages] and lens [rows]")
     rows, entries = table.shape
-    if table.dtype != torch.int32 or table.device != dev or (table.stride(1) != 1 and entries > 1):
+    stride, one = table.stride()
+    if table.dtype != torch.int32 or table.device != dev or (one != 1 and entries > 1):
         raise ValueError("block_table must be int32 [rows, table_pages] on one GPU, its last dimension contiguous")
-    stride = max(table.stride(0), entries) if rows <= 1 else table.stride(0)
+    if rows <= 1:
+        stride = entries                    # no other row to go to
     return (_array(refs, "refs", torch.int32, dev, refs.shape[0]), table.data_ptr(),
             _array(lens, "lens", torch.int32, dev, rows), refs.shape[0], stride, rows, entries, size, 0)
 
