@@ -55,7 +55,8 @@ def test_opcheck():
             (ops.verify_drafts, (*a[:3], 8, *a[3:6], None, None)),
             (ops.verify_drafts, (*a[:3], 8, *a[3:5], None, a[0].softmax(-1), torch.ones(5, device="cuda"))),
             (ops.pages_resize, (*a[6:9], 16, rows, rows)), (ops.pages_fork, (*a[6:9], 16, rows, rows + 5)),
-            (ops.kv_copy_pages, (*lists, pages, pages + 2)), (ops.kv_copy_pages, (*([c[0].half()] for c in lists[:2]), [], [], pages, pages + 2)),
+            (ops.kv_copy_pages, (*lists, pages, pages + 2)),
+            (ops.kv_copy_pages, (*([c[0].half()] for c in lists[:2]), [], [], pages, pages + 2)),
             (ops.lora_plan, (index, 3)), (ops.lora, (x, la, lb, plan, None, None, None))]:
         torch.library.opcheck(op.default, args, test_utils=utils)
     tokens, path, counts = ops.verify_drafts(*a[:3], 8, *a[3:6])

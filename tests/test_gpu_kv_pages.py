@@ -125,6 +125,24 @@ def test_a_long_list_and_a_large_pool():
     equal(pool, o)
 
 
+@pytest.mark.parametrize("others", [0, 1, 70])
+def test_long_rows(others):
+    # more pages than threads, one sequence or several at a time
+    rows, entries, page = 4 + 2 * others, 5000, 16
+    o = O.Pool([0] * 30000, [[-1] * entries for _ in range(rows)], [0] * rows, page)
+    pool, _ = on_gpu(o)
+    short = list(range(4, 4 + others))
+    steps = [("resize", [0, 3, *short], [entries * page - 3, 2000 * page, *[37 * page + i for i in short]]),
+             ("fork", [0, 3, *short], [1, 2, *[i + others for i in short]]),
+             ("resize", [1, 0, *short], [1500 * page + 1, 0, *[5 * i for i in short]]),
+             ("resize", [2, 3, 1], [0, 0, entries * page])]
+    for kind, a, b in steps:
+        got = (paging.pages_fork if kind == "fork" else paging.pages_resize)(pool, ints(a), ints(b))
+        assert lists(got) == (o.fork(a, b) if kind == "fork" else o.resize(a, b))
+        assert all(lists(got)[0])
+        equal(pool, o)
+
+
 def test_entries_that_are_no_pages():
     # a table with entries outside the pool: counted as no page, never followed
     o = O.Pool([1, 0, 0, 5], [[99, -7, 0], [3, 1 << 30, -1], [-1, -1, -1]], [40, 20, 0], 16)

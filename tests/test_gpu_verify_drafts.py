@@ -103,6 +103,17 @@ def test_rows_of_draft_probabilities_that_lie_apart():
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("mode", ["given", "tree", "drawn"])
+def test_rows_of_more_spans_than_a_sequence_has_waves(mode, dtype):
+    # 96 to 600 sequences leave each 5 workgroups to one, of 8 waves, for 20 spans of 1024
+    for seed, sequences in enumerate((96, 250, 600)):
+        g = np.random.default_rng(seed)
+        news = [int(n) for n in g.integers(1, 4, sequences)]
+        c = make(seed + 30, news, 20003, dtype, mode == "tree", mode == "drawn", temps=list(g.choice([0.7, 1.0], sequences)))
+        same(call(c), want(c))
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
 @pytest.mark.parametrize("mode", ["given", "drawn"])
 def test_the_largest_vocabulary_and_most_nodes(mode, dtype):
     c = make(8, [3, 0, 5], 1 << 20, dtype, False, mode == "drawn", temps=[1.0, 1.0, 0.5], pad=3)

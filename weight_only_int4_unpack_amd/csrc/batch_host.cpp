@@ -39,7 +39,8 @@ w4a16_status verify_workspace(int64_t tokens, int64_t vocab, int32_t sequences, 
   if (tokens > kMaxGrid * (kVerifyThreads / 64) / chunks)
     return report(W4A16_ERR_SHAPE, "%lld tokens of %lld logits are too many for one launch", (long long)tokens,
                   (long long)vocab);
-  *bytes = tokens == 0 ? 0 : kCounterBytes + tokens * chunks * (int64_t)sizeof(VerifyChunk) + sequences * verify_spans(vocab) * (int64_t)24;
+  const int64_t sums = tokens * chunks * (int64_t)sizeof(VerifyChunk) + (int64_t)sequences * verify_spans(vocab) * 24;
+  *bytes = tokens == 0 ? 0 : kCounterBytes + sums;
   return W4A16_OK;
 }
 
@@ -156,7 +157,7 @@ int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int32_t rank, i
 //   1 token, 16 ranks: k 1024 7.1, 4.9; 4096 8.8, 6.9; 8192 9.2, 9.3; 12288 9.8, 11.8
 //   64 tokens, 32 adapters of 16: k 1024 8.2, 5.4; 4096 10.7, 8.1; 8192 12.3, 10.7; 16384 15.4, 16.5
 //   1 token, 32 ranks: k 1024 7.9, 5.2; 4096 9.8, 8.5; 8192 10.2, 12.3
-//   1 token, 64 ranks: k 1024 10.5, 7.8; 2048 11.0, 9.2; 4096 11.9, 12.5
+//   1 token, 64 ranks: k 1024 10.5, 7.8; 4096 11.9, 12.5
 // 200 tokens, 64 adapters, k 1024, 6144 columns a workgroup: 16 ranks 15.9, 14.2, 64 ranks 37.2, 42.8.
 constexpr int kOnceSteps = 4;
 constexpr int64_t kOnceMaxColumns = 4096;
