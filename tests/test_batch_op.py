@@ -148,3 +148,26 @@ def test_a_traced_graph_keeps_one_node_each_and_its_sizes_free():
 def test_fakes_refuse_malformed_calls(call):
     with FakeTensorMode(), pytest.raises(ValueError):
         call()
+
+
+@pytest.mark.parametrize("made_for,rows", [(200, 6), (2, 64), (7, 6), (5, 6), (65, 64)])
+def test_a_plan_of_another_step_is_refused(made_for, rows):
+    # 64 rows and 2, or 200 and 6, have plans whose memory is large enough for each other
+    with FakeTensorMode():
+        plan = batch_op.lora_plan(empty(made_for, dtype=I32), 3)
+        with pytest.raises(ValueError, match=f"{made_for} tokens and 3 adapters, not {rows} and 3"):
+            lora(T=rows, plan=plan)
+        with pytest.raises(ValueError, match="the plan is for"):
+            lora(T=made_for, R=4, plan=plan)
+        assert lora(T=made_for, plan=plan).shape == (made_for, 72)
+
+
+def test_a_traced_graph_ties_the_plan_to_the_rows():
+    def product(x, a, b, index):
+        return batch_op.lora(x, a, b, batch_op.lora_plan(index, a.shape[0]))
+    args = [torch.zeros(s).bfloat16() for s in ((12, 64), (3, 8, 64), (3, 72, 8))]
+    gm = make_fx(product, tracing_mode="symbolic")(*args, torch.zeros(12, dtype=I32))
+    rows = next(n for n in gm.graph.nodes if n.op == "placeholder").meta["val"].shape[0]
+    assert not isinstance(rows, int)
+    with pytest.raises(ValueError, match="the plan is for"):
+        make_fx(product, tracing_mode="symbolic")(*args, torch.zeros(11, dtype=I32))

@@ -127,3 +127,14 @@ def test_a_generation_equals_its_text_scored_alone(cache, temperature):
 
 def test_example_with_all_options_runs():
     example().main(["--steps", "3", "--adapters", "2", "--samples", "2", "--temperature", "0.7"])
+
+
+@pytest.mark.parametrize("made_for,rows", [(200, 6), (2, 64)])
+def test_a_plan_of_another_step_is_refused(made_for, rows):
+    x, la, lb, index = sizes(rows, 2, "cuda")[14:]
+    plan = batch_op.lora_plan(torch.zeros(made_for, dtype=torch.int32, device="cuda"), 3)
+    for lora in (batch_op.lora, adapters.lora):
+        with pytest.raises(ValueError, match="the plan is for"):
+            lora(x, la, lb, plan)
+    assert torch.equal(batch_op.lora(x, la, lb, batch_op.lora_plan(index, 3)),
+                       adapters.lora(x, la, lb, adapters.lora_plan(index, 3)))

@@ -209,12 +209,14 @@ def lora_plan(index: torch.Tensor, adapters: int) -> _L.LoraPlan:
 @torch.library.custom_op("w4a16::lora", mutates_args=())
 def _lora_op(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: torch.Tensor,
              base: torch.Tensor | None = None, scales: torch.Tensor | None = None,
-             ranks: torch.Tensor | None = None) -> torch.Tensor:
-    return _L.lora(x, a, b, _L.LoraPlan(plan, x.shape[0], a.shape[0]), base, scales, ranks)
+             ranks: torch.Tensor | None = None, plan_tokens: int | None = None,
+             plan_adapters: int | None = None) -> torch.Tensor:
+    return _L.lora(x, a, b, _L.LoraPlan(plan, x.shape[0] if plan_tokens is None else plan_tokens,
+                                        a.shape[0] if plan_adapters is None else plan_adapters), base, scales, ranks)
 
 
 @_lora_op.register_fake
-def _lora_fake(x, a, b, plan, base=None, scales=None, ranks=None):
+def _lora_fake(x, a, b, plan, base=None, scales=None, ranks=None, plan_tokens=None, plan_adapters=None):
     _need(x.dim() == 2 and a.dim() == 3 and b.dim() == 3,
           "x must be [tokens, k], a [adapters, rank, k], b [adapters, n, rank]")
     _need(x.dtype in _FLOATS, "x must be float16 or bfloat16")
@@ -222,6 +224,8 @@ def _lora_fake(x, a, b, plan, base=None, scales=None, ranks=None):
     _check_list(a, "a", x.dtype, R, rank, x.shape[1])
     _check_list(b, "b", x.dtype, R, N, rank)
     _need(plan.dim() == 1 and plan.dtype == torch.uint8, "plan must be lora_plan's")
+    _need((plan_tokens is None or plan_tokens == x.shape[0]) and (plan_adapters is None or plan_adapters == R),
+          f"the plan is for {plan_tokens} tokens and {plan_adapters} adapters, not {x.shape[0]} and {R}")
     if base is not None:
         _check_list(base, "base", x.dtype, x.shape[0], N)
     if scales is not None:
@@ -234,6 +238,6 @@ def _lora_fake(x, a, b, plan, base=None, scales=None, ranks=None):
 def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, plan: _L.LoraPlan,
          base: torch.Tensor | None = None, scales: torch.Tensor | None = None,
          ranks: torch.Tensor | None = None) -> torch.Tensor:
-    """``adapters.lora`` through ``torch.ops.w4a16.lora``."""
-    _need(plan.adapters == a.shape[0], f"the plan is for {plan.adapters} adapters, not {a.shape[0]}")
-    return torch.ops.w4a16.lora(x, a, b, plan.data, base, scales, ranks)
+    """``adapters.lora`` through ``torch.ops.w4a16.lora``, which sees the plan's memory alone and is told
+    what it is for (``plan_tokens``, ``plan_adapters``; a call without them vouches for x's and a's)."""
+    return torch.ops.w4a16.lora(x, a, b, plan.data, base, scales, ranks, plan.tokens, plan.adapters)
