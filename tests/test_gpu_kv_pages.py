@@ -380,3 +380,20 @@ def test_captured_and_replayed():
             for x, y in zip(c, w):
                 assert y is None or torch.equal(x, y)
         torch.zeros(1000, device="cuda").sum().item()    # eager work between the replays
+
+
+def test_lists_that_are_views_of_the_pool():
+    # the parents of rows 1 and 2 stand in their own lengths, which the call changes: 0, then 40
+    o = O.Pool([0] * 12, [[-1] * 4 for _ in range(5)], [0] * 5, 16)
+    pool, _ = on_gpu(o)
+    paging.pages_resize(pool, ints([0, 3]), ints([40, 5]))
+    o.resize([0, 3], [40, 5])
+    got = lists(paging.pages_fork(pool, pool.lens[1:3], ints([1, 2])))
+    assert got == o.fork([0, 0], [1, 2]) and got[0] == [1, 1]
+    equal(pool, o)
+    # every row at the length that it has: those that share a partly filled page get their own
+    assert lists(paging.pages_resize(pool, ints(range(5)), pool.lens)) == o.resize(list(range(5)), list(o.lens))
+    equal(pool, o)
+    # row 4 is empty: its length is the number of the row to be freed
+    assert lists(paging.pages_resize(pool, pool.lens[4:], ints([0]))) == o.resize([0], [0])
+    equal(pool, o)

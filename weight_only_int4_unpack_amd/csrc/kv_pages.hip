@@ -123,21 +123,21 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
   __syncthreads();
   const Look first_look = look(p.refs, p.pages, 0, tid);   // on its way while the changes are read
   uint32_t need[kEach], carry = 0;
-  int old_len[kEach], new_len[kEach], src[kEach], entry[kEach];
+  int old_len[kEach], new_len[kEach], src[kEach], entry[kEach], from[kEach];
   bool good[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     if (e * kPagesThreads >= p.count) break;
     const int i = tid + e * kPagesThreads;
     need[e] = 0;
-    old_len[e] = new_len[e] = entry[e] = 0;
+    old_len[e] = new_len[e] = entry[e] = from[e] = 0;
     src[e] = -1;
     good[e] = false;
     if (i < p.count) {
       const int row = l.row[i];
       bool ok = row >= 0 && row < p.rows && l.entry[i] == 0;
       if constexpr (FORK) {
-        const int parent = p.from[i];
+        const int parent = from[e] = p.from[i];
         ok = ok && parent >= 0 && parent < p.rows && parent != row;
         if (ok) {
           const int held = p.lens[row];
@@ -226,9 +226,11 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     p.src[i] = ok ? src[e] : -1;
     if (!FORK && ok && src[e] >= 0) release(src[e]);
     if (ok) p.lens[l.row[i]] = new_len[e];
-    // pages: [first, last) of this row are taken back, or of the parent's row shared
+    // pages: [first, last) of this row are taken back, or of the parent's row shared. The lists are
+    // read no more: they may be views of the lengths, which change here.
     if (FORK) {
       l.entry[i] = ok ? new_len[e] >> p.page_shift : 0;
+      l.upto[i] = from[e];
     } else {
       l.entry[i] = pages_of(new_len[e]);
       l.upto[i] = ok ? pages_of(old_len[e]) : 0;
@@ -242,7 +244,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
     const int row = l.row[i];
     if (row < 0) continue;
     if constexpr (FORK) {
-      const int parent = p.from[i];
+      const int parent = (int)l.upto[i];
       for (int k = tid % lanes; k < l.entry[i]; k += lanes) {
         const int page = entry_of(parent, k);
         entry_of(row, k) = page;
