@@ -706,7 +706,7 @@ typedef struct {
 w4a16_status w4a16_kv_copy_pages(const w4a16_kv_copy_pages_t* args, void* stream);
 
 typedef struct {
-  const w4a16_kv_cache_t* caches; /* as above */
+  const w4a16_kv_cache_t* caches; /* as above, no two of their arrays in the same memory */
   const int32_t* block_table; /* [sequences, table_pages], as for w4a16_tree_attention, but no two
                                  sequences in one row */
   const int32_t* kv_lens;   /* [sequences]: cached tokens, the new ones (the last) included */

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import batch_oracle as O
-from weight_only_int4_unpack_amd import attn, paging
+from weight_only_int4_unpack_amd import attn, batch_op, paging
 
 pytestmark = pytest.mark.gpu
 FORMATS = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8, "fp16": torch.float16, "bf16": torch.bfloat16}
@@ -397,3 +397,26 @@ def test_lists_that_are_views_of_the_pool():
     # row 4 is empty: its length is the number of the row to be freed
     assert lists(paging.pages_resize(pool, pool.lens[4:], ints([0]))) == o.resize([0], [0])
     equal(pool, o)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+def test_arrays_that_share_memory_are_copied_but_not_compacted(fmt):
+    # one workgroup would move what another has moved already
+    c, d = caches(2, 6, 2, 64, 16, fmt)
+    part = lambda x, i: None if x is None else x[i:i + 3]                            # noqa: E731
+    cut = lambda i: attn.KVCache(*(part(x, i) for x in c))                           # noqa: E731
+    args = ints([[0, 1, 2]]), ints([40]), ints([0, 30]), ints([list(range(1, 13))]), ints([12])
+    for shared in ([c, c], [c, d, c], [c, d._replace(v=c.k)], [c._replace(v=c.k)], [cut(0), cut(2)]):
+        group = paging.cache_group(shared)
+        assert not group.apart
+        with pytest.raises(ValueError, match="share memory"):
+            paging.kv_compact(group, *args)
+        with pytest.raises(ValueError, match="share memory"):
+            batch_op.kv_compact(group, *args)
+    if fmt == "e4m3":
+        assert not paging.cache_group([c, d._replace(k_scale=c.v_scale)]).apart
+    paging.kv_copy_pages(paging.cache_group([c, c]), ints([1]), ints([4]))
+    assert all(torch.equal(x[1].view(torch.uint8), x[4].view(torch.uint8)) for x in c if x is not None)
+    # halves of one array lie side by side
+    assert paging.cache_group([cut(0), cut(3)]).apart
+    run_compact([cut(0), cut(3)], np.array([[2, 0, 1]]), 16, [40], [30], np.array([list(range(1, 13))]), [12])

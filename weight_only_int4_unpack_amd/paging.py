@@ -42,9 +42,11 @@ class PagePool(NamedTuple):
 
 
 class CacheGroup(NamedTuple):
-    """Caches of one geometry (a model's layers), checked once, as the library takes them."""
+    """Caches of one geometry (a model's layers), checked once, as the library takes them; ``apart``:
+    no two of their arrays share memory."""
     caches: tuple[KVCache, ...]
     fields: ctypes.Array
+    apart: bool = True
 
 
 def page_pool(pages: int, rows: int, table_pages: int, page_size: int = 64, device="cuda") -> PagePool:
@@ -52,6 +54,12 @@ def page_pool(pages: int, rows: int, table_pages: int, page_size: int = 64, devi
     return PagePool(torch.zeros(pages, dtype=torch.int32, device=device),
                     torch.full((rows, table_pages), -1, dtype=torch.int32, device=device),
                     torch.zeros(rows, dtype=torch.int32, device=device), page_size)
+
+
+def _apart(addresses: list[int], nbytes: int) -> bool:
+    """Whether arrays of that many bytes at the addresses lie beside each other."""
+    addresses = sorted(addresses)
+    return nbytes == 0 or all(y - x >= nbytes for x, y in zip(addresses, addresses[1:]))
 
 
 def cache_group(caches: Sequence[KVCache]) -> CacheGroup:
@@ -66,7 +74,10 @@ def cache_group(caches: Sequence[KVCache]) -> CacheGroup:
     if any(f[4:] != fields[0][4:] or c.k.dtype != caches[0].k.dtype for f, c in zip(fields, caches)):
         raise ValueError("the caches of a group must have one shape and dtype")
     held = b"".join(_FIELDS.pack(*f) for f in fields)
-    return CacheGroup(caches, (ctypes.c_char * len(held)).from_buffer_copy(held))
+    k, _, scale, _ = caches[0]
+    apart = _apart([x for f in fields for x in f[:2]], k.numel() * k.element_size()) and \
+        (scale is None or _apart([x for f in fields for x in f[2:4]], scale.numel() * 4))
+    return CacheGroup(caches, (ctypes.c_char * len(held)).from_buffer_copy(held), apart)
 
 
 def _pool(pool: PagePool, dev) -> tuple:
@@ -139,8 +150,10 @@ def kv_compact(group: CacheGroup, block_table: torch.Tensor, kv_lens: torch.Tens
     ``q_starts[b + 1] - q_starts[b]`` of ``kv_lens[b]``: those that ``path`` (int32
     ``[sequences, width]``, ascending) names in its first ``counts[b]`` (int32) entries, as
     ``scoring.verify_drafts`` returns them, move to the front of the new ones in every
-    cache of the group. Returns the new lengths, int32 ``[sequences]``. ``block_table``, ``kv_lens``
-    and ``q_starts`` as for ``tree_attention``, with a row for each sequence."""
+    cache of the group, whose arrays have to lie apart. Returns the new lengths, int32 ``[sequences]``.
+    ``block_table``, ``kv_lens`` and ``q_starts`` as for ``tree_attention``, with a row for each sequence."""
+    if not group.apart:
+        raise ValueError("arrays of the group's caches share memory, where tokens would move twice")
     dev = group.caches[0].k.device
     if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev:
         raise ValueError("block_table must be int32 [sequences, pages] on the caches' device")
