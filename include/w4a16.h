@@ -713,7 +713,7 @@ typedef struct {
   const int32_t* q_starts;  /* [sequences + 1]: where each sequence's new tokens start */
   const int32_t* path;      /* [sequences, width]: the new tokens to keep, ascending */
   const int32_t* counts;    /* [sequences]: how many */
-  int32_t* new_lens;        /* [sequences], not kv_lens itself */
+  int32_t* new_lens;        /* [sequences], apart from every array that is read */
   int64_t table_stride;
   int32_t sequences;
   int32_t table_pages;

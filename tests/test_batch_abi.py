@@ -234,3 +234,21 @@ def test_cpu_tensors_are_refused():
     for fn in (paging.pages_resize, paging.pages_fork):
         with pytest.raises(ValueError, match="same GPU"):
             fn(pool, z(1, **i32), z(1, **i32))
+
+
+@pytest.mark.parametrize("name,count", [("table", 7 * 8 + 8), ("lens", 8), ("starts", 9), ("path", 8 * 4), ("counts", 8)])
+@pytest.mark.parametrize("group", [1, 70])
+def test_new_lengths_are_apart_from_what_is_read(name, count, group):
+    # 8 sequences: arrays that end where the new lengths start, or start where those end, are apart
+    at, size = 16 * P, dict(table=7 * 8 + 8, lens=8, starts=9, path=8 * 4, counts=8)
+    call = lambda new: _compact([_cache()] * group, B=8, new=new,                                      # noqa: E731
+                                **{n: at if n == name else 32 * P + i * P for i, n in enumerate(size)})
+    for inside in (at, at + 4, at + 4 * (count - 1), at - 4 * 7):
+        assert call(inside) == W.ERR_SHAPE and "new_lens" in W.last_error()
+    if not HAS_GPU:
+        assert call(at + 4 * count) == call(at - 4 * 8) == W.ERR_DEVICE
+
+
+def test_arrays_of_no_entries_share_nothing():
+    if not HAS_GPU:
+        assert _compact(new=2 * P, path=2 * P, width=0) == _compact(new=2 * P, table=2 * P, entries=0) == W.ERR_DEVICE

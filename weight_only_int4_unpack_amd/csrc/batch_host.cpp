@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "batch_internal.h"
 #include "serve_checks.h"
@@ -119,6 +120,11 @@ int fill_addresses(const w4a16_kv_cache_t* caches, int32_t first, int32_t count,
     to->at[i] = CacheAddresses{(char*)c.k, (char*)c.v, (char*)c.k_scale, (char*)c.v_scale};
   }
   return n;
+}
+
+bool overlap(const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) {
+  const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
+  return nx > 0 && ny > 0 && a < b + (uintptr_t)ny * 4 && b < a + (uintptr_t)nx * 4;
 }
 
 int element_bytes(int32_t format) { return format == W4A16_KV_SAME ? 2 : 1; }
@@ -315,7 +321,14 @@ w4a16_status w4a16_kv_compact(const w4a16_kv_compact_t* a, void* stream) {
   if (!aligned(a->block_table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->q_starts, 4) || !aligned(a->path, 4) ||
       !aligned(a->counts, 4) || !aligned(a->new_lens, 4))
     return report(W4A16_ERR_ALIGN, "arrays must be aligned to their elements");
-  if (a->new_lens == a->kv_lens) return report(W4A16_ERR_SHAPE, "new_lens must be apart from kv_lens");
+  // other workgroups, and the launches of later caches, read these after the lengths are written
+  const int64_t B = a->sequences, width = a->width;
+  const int64_t entries = a->table_pages ? (B - 1) * a->table_stride + a->table_pages : 0;
+  using Read = std::pair<const int32_t*, int64_t>;
+  for (const auto& [x, count] : {Read{a->kv_lens, B}, Read{a->q_starts, B + 1}, Read{a->counts, B},
+                                 Read{a->path, B * width}, Read{a->block_table, entries}})
+    if (overlap(a->new_lens, B, x, count))
+      return report(W4A16_ERR_SHAPE, "new_lens must be apart from block_table, kv_lens, q_starts, path and counts");
   const bool none = a->count == 0 || view.pages == 0;
   CompactParams p{};
   CacheList<kGroupCaches> caches{};
