@@ -386,3 +386,67 @@ def test_refusals():
     with pytest.raises(RuntimeError, match="2\\^20"):
         scoring.verify_drafts(torch.zeros((1, (1 << 20) + 1), dtype=torch.bfloat16).cuda(), cuda([0]),
                               cuda([0, 1], torch.int32), 1, cuda([0.0]), cuda([0.0]))
+
+
+# Rows that are summed again: where a random number is next to the border that it is compared with (fp32 sums
+# cannot tell).
+def beside_borders(c, seed, accept):
+    """Sets each random number on the walk to the fp32 number below the oracle's border (the token is accepted) or to
+    the one from the border on (it is not), as accept() says; a walk ends where it says no to all of a node's."""
+    g, last = np.random.default_rng(seed), np.float32(1 - 2.0 ** -24)
+    for b, n in enumerate(c["news"]):
+        lo, node = c["starts"][b], 0
+        while node is not None:
+            w = O.weights(c["held"][lo + node], 1.0 if c["temps"] is None else float(np.float32(c["temps"][b])))
+            left, gone, at, node = w.sum(), [], node, None
+            for k in range(at + 1, n):
+                if c["parents"][lo + k] != at or c["ids"][lo + k] in gone:
+                    continue
+                t = c["ids"][lo + k]
+                q = 1.0 if c["q"] is None else float(c["q"][lo + at, t])
+                border = float(w[t] / (left * q))
+                up = np.float32(border)
+                up = up if float(up) >= border else np.nextafter(up, np.float32(2), dtype=np.float32)
+                if border > float(last) or accept(g):
+                    c["u"][lo + k] = min(np.nextafter(up, np.float32(0), dtype=np.float32), last)
+                    node = k
+                    break
+                c["u"][lo + k] = up
+                if c["q"] is not None:
+                    break
+                gone.append(t)
+                left -= w[t]
+    return c
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("mode", ["given", "tree", "drawn"])
+@pytest.mark.parametrize("vocab,sequences,pad", [(20003, 1, 0), (20003, 40, 3), (20003, 300, 0), (151667, 1, 5), (151667, 6, 0),
+                                                 (1 << 20, 1, 0)])
+def test_random_numbers_beside_the_borders_of_large_rows(vocab, sequences, pad, mode, dtype):
+    news = [6] if sequences == 1 else [2 + b % 5 if sequences < 300 else 2 + b % 2 for b in range(sequences)]
+    temps = None if sequences == 6 else [0.8, 1.0, 1.7][:len(news)] + [1.0] * (len(news) - 3)
+    for seed, share in ((0, 1.0), (1, 0.7), (2, 0.0))[:1 if vocab == 1 << 20 else 3]:
+        c = make(seed, news, vocab, dtype, mode == "tree", mode == "drawn", temps, pad)
+        beside_borders(c, seed, lambda g: g.random() < share)
+        got = call(c)
+        same(got, want(c))
+        if mode == "given" and share in (0.0, 1.0):
+            assert got[2].tolist() == (news if share else [1] * sequences)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("vocab", [151667, 1 << 20])
+@pytest.mark.parametrize("tokens", [1, 2, 1 << 17])
+def test_nothing_above_the_draft_in_a_large_row(tokens, vocab, dtype):
+    # equal weights of a power of two of tokens, and a draft that equals them exactly; a number that is not below 1
+    g = np.random.default_rng(tokens)
+    place = np.sort(g.choice(vocab, tokens, replace=False))
+    x = torch.full((2, vocab), -math.inf)
+    x[:, place] = 1.5
+    q = torch.zeros((2, vocab))
+    q[:, place] = 1.0 / tokens
+    for final in (0.0, 0.3, 0.5, 1 - 2.0 ** -24):
+        t, p, n = scoring.verify_drafts(x.to(DT[dtype]).cuda(), cuda([0, int(place[0])]), cuda([0, 2], torch.int32), 2,
+                                        cuda([0.0, 1.0]), cuda([final]), draft_probs=q.cuda())
+        assert n.tolist() == [1] and t[0].tolist() == [place[int(final * tokens)], -1]
