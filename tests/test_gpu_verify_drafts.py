@@ -389,7 +389,7 @@ def test_refusals():
 
 
 # Rows that are summed again: where a random number is next to the border that it is compared with (fp32 sums
-# cannot tell).
+# cannot tell), and where the draft follows the model so closely that little but roundings remains.
 def beside_borders(c, seed, accept):
     """Sets each random number on the walk to the fp32 number below the oracle's border (the token is accepted) or to
     the one from the border on (it is not), as accept() says; a walk ends where it says no to all of a node's."""
@@ -433,6 +433,51 @@ def test_random_numbers_beside_the_borders_of_large_rows(vocab, sequences, pad, 
         same(got, want(c))
         if mode == "given" and share in (0.0, 1.0):
             assert got[2].tolist() == (news if share else [1] * sequences)
+
+
+def follows(seed, vocab, dtype, draws, temperature):
+    """`draws` sequences of one drafted token, which is rejected: the draft is the model's distribution as fp32 numbers but
+    for two tokens, one with more and, at the end, one with less. Below the latter lies what fp32 rounded away, token
+    by token, and final random numbers in the middle of a token's share of it."""
+    c = make(seed, [2], vocab, dtype, temps=[temperature])
+    held = c["held"][0]
+    for t in (vocab // 3, vocab - 2):
+        held[t] = held.max() if t == vocab // 3 else held[vocab // 3]
+    c["logits"][0] = torch.from_numpy(held)
+    c["held"][0] = c["logits"][0].float().cpu().numpy()
+    p = O.weights(c["held"][0], float(np.float32(temperature)))
+    p /= p.sum()
+    q = p.astype(np.float32)
+    q[vocab // 3] += np.float32(0.25)
+    q[vocab - 2] = 0.0
+    r = np.fmax(p - q.astype(np.float64), 0.0)
+    up = np.cumsum(r)
+    # shares that final numbers of 24 bits can name, and that are wider than what both sides' sums differ by
+    places = np.flatnonzero(r / 2 > up * 2.0 ** -24 + np.cumsum(p) * 2.0 ** -45)
+    first, wide = int(np.flatnonzero(r)[0]), vocab - 2
+    assert r[first] > p[first] * 2.0 ** -44
+    picks = [first, wide, *np.random.default_rng(seed).choice(places, draws - 2)]
+    final = np.array([(up[t] - r[t] / 2) / up[-1] for t in picks]).astype(np.float32)
+    final[0] = 0.0
+    c.update(news=[2] * draws, starts=np.arange(draws + 1) * 2, parents=[-1, 0] * draws, ids=[0, vocab // 3] * draws,
+             u=np.full(2 * draws, 1 - 2.0 ** -24, np.float32), final=final, temps=[temperature] * draws,
+             q=np.tile(np.stack([q, q]), (draws, 1)), held=np.tile(c["held"], (draws, 1)),
+             logits=c["logits"].repeat(draws, 1))
+    return c, picks
+
+
+# A share is what is left of a probability less its rounding, some 2^-26 of it. The kernel's exponential is right to
+# 2^-46, the row's sum of them too, and the oracle's to far more: the sum of the shares up to a token is off by
+# at most 2^-45 of the probabilities up to there.
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("vocab,draws", [(700, 60), (5003, 60), (151667, 12)])
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+def test_a_draft_that_follows_the_model(vocab, draws, temperature, dtype):
+    for seed in range(3):
+        c, picks = follows(seed, vocab, dtype, draws, temperature)
+        expected = want(c)
+        assert [t[0] for t in expected[0]] == picks and expected[2] == [1] * draws
+        same(call(c), expected)
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))

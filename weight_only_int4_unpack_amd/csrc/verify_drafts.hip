@@ -12,11 +12,18 @@
 //
 // What needs fp64: a draw is a border in a cumulative sum over 2^17 terms, and rounding moves
 // one draw in 1 / (terms x rounding), a hundred with fp32 and 10^8 with sums that are right
-// to 2^-46. A token is accepted by one comparison; where the row's fp32 sum is too near to
-// tell (2^-16 of it, some 16 times its error), the row is summed in fp64 and compared again.
-// Where a drawn token was rejected, max(w - S q, 0) is summed with S of the first kernel,
-// together with the sum Q of the q under w: with the exact S, known when all spans are, the
-// sum is that plus (S_first - S) Q (what changes sides on the way is 2^-24 of 2^-24).
+// to 2^-46. The first kernel's sums are off by less than 2^-18: 56 half steps of fp32, 31 for a
+// lane's additions, 23 for the three roundings of exponents that are log2 of the chunk, 11, in
+// the mean over its weights at most, 2 for the exponential. A token is accepted by one comparison;
+// where that sum is too near to tell (2^-16 of it), the row is summed in fp64 and compared again.
+//
+// Where a drawn token was rejected, the remainder R(S) = sum of max(w - S q, 0) is needed before S is
+// known exactly. It is convex in S, and linear but for kinks where w = S q for a token: it is
+// summed at two points around the first kernel's sum S', S' (1 -+ 2^-21), and taken between them on the
+// chord. The slope at the upper one, the sum of q where w is above S q, says how far the chord may be off.
+// Where that is above 2^-34 of the remainder (a draft that follows the model to 2^-20 in much of
+// its mass, or a remainder of almost nothing), or a random number near 0 asks for more, the last
+// workgroup sums the remainder again with the exact S.
 #include <climits>
 
 #include "batch_internal.h"
@@ -83,6 +90,17 @@ __device__ __forceinline__ double weigh_near(float x, double m, const Scale& s) 
   return exp2_of(__builtin_fmax((double)x - m, s.least), s.c);
 }
 constexpr double kNothing = 0x1p-900;
+// The sign, the exponent and 20 bits of x.
+__device__ __forceinline__ int leading(double x) {
+  typedef int Halves __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(Halves, x).y;
+}
+
+// Drafted rows: how far the two points are, and what may be wrong of the remainder, and of it up to the border.
+constexpr double kAside = 0x1p-21, kRemainder = 0x1p-34, kUpto = 0x1p-20;
+// max(x, 0) of x <= 1, 0 for NaN: a modifier of the instruction that x comes from.
+__device__ __forceinline__ double above_0(double x) { return __builtin_fmin(__builtin_fmax(x, 0.0), 1.0); }
+
 // The value of the lane whose number differs in one bit (or, inside 8 and 16 lanes, the
 // mirrored one: enough where whole groups agree already).
 template <int STEP>
@@ -366,8 +384,8 @@ __device__ __forceinline__ double load_shared(const double* from) {
 }
 
 // A chain of loads and barriers: one sequence over 32000 logits 12.5 us. 64 chains over 151667
-// with drafts 27.4, of which 58 MB of rows and drafts take 14.5 (HBM 11; a row's loads are two
-// vectors ahead of the weighing: a chunk's at once take 3 us more).
+// with drafts 28.5, of which 58 MB of rows and drafts take 15.5 (HBM 11; a row's loads are two
+// vectors ahead of the weighing: a chunk's at once take 3 us more; the remainder at S' alone 1.1 less).
 template <typename E>
 __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   using C = Chunk<E>;
@@ -521,9 +539,10 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
   };
 
   // Stages that end in spans' sums, with one copy of code: the walk up to a row whose sum is
-  // too near to tell; the last row; that row again with all its weights, where the remainder
-  // is empty.
-  enum { kWalking, kDrawing, kDrawingAll };
+  // too near to tell; the last row; its remainder above a draft again, with the row's exact sum; that
+  // row with all its weights, where the remainder is empty.
+  enum { kWalking, kDrawing, kDrawingExact, kDrawingAll };
+  constexpr int kNoSpan = -1, kInexact = -2;   // in place of a span: nothing is left; the remainder may be wrong
   int stage = kWalking, len = 1, last = 0;
   for (;;) {
     int node = 0, from = wave, step = kWaves, dropped = 0;
@@ -608,20 +627,22 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
       from = group * kWaves + wave;
       step = p.groups * kWaves;
       dropped = dropped_;
-      q = drawn_ ? p.probs + (lo + last) * p.probs_stride : nullptr;
     }
+    if ((stage == kDrawing || stage == kDrawingExact) && drawn_) q = p.probs + (lo + last) * p.probs_stride;
     double* shared = p.over + (int64_t)b * 3 * p.spans;
 
     // Of each span, by a wave: the sum of the weights without the rejected tokens, and, over
-    // a draft, the sum of max(w - near q, 0) and of the q under w. Loads of two vectors are
-    // on their way while one is weighed.
+    // a draft, the remainder at two points around `near`, as the upper's and the difference; what
+    // that is above the slope's is summed over the wave's spans. Loads of two vectors are on
+    // their way while one is weighed.
     auto weigh_spans = [&](auto drafted) {
       constexpr bool kDraft = decltype(drafted)::value;
       using P = Part<E, kDraft>;
       constexpr int kVecs = kVerifySpan / (64 * L::kVec);
       const int count = from < p.spans ? (p.spans - from + step - 1) / step : 0;
-      double s = 0.0, over = 0.0;
-      float under = 0.0f;                // only meets the difference of two sums of the row
+      const double aside = stage == kDrawing ? kAside * near : 0.0, lower = near - aside, upper = near + aside;
+      double s = 0.0, over = 0.0, over_lower = 0.0, bent = 0.0;
+      float under = 0.0f;
       auto fetch = [&](P& part, int unit) {
         const int span = from + unit / kVecs * step;
         part.fetch(row, q, p.vocab, span * kVerifySpan - C::lead(row) + unit % kVecs * (64 * L::kVec), lane);
@@ -641,35 +662,39 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
           s += y;
           if constexpr (kDraft) {
             const float d = part.draft[e / 4][e % 4];
-            const double r = __builtin_fma(-near, (double)d, y);
-            over += __builtin_fmax(r, 0.0);
-            under += r > 0.0 ? d : 0.0f;
+            const double r = above_0(__builtin_fma(-upper, (double)d, y));
+            over += r;
+            over_lower += above_0(__builtin_fma(-lower, (double)d, y));
+            under += leading(r) != 0 ? d : 0.0f;
           }
         }
       };
       auto finish = [&](int unit) {
         const int k = from + unit / kVecs * step;
         if (k >= p.spans) return;
-        s = wave_sum(s);
-        s = s > kNothing ? s : 0.0;
-        double below = 0.0;
+        f32x2 slope{0.0f, 0.0f};
         if constexpr (kDraft) {
+          const double step_up = over_lower - over;
+          slope.x = (float)wave_sum(step_up);
+          bent += __builtin_fma(-2.0 * aside, (double)under, step_up);
+          if (k + step >= p.spans) slope.y = (float)wave_sum(bent);
           over = wave_sum(over);
           over = over > kNothing ? over : 0.0;
-          below = wave_sum((double)under);
         }
+        s = wave_sum(s);
+        s = s > kNothing ? s : 0.0;
         if (lane == 0) {
           if (stage == kDrawing) {
             store_shared(shared + k, s);
             if constexpr (kDraft) {
               store_shared(shared + p.spans + k, over);
-              store_shared(shared + 2 * p.spans + k, below);
+              store_shared(shared + 2 * p.spans + k, __builtin_bit_cast(double, slope));
             }
           } else {
-            w.mass[k] = s;
+            w.mass[k] = kDraft ? over : s;
           }
         }
-        s = over = 0.0;
+        s = over = over_lower = 0.0;
         under = 0.0f;
       };
       P part[2];
@@ -705,16 +730,18 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         if (arrived != p.groups - 1) return;
       }
       constexpr int kEachSpan = (kVerifyMaxSpans + kWalkThreads - 1) / kWalkThreads;
-      double over[kEachSpan], under[kEachSpan];
+      double over[kEachSpan];
+      f32x2 slope[kEachSpan];
 #pragma unroll
       for (int e = 0; e < kEachSpan; ++e) {
         const int k = tid + e * kWalkThreads;
-        over[e] = under[e] = 0.0;
+        over[e] = 0.0;
+        slope[e] = f32x2{0.0f, 0.0f};
         if (k >= p.spans) continue;
         w.mass[k] = load_shared(shared + k);
         if (q) {
           over[e] = load_shared(shared + p.spans + k);
-          under[e] = load_shared(shared + 2 * p.spans + k);
+          slope[e] = __builtin_bit_cast(f32x2, load_shared(shared + 2 * p.spans + k));
         }
       }
       __syncthreads();
@@ -726,12 +753,20 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         }
         __syncthreads();
         total = target_;
+        // what may be wrong: the difference to the slope, and as much as its 16 additions may hide
+        const double by = 0.5 + (near - total) / (2.0 * kAside * near);
+        double wrong = 0.0;
 #pragma unroll
         for (int e = 0; e < kEachSpan; ++e) {
           const int k = tid + e * kWalkThreads;
-          if (k < p.spans) w.mass[k] = __builtin_fmax(__builtin_fma(near - total, under[e], over[e]), 0.0);
+          if (k < p.spans) w.mass[k] = __builtin_fma(by, (double)slope[e].x, over[e]);
+          wrong += __builtin_fma(0x1p-20, (double)slope[e].x, (double)slope[e].y);
         }
+        wrong = wave_sum(wrong);
+        if (lane == 0) sums_[wave] = wrong;
       }
+    } else if (stage == kDrawingExact) {
+      total = near;
     }
     __syncthreads();
     if (wave == 0) {
@@ -748,7 +783,7 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
         uint64_t passing = __ballot(upto > target && mine > 0.0);
         const bool none = passing == 0;
         if (none) passing = __ballot(mine > 0.0);
-        int span = -1;
+        int span = kNoSpan;
         double before = 0.0;
         if (all > 0.0 && passing != 0) {
           const int owner = none ? 63 - __builtin_clzll(passing) : __builtin_ctzll(passing);
@@ -762,6 +797,13 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
               found = !none && run > target;
             }
           }
+        }
+        if (stage == kDrawing && q) {
+          double wrong = 0.0;
+          for (int i = 0; i < kWaves; ++i) wrong += sums_[i];
+          if (__builtin_fabs(near - total) > kAside * near || wrong > kRemainder * all || wrong > kUpto * target)
+            span = kInexact;
+          if (lane == 0) w.sum[node] = total;
         }
         if (lane == 0) {
           span_ = span;
@@ -825,7 +867,8 @@ __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {
     }
     __syncthreads();
     if (token_ >= 0 || stage == kDrawingAll) break;
-    stage = kDrawingAll;
+    // (a span's remainder may be a rounding alone, of which no token has any)
+    stage = stage == kDrawing && drawn_ && span_ != kNoSpan ? kDrawingExact : kDrawingAll;
   }
   __syncthreads();
   for (int i = tid; i < p.max_q; i += kWalkThreads) {
