@@ -772,7 +772,8 @@ typedef struct {
  *   out[t] = base[t] + scales[i] sum_r v_r b[i, :, r],  v_r = sum_k x[t, k] a[i, r, k],
  * i the token's adapter; without one, out[t] = base[t]. v and the sums are fp32
  * (v meets b as two 16-bit parts, which hold 16 of its bits in bf16 and 22 in
- * fp16), rounded once to the dtype.
+ * fp16, of a row's largest v: what is below 2^-39 of that counts as 0), rounded
+ * once to the dtype. What is not finite in x, a or b comes out as the formula has it.
  * Scratch: a workspace as for w4a16_gemm_ws, of at least w4a16_lora_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.
  */

@@ -366,3 +366,65 @@ def test_refusals():
         adapters.lora(e["x"].cuda(), e["a"][:, :12].contiguous().cuda(), e["b"][:, :, :12].contiguous().cuda(), plan)
     with pytest.raises(RuntimeError, match="k=60"):
         adapters.lora(e["x"][:, :60].contiguous().cuda(), e["a"][:, :, :60].contiguous().cuda(), e["b"].cuda(), plan)
+
+
+def as_infinities(x):
+    """1, -1 and 0 for infinities and finite numbers, NaN as it is."""
+    x = np.asarray(x)
+    return np.where(np.isinf(x), np.sign(x), np.where(np.isnan(x), np.nan, 0.0))
+
+
+@pytest.mark.parametrize("tokens,K", [(1, 264), (20, 264), (20, 20488), (700, 264)])   # one kernel, two, tiles of 64
+@pytest.mark.parametrize("rank", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_what_is_not_finite_in_b(dtype, rank, tokens, K):
+    # v is finite and not 0: an infinity by its sign and b's, NaN where two meet of different signs
+    c = make(30 + rank, tokens, K, 200, 2, rank, dtype, [t % 2 for t in range(tokens)])
+    c["x"][:, 0] = 8                                     # v is 32 or -32, and some
+    c["a"][:, :, 0] = 4 * (-1.0) ** torch.arange(rank)
+    clean = run(c)
+    x, a = f64(c["x"]), f64(c["a"])
+    inf = math.inf
+    places = {3: [(0, 0, inf)], 64: [(1, rank - 1, -inf)], 70: [(0, 1, inf), (0, 2, inf)], 71: [(1, 1, inf), (1, rank - 2, -inf)],
+              130: [(0, rank - 1, math.nan)], 199: [(0, 5, -inf), (1, 7, inf)]}
+    for n, them in places.items():
+        for i, r, value in them:
+            c["b"][i, n, r] = value
+    for i in range(2):                                   # by more than any rounding
+        v, deep = x @ a[i].T, np.abs(x) @ np.abs(a[i]).T
+        assert (np.abs(v) > deep * K * 2.0 ** -23)[i::2].all()
+    y = O.lora(x, a, f64(c["b"]), c["index"], f64(c["base"]), f64(c["scales"]))[0]
+    got = run(c)
+    np.testing.assert_array_equal(as_infinities(got.float().cpu().numpy()), as_infinities(y))
+    same = np.isfinite(y)
+    assert same[:, [0, 65, 198]].all() and np.array_equal(got.float().cpu().numpy()[same], clean.float().cpu().numpy()[same])
+
+
+@pytest.mark.parametrize("tokens", [20, 700])
+@pytest.mark.parametrize("rank", [8, 32, 128])
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_an_infinite_v_by_its_sign_and_bs(dtype, rank, tokens):
+    c = make(40 + rank, tokens, 264, 200, 1, rank, dtype, [0] * tokens)
+    c["x"][5] = 0
+    c["x"][5, 7] = math.inf
+    signs = torch.ones(rank)
+    signs[1] = -1
+    c["a"][0, :, 7] = signs.to(c["a"].dtype)
+    c["b"][0, :50] = (c["b"][0, :50].abs() * signs).to(c["b"].dtype)          # all plus infinity
+    c["b"][0, 50:90] = (-c["b"][0, 50:90].abs() * signs).to(c["b"].dtype)     # all minus
+    c["b"][0, 0, 0] = math.inf                                                # infinity times infinity
+    c["b"][0, 50, 1] = math.inf
+    c["b"][0, 89, rank - 1] = 0.0                                             # infinity times 0
+    y = O.lora(*(f64(c[k]) for k in "xab"), c["index"], f64(c["base"]), f64(c["scales"]))[0][5]
+    expected = as_infinities(y)
+    assert (expected[:50] * expected[51] < 0).all() and expected[50] == expected[51] and np.isnan(expected[89])
+    np.testing.assert_array_equal(as_infinities(run(c)[5].float().cpu().numpy()), expected)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_a_v_of_0_and_an_infinite_b(dtype):
+    c = make(50, 30, 64, 72, 1, 16, dtype, [0] * 30)
+    c["x"][4] = 0
+    c["b"][0, 9, 3] = math.inf
+    got = run(c)
+    assert got[4, 9].isnan() and got[4, [8, 10]].isfinite().all() and got[3, 9].isinf()

@@ -417,6 +417,19 @@ __global__ __launch_bounds__(kLoraDownThreads) void down_kernel(LoraParams p) {
   }
 }
 
+// What is infinite in b meets both parts of v, and the second may be 0 or of the other sign: NaN in place of
+// an infinite sum. Where a sum is NaN (asked here for a wave's) that of the first parts alone stands.
+__device__ __forceinline__ bool any_nan(const f32x4 (&sum)[4]) {
+  const f32x4 all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  const float any = (all.x + all.y) + (all.z + all.w);
+  return __ballot(any != any) != 0;
+}
+__device__ __forceinline__ f32x4 where_nan(f32x4 sum, const f32x4& alone) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = sum[e] != sum[e] ? alone[e] : sum[e];
+  return sum;
+}
+
 // ---- up, small tiles and ranks: a wave takes 64 columns of a tile of 16 tokens at a time. Rank
 // blocks of 16 are one matrix instruction of depth 32, v's high parts in the first half and
 // its low ones in the second; larger ones two for each 32 ranks. b is the left operand, its
@@ -510,6 +523,17 @@ struct Few {
       for (int i = 0; i < kParts; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v[s][i], sum[j]);
+    if (any_nan(sum)) {
+      const bool low = kPacked && group >= 2;
+      const u32x4 none{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 alone{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) alone = mfma<T>(low ? none : c.x[s][j], low ? none : v[s][0], alone);
+        sum[j] = where_nan(sum[j], alone);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f32x8 y = widen8<T>(h.x[i]);
@@ -749,6 +773,21 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p)
       // a lane holds columns 16 j + 4 group .. + 3 of token 16 m + col
 #pragma unroll
       for (int j = 0; j < 4; ++j) *(f32x4*)&turn_y[col * kStrideY + 16 * j + 4 * group] = sum[j];
+      if (any_nan(sum)) {
+        const bool low = kPacked && group >= 2;
+        const u32x4 none{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 alone{0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const u32x4 v = *(const u32x4*)&vs[(16 * m + col) * kStride + (kPacked ? group * 8 : 32 * s + group * 8)];
+            alone = mfma<T>(low ? none : bs[s][j], low ? none : v, alone);
+          }
+          f32x4& y = *(f32x4*)&turn_y[col * kStrideY + 16 * j + 4 * group];
+          y = where_nan(y, alone);
+        }
+      }
       wave_sync();
       Held now = held[m];
       held[m] = load_base(n0 + kUpColumns, m);
