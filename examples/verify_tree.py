@@ -95,16 +95,22 @@ class Decoder:
 
     def resize(self, lens):
         """Pages for `lens` tokens of the first sequences."""
-        served, src, dst = batch_op.pages_resize(self.pool, ints(range(len(lens)), torch.int32), lens)
-        batch_op.kv_copy_pages(self.group, src, dst)
-        return served
+        rows = range(len(lens))
+        self.copy(rows, *batch_op.pages_resize(self.pool, ints(rows, torch.int32), lens))
 
     def fork(self, parents, children):
         """Continues sequences as others too."""
         self.adapter[ints(children)] = self.adapter[ints(parents)]
-        served, src, dst = batch_op.pages_fork(self.pool, ints(parents, torch.int32), ints(children, torch.int32))
+        self.copy(children, *batch_op.pages_fork(self.pool, ints(parents, torch.int32), ints(children, torch.int32)))
+
+    def copy(self, rows, served, src, dst):
+        """The pages that a change of `rows` has to copy. A sequence that was not served has no place for
+        its tokens: nothing may run on it."""
         batch_op.kv_copy_pages(self.group, src, dst)
-        return served
+        if not served.all():
+            short, free = [r for r, ok in zip(rows, served.tolist()) if not ok], int((self.pool.refs == 0).sum())
+            raise RuntimeError(f"no room for sequences {short}: up to {self.s.pages_each * self.s.page} tokens each, "
+                               f"{free} pages free")
 
     def __call__(self, tokens, sequence, places, positions, kv_lens, q_starts, max_q, mask=None):
         """Logits after each of `tokens`, whose keys and values go to `places`."""

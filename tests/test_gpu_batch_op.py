@@ -138,3 +138,23 @@ def test_a_plan_of_another_step_is_refused(made_for, rows):
             lora(x, la, lb, plan)
     assert torch.equal(batch_op.lora(x, la, lb, batch_op.lora_plan(index, 3)),
                        adapters.lora(x, la, lb, adapters.lora_plan(index, 3)))
+
+
+@pytest.mark.parametrize("prompt,steps", [(20, 30), (40, 1)])
+def test_a_text_that_does_not_fit_stops_the_example(prompt, steps):
+    # two pages a sequence: the text grows past them, or never fits
+    m = example()
+    s = m.Sizes(pages_each=2)
+    model = m.Decoder(s, 2, None)
+    with pytest.raises(RuntimeError, match=r"no room for sequences \[0\]: up to 32 tokens each"):
+        m.generate(model, [list(range(prompt)), [1]], steps, drafts=False)
+
+
+def test_a_fork_without_free_pages_stops_the_example():
+    m = example()
+    model = m.Decoder(m.Sizes(pages_each=2), 4, None)
+    model.resize(m.ints([20, 32, 0, 0], torch.int32))
+    model.pool.refs[model.pool.refs == 0] = 1                 # others hold the rest
+    with pytest.raises(RuntimeError, match=r"no room for sequences \[2\]: .* 0 pages free"):
+        model.fork([0, 1], [2, 3])
+    assert model.pool.lens.tolist() == [20, 32, 0, 32]        # full pages alone are shared
