@@ -123,9 +123,9 @@ def _lists(group: _P.CacheGroup):
     return (list(k), list(v), *([] if ks[0] is None else list(s) for s in (ks, vs)))
 
 
-def _group(k, v, k_scales, v_scales) -> _P.CacheGroup:
+def _caches(k, v, k_scales, v_scales) -> list[_A.KVCache]:
     none = [None] * len(k)
-    return _P.cache_group(list(map(_A.KVCache, k, v, k_scales or none, v_scales or none)))
+    return list(map(_A.KVCache, k, v, k_scales or none, v_scales or none))
 
 
 def _check_group(k, v, k_scales, v_scales):
@@ -142,7 +142,8 @@ def _check_group(k, v, k_scales, v_scales):
 @torch.library.custom_op("w4a16::kv_copy_pages", mutates_args=("k", "v", "k_scales", "v_scales"))
 def _copy_op(k: Sequence[torch.Tensor], v: Sequence[torch.Tensor], k_scales: Sequence[torch.Tensor],
              v_scales: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tensor) -> None:
-    _P.kv_copy_pages(_group(k, v, k_scales, v_scales), src, dst)
+    # (a copy does not ask whether the caches lie apart)
+    _P.kv_copy_pages(_P._group(*_P._packed(_caches(k, v, k_scales, v_scales))), src, dst)
 
 
 @_copy_op.register_fake
@@ -161,7 +162,7 @@ def kv_copy_pages(group: _P.CacheGroup, src: torch.Tensor, dst: torch.Tensor) ->
 def _compact_op(k: Sequence[torch.Tensor], v: Sequence[torch.Tensor], k_scales: Sequence[torch.Tensor],
                 v_scales: Sequence[torch.Tensor], block_table: torch.Tensor, kv_lens: torch.Tensor,
                 q_starts: torch.Tensor, path: torch.Tensor, counts: torch.Tensor) -> torch.Tensor:
-    return _P.kv_compact(_group(k, v, k_scales, v_scales), block_table, kv_lens, q_starts, path, counts)
+    return _P.kv_compact(_P.cache_group(_caches(k, v, k_scales, v_scales)), block_table, kv_lens, q_starts, path, counts)
 
 
 @_compact_op.register_fake

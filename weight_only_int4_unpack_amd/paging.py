@@ -15,6 +15,7 @@ captured into a graph; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import NamedTuple, Sequence
 
@@ -56,14 +57,14 @@ def page_pool(pages: int, rows: int, table_pages: int, page_size: int = 64, devi
                     torch.zeros(rows, dtype=torch.int32, device=device), page_size)
 
 
-def _apart(addresses: list[int], nbytes: int) -> bool:
+def _apart(addresses: tuple[int, ...], nbytes: int) -> bool:
     """Whether arrays of that many bytes at the addresses lie beside each other."""
     addresses = sorted(addresses)
-    return nbytes == 0 or all(y - x >= nbytes for x, y in zip(addresses, addresses[1:]))
+    return nbytes == 0 or min(map(operator.sub, addresses[1:], addresses)) >= nbytes
 
 
-def cache_group(caches: Sequence[KVCache]) -> CacheGroup:
-    """The given caches (at least one, on one GPU, alike but for their memory) as a group."""
+def _packed(caches: Sequence[KVCache]) -> tuple[tuple[KVCache, ...], list[tuple]]:
+    """The caches and their fields, checked but for where they lie."""
     caches = tuple(KVCache(*c) for c in caches)
     if not caches:
         raise ValueError("a group needs a cache")
@@ -73,11 +74,21 @@ def cache_group(caches: Sequence[KVCache]) -> CacheGroup:
     fields = [_packed_cache(c, dev) for c in caches]
     if any(f[4:] != fields[0][4:] or c.k.dtype != caches[0].k.dtype for f, c in zip(fields, caches)):
         raise ValueError("the caches of a group must have one shape and dtype")
+    return caches, fields
+
+
+def _group(caches: tuple[KVCache, ...], fields: list[tuple], apart: bool = True) -> CacheGroup:
     held = b"".join(_FIELDS.pack(*f) for f in fields)
-    k, _, scale, _ = caches[0]
-    apart = _apart([x for f in fields for x in f[:2]], k.numel() * k.element_size()) and \
-        (scale is None or _apart([x for f in fields for x in f[2:4]], scale.numel() * 4))
     return CacheGroup(caches, (ctypes.c_char * len(held)).from_buffer_copy(held), apart)
+
+
+def cache_group(caches: Sequence[KVCache]) -> CacheGroup:
+    """The given caches (at least one, on one GPU, alike but for their memory) as a group."""
+    caches, fields = _packed(caches)
+    k, v, k_scale, v_scale, *_ = zip(*fields)
+    one = caches[0]
+    return _group(caches, fields, _apart(k + v, one.k.numel() * one.k.element_size()) and (
+        one.k_scale is None or _apart(k_scale + v_scale, one.k_scale.numel() * 4)))
 
 
 def _pool(pool: PagePool, dev) -> tuple:
