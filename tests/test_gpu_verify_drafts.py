@@ -495,3 +495,48 @@ def test_nothing_above_the_draft_in_a_large_row(tokens, vocab, dtype):
         t, p, n = scoring.verify_drafts(x.to(DT[dtype]).cuda(), cuda([0, int(place[0])]), cuda([0, 2], torch.int32), 2,
                                         cuda([0.0, 1.0]), cuda([final]), draft_probs=q.cuda())
         assert n.tolist() == [1] and t[0].tolist() == [place[int(final * tokens)], -1]
+
+
+# Of the remainder, some 0.4 of the noise, both sides know 2^-45 of the row's sum: with 2^-10 of noise the sum up to
+# a token is off by at most 2^-33 of it, and a random number is so near to one of 2^14.3 borders with
+# probability 2^-18; 40 draws in a case, 18 cases of the smallest noise: 2^-8 together, for bounds that nothing
+# comes near to (the exponential's errors have both signs).
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("noise", [2.0 ** -3, 2.0 ** -6, 2.0 ** -10])
+@pytest.mark.parametrize("vocab,sequences", [(20003, 40), (20003, 1), (3001, 40)])
+def test_drafts_close_to_the_model(vocab, sequences, noise, dtype):
+    for seed in range(2):
+        g = np.random.default_rng(seed)
+        news = [2 + b % 3 for b in range(sequences)]
+        c = make(seed + 60, news, vocab, dtype, probs=True, temps=list(g.choice([0.7, 1.0, 1.3], sequences)))
+        for b, n in enumerate(news):
+            t = float(np.float32(c["temps"][b]))
+            for i in range(c["starts"][b], c["starts"][b] + n):
+                p = O.weights(c["held"][i], t)
+                p /= p.sum()
+                q = p * np.exp(noise * g.standard_normal(vocab))
+                c["q"][i] = (q / q.sum()).astype(np.float32)
+                if i + 1 < c["starts"][b] + n:
+                    # a token that the draft likes better, which is rejected, or one that it likes less
+                    more = c["q"][i] > p * (1 + 2.0 ** -20)
+                    c["ids"][i + 1] = int(g.choice(np.flatnonzero(more if g.random() < 0.6 else ~more)))
+        c["u"][:] = 1 - 2.0 ** -24
+        expected = want(c)
+        assert sequences == 1 or 1 in expected[2] and max(expected[2]) > 1
+        same(call(c), expected)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("vocab", [5003, 151667])
+def test_every_token_of_a_large_row_rejected(vocab, dtype):
+    # three tokens that can be, and siblings that name them all, with numbers that are not below 1: a draw from all
+    place = [3, vocab // 2, vocab - 1]
+    x = torch.full((4, vocab), -math.inf)
+    x[:, place] = torch.tensor([1.0, 2.0, 0.5])
+    starts, parents = cuda([0, 4], torch.int32), cuda([-1, 0, 0, 0], torch.int32)
+    for last, final in ((1.0, 0.0), (1.0, 0.2), (1.0, 0.5), (1.0, 0.99), (0.5, 0.5)):
+        u = cuda([0.0, 1.0, 1.0, last])
+        t, p, n = scoring.verify_drafts(x.to(DT[dtype]).cuda(), cuda([0, *place]), starts, 4, u, cuda([final]), parents=parents)
+        tokens, path = O.verify(x.numpy(), [0, *place], [-1, 0, 0, 0], u.tolist(), np.float32(final))
+        assert t[0, :int(n)].tolist() == tokens and p[0, :int(n)].tolist() == path
+        assert len(path) == (2 if last < 1 else 1)
