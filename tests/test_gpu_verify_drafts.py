@@ -497,10 +497,10 @@ def test_nothing_above_the_draft_in_a_large_row(tokens, vocab, dtype):
         assert n.tolist() == [1] and t[0].tolist() == [place[int(final * tokens)], -1]
 
 
-# Of the remainder, some 0.4 of the noise, both sides know 2^-45 of the row's sum: with 2^-10 of noise the sum up to
-# a token is off by at most 2^-33 of it, and a random number is so near to one of 2^14.3 borders with
-# probability 2^-18; 40 draws in a case, 18 cases of the smallest noise: 2^-8 together, for bounds that nothing
-# comes near to (the exponential's errors have both signs).
+# The remainder is some 0.4 of the noise; the draft is within 2^-20 of the model for 0.8 2^-20 / noise of its mass.
+# What the kernel leaves to the chord is below 2^-22 of that mass, 2^-36 with the noise of 2^-6, 2^-29 of the
+# remainder: a random number is so near to one of 2^14.3 borders with a probability of 2^-14 (2^-20 with
+# 2^-3; with 2^-10 the remainder is summed again, and 2^-45 of the row's sum is unknown).
 @pytest.mark.parametrize("dtype", sorted(DT))
 @pytest.mark.parametrize("noise", [2.0 ** -3, 2.0 ** -6, 2.0 ** -10])
 @pytest.mark.parametrize("vocab,sequences", [(20003, 40), (20003, 1), (3001, 40)])

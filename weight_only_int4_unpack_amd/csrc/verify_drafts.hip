@@ -21,9 +21,11 @@
 // known exactly. It is convex in S, and linear but for kinks where w = S q for a token: it is
 // summed at two points around the first kernel's sum S', S' (1 -+ 2^-21), and taken between them on the
 // chord. The slope at the upper one, the sum of q where w is above S q, says how far the chord may be off.
-// Where that is above 2^-34 of the remainder (a draft that follows the model to 2^-20 in much of
-// its mass, or a remainder of almost nothing), or a random number near 0 asks for more, the last
-// workgroup sums the remainder again with the exact S.
+// Where that is above 2^-28 of the remainder, a sixteenth of the steps of a random number of 24
+// bits (a draft that follows the model to 2^-20 in some of its mass, or a remainder of almost
+// nothing), or a random number near 0 asks for more, the last workgroup sums the remainder
+// again with the exact S, alone: 68 us more over 151667. Remainders below 2^-12 S come to that,
+// for which few tokens are rejected; above it hardly any.
 #include <climits>
 
 #include "batch_internal.h"
@@ -97,7 +99,7 @@ __device__ __forceinline__ int leading(double x) {
 }
 
 // Drafted rows: how far the two points are, and what may be wrong of the remainder, and of it up to the border.
-constexpr double kAside = 0x1p-21, kRemainder = 0x1p-34, kUpto = 0x1p-20;
+constexpr double kAside = 0x1p-21, kRemainder = 0x1p-28, kUpto = 0x1p-14;
 // max(x, 0) of x <= 1, 0 for NaN: a modifier of the instruction that x comes from.
 __device__ __forceinline__ double above_0(double x) { return __builtin_fmin(__builtin_fmax(x, 0.0), 1.0); }
 
