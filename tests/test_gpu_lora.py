@@ -428,3 +428,20 @@ def test_a_v_of_0_and_an_infinite_b(dtype):
     c["b"][0, 9, 3] = math.inf
     got = run(c)
     assert got[4, 9].isnan() and got[4, [8, 10]].isfinite().all() and got[3, 9].isinf()
+
+
+@pytest.mark.parametrize("T,K", [(1, 64), (20, 20488), (300, 64)])
+@pytest.mark.parametrize("rank", [8, 64])
+def test_bf16_up_to_the_end_of_fp32(rank, T, K):
+    # v between the largest bf16 and the largest fp32 number, a sum that is exact
+    c = make(51, T, K, 72, 1, rank, "bf16", [0] * T, gain=2.0 ** 60)
+    c["x"][:] = 0
+    c["x"][:, 3], c["x"][:, K - 1] = 1.0, 1.0
+    c["a"][:, :, 3], c["a"][:, :, K - 1] = float(torch.finfo(torch.bfloat16).max), 2.0 ** 119
+    c["a"][:, 1::2] *= -1
+    c["b"] = (c["b"].float() * 2.0 ** -60).bfloat16()
+    v = f64(c["x"]) @ f64(c["a"][0]).T
+    assert (np.abs(v) > float(torch.finfo(torch.bfloat16).max)).all() and (np.abs(v) < np.finfo(np.float32).max).all()
+    got = run(c)
+    assert got.isfinite().all()
+    check(got, c)

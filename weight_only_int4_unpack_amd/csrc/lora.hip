@@ -340,7 +340,14 @@ __device__ __forceinline__ float in_parts(f32x8 v, float scale, u32x4* high, u32
         if (__builtin_isfinite(v[e])) v[e] = fminf(fmaxf(v[e], -65504.0f), 65504.0f);
     }
   }
-  const u32x4 h = narrow8<T>(v);
+  f32x8 near = v;
+  if constexpr (T::kCode != W4A16_F16) {
+    // the last step below fp32's end would round to infinity
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (__builtin_isfinite(v[e])) near[e] = fminf(fmaxf(v[e], -0x1.FEp127f), 0x1.FEp127f);
+  }
+  const u32x4 h = narrow8<T>(near);
   const f32x8 wide = widen8<T>(h);
   f32x8 rest;
 #pragma unroll
