@@ -486,16 +486,21 @@ struct Few {
       if (token >= 0 && n0 + 32 * i + group * 8 < n_hi) *(u32x4*)(out + n0 + 32 * i) = h.x[i];
   }
   // past the adapter's own rank: zeros, as 0 x NaN is NaN
+  __device__ __forceinline__ u32x4 load_one(int n0, int s, int j) const {
+    const int n = n0 + (j >> 1) * 32 + (j & 1) * 4 + row;
+    return n < n_hi && rank_at(s) < rank ? load16(b + (int64_t)n * rank_all + rank_at(s)) : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void cut_one(u32x4& x, int s) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (rank_at(s) + e >= rank) x[e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  }
   __device__ __forceinline__ Columns load_b(int n0) const {
     Columns c;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + (j >> 1) * 32 + (j & 1) * 4 + row;
-        c.x[s][j] = u32x4{0, 0, 0, 0};
-        if (n < n_hi && rank_at(s) < rank) c.x[s][j] = load16(b + (int64_t)n * rank_all + rank_at(s));
-      }
+      for (int j = 0; j < 4; ++j) c.x[s][j] = load_one(n0, s, j);
     return c;
   }
   __device__ __forceinline__ void cut_b(Columns& c) const {
@@ -503,10 +508,7 @@ struct Few {
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (rank_at(s) + e >= rank) c.x[s][j][e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+      for (int j = 0; j < 4; ++j) cut_one(c.x[s][j], s);
   }
   // The lane's operands of v, from rows of RB high and RB low parts.
   __device__ __forceinline__ void load_v(const uint16_t* high, const uint16_t* low, u32x4 (&v)[KS][kParts]) const {
@@ -520,7 +522,7 @@ struct Few {
       }
     }
   }
-  __device__ __forceinline__ Held add(Held h, const Columns& c, const u32x4 (&v)[KS][kParts], float factor) const {
+  __device__ __forceinline__ Held add(int n0, Held h, const Columns& c, const u32x4 (&v)[KS][kParts], float factor) const {
     f32x4 sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = f32x4{0, 0, 0, 0};
@@ -530,14 +532,19 @@ struct Few {
       for (int i = 0; i < kParts; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] = mfma<T>(c.x[s][j], v[s][i], sum[j]);
-    if (any_nan(sum)) {
+    if (__builtin_expect(any_nan(sum), 0)) {
+      // (b once more from memory: its registers are free in all other steps)
       const bool low = kPacked && group >= 2;
       const u32x4 none{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f32x4 alone{0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) alone = mfma<T>(low ? none : c.x[s][j], low ? none : v[s][0], alone);
+        for (int s = 0; s < KS; ++s) {
+          u32x4 x = load_one(n0, s, j);
+          cut_one(x, s);
+          alone = mfma<T>(low ? none : x, low ? none : v[s][0], alone);
+        }
         sum[j] = where_nan(sum[j], alone);
       }
     }
@@ -580,16 +587,16 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_kernel(LoraParams p) {
     f.cut_b(c);
     next = f.load_b(n0 + kUpColumns);
     held = f.load_base(n0 + kUpColumns);
-    f.store_out(n0, f.add(now, c, v, factor));
+    f.store_out(n0, f.add(n0, now, c, v, factor));
   }
 }
 
 // ---- both for a few tokens: every workgroup forms v for itself and multiplies it with its own
 // columns, whose first b and base are on their way meanwhile. One launch in place of two, no
 // scratch; a is read by each workgroup (the host's rule says where that pays). 64 tokens of 32
-// adapters, k 5120, n 17408, rank 16: 12.2 us instead of 6.3 + 6.5, a call 11.5 instead of 14.3
+// adapters, k 5120, n 17408, rank 16: 12.7 us instead of 6.3 + 6.5, a call 11.5 instead of 14.3
 // (with 512 threads and loads of 2 steps ahead 12.8, of 3 to 5 13.0 to 13.6). One token, k and
-// n 4096, rank 8: 7.2 us instead of 4.8 + 3.3, a call 9.6 instead of 15.0.
+// n 4096, rank 8: 7.4 us instead of 4.8 + 3.3, a call 9.8 instead of 15.0.
 template <typename T, int RB>
 __global__ __launch_bounds__(lora_once_threads(RB)) void once_kernel(LoraParams p) {
   constexpr int kThreads = lora_once_threads(RB);
@@ -635,7 +642,7 @@ __global__ __launch_bounds__(lora_once_threads(RB)) void once_kernel(LoraParams 
     f.cut_b(c);
     next = f.load_b(n0 + kThreads);
     held = f.load_base(n0 + kThreads);
-    f.store_out(n0, f.add(now, c, v, factor));
+    f.store_out(n0, f.add(n0, now, c, v, factor));
   }
 }
 
@@ -644,7 +651,7 @@ __global__ __launch_bounds__(lora_once_threads(RB)) void once_kernel(LoraParams 
 // whole lines, 8 lanes a row of 64 columns; b and the products are turned in LDS, each wave
 // in a place of its own. Loads return in the order in which they were issued: base is loaded
 // a step of columns ahead, and b of the next columns before the base that is needed after it.
-// 8192 tokens, 17408 columns, rank 64: 122-125 us, 4.6 TB/s of base and out (a copy: 5.2); with
+// 8192 tokens, 17408 columns, rank 64: 123-127 us, 4.6 TB/s of base and out (a copy: 5.2); with
 // operands read straight from memory, whose neighbouring lanes hold different rows, 162 us;
 // with base two steps ahead 127-131. A third wave a SIMD has no registers for it (spills: 157).
 template <typename T, int MT, int RB>
@@ -780,7 +787,7 @@ __global__ __launch_bounds__(kLoraThreads, 2) void up_lines_kernel(LoraParams p)
       // a lane holds columns 16 j + 4 group .. + 3 of token 16 m + col
 #pragma unroll
       for (int j = 0; j < 4; ++j) *(f32x4*)&turn_y[col * kStrideY + 16 * j + 4 * group] = sum[j];
-      if (any_nan(sum)) {
+      if (__builtin_expect(any_nan(sum), 0)) {
         const bool low = kPacked && group >= 2;
         const u32x4 none{0, 0, 0, 0};
 #pragma unroll
