@@ -620,7 +620,8 @@ typedef struct {
  * sums are fp32 where that decides an acceptance beyond doubt, and fp64 in the
  * row that the last token is drawn from and where it does not: of the 2^17
  * borders that a draw falls between, fp32 sums (off by 1e-7) move one under one
- * draw in a hundred.
+ * draw in a hundred. The sum of what is above a draft is right to 2^-28 of it,
+ * where a uniform number of 24 bits has steps of 2^-24, and to 2^-45 of S_i.
  * Scratch: as for w4a16_tree_attention, of at least
  * w4a16_verify_drafts_workspace_bytes.
  * Errors: NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, DEVICE, HIP.
@@ -708,7 +709,7 @@ w4a16_status w4a16_kv_copy_pages(const w4a16_kv_copy_pages_t* args, void* stream
 typedef struct {
   const w4a16_kv_cache_t* caches; /* as above, no two of their arrays in the same memory */
   const int32_t* block_table; /* [sequences, table_pages], as for w4a16_tree_attention, but no two
-                                 sequences in one row */
+                                 sequences in one row, and new tokens in pages that no other holds */
   const int32_t* kv_lens;   /* [sequences]: cached tokens, the new ones (the last) included */
   const int32_t* q_starts;  /* [sequences + 1]: where each sequence's new tokens start */
   const int32_t* path;      /* [sequences, width]: the new tokens to keep, ascending */

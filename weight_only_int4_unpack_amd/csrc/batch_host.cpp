@@ -163,8 +163,10 @@ int32_t lora_splits(int64_t tokens, int32_t adapters, int32_t k, int32_t rank, i
 //   1 token, 16 ranks: k 1024 7.1, 4.9; 4096 8.8, 6.9; 8192 9.2, 9.3; 12288 9.8, 11.8
 //   64 tokens, 32 adapters of 16: k 1024 8.2, 5.4; 4096 10.7, 8.1; 8192 12.3, 10.7; 16384 15.4, 16.5
 //   1 token, 32 ranks: k 1024 7.9, 5.2; 4096 9.8, 8.5; 8192 10.2, 12.3
-//   1 token, 64 ranks: k 1024 10.5, 7.8; 4096 11.9, 12.5
+//   1 token, 64 ranks: k 1024 10.5, 7.8; 2048 11.0, 9.2; 4096 11.9, 12.5
 // 200 tokens, 64 adapters, k 1024, 6144 columns a workgroup: 16 ranks 15.9, 14.2, 64 ranks 37.2, 42.8.
+// More tiles move the crossing up, which the rule leaves aside: 64 tokens, 32 adapters of 64, k 5120 20.6,
+// 19.0; 200 tokens, 64 adapters of 16, k 12288 18.3, 16.0.
 constexpr int kOnceSteps = 4;
 constexpr int64_t kOnceMaxColumns = 4096;
 int32_t lora_once_columns(int64_t tokens, int32_t k, int32_t n, int32_t adapters, int32_t rank, int num_cus) {

@@ -13,7 +13,7 @@ namespace {
 using namespace serve;
 
 // ---- forks and resizes
-// One sequence forked in 3 ways 6.2 us, 10 in 4 each 7.7; resized 4.0 and 6.0: waits are 75 %.
+// One sequence forked in 3 ways 6.1 us, 10 in 4 each 7.5; resized 4.0 and 5.7: waits are 75 %.
 // (The first look at the counts only when their number is known, and a wave for each row in
 // turn: 9.1 and 7.2 us for the 40.)
 // Every listed change needs `need` new pages, which go into consecutive entries of its row
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_kernel(PagesParams p) {
 // ---- copies of pages
 // A workgroup copies kCopyEach * 256 units of 16 bytes of one pair in one cache; k, v and
 // their scales count as one run of units. 40 pages of 64 tokens in 16 caches of 8 bf16 heads
-// of 128: 56 us, 6.0 TB/s read and written.
+// of 128: 57 us, 5.9 TB/s read and written.
 template <int N>
 __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyPagesParams p, CacheList<N> caches) {
   uint32_t at = blockIdx.x;
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(CopyPagesParam
 // order. Place j is read, if at all, as the source of a token before the j-th (a path
 // ascends): by the same thread, before it writes there. Loads of a few tokens are ahead of
 // their stores: they only get earlier. 64 sequences, up to 5 tokens each, 32 caches of 8 e4m3
-// heads of 128: 8.2 us, 2.3 TB/s; one sequence 4: path, table and tokens follow one another
+// heads of 128: 8.5 us, 2.2 TB/s; one sequence 4: path, table and tokens follow one another
 // (waits: 72 %).
 constexpr int kCompactList = 64;
 template <int N>

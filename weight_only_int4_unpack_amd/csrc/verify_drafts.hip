@@ -385,8 +385,8 @@ __device__ __forceinline__ double load_shared(const double* from) {
   return __builtin_bit_cast(double, __hip_atomic_load((const uint64_t*)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
-// A chain of loads and barriers: one sequence over 32000 logits 12.5 us. 64 chains over 151667
-// with drafts 28.5, of which 58 MB of rows and drafts take 15.5 (HBM 11; a row's loads are two
+// A chain of loads and barriers: one sequence over 32000 logits 13 us. 64 chains over 151667
+// with drafts 29.0, of which 58 MB of rows and drafts take 15.5 (HBM 11; a row's loads are two
 // vectors ahead of the weighing: a chunk's at once take 3 us more; the remainder at S' alone 1.1 less).
 template <typename E>
 __global__ __launch_bounds__(kWalkThreads, 4) void walk_kernel(VerifyParams p) {

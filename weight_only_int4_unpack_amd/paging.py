@@ -162,7 +162,8 @@ def kv_compact(group: CacheGroup, block_table: torch.Tensor, kv_lens: torch.Tens
     ``[sequences, width]``, ascending) names in its first ``counts[b]`` (int32) entries, as
     ``scoring.verify_drafts`` returns them, move to the front of the new ones in every
     cache of the group, whose arrays have to lie apart. Returns the new lengths, int32 ``[sequences]``.
-    ``block_table``, ``kv_lens`` and ``q_starts`` as for ``tree_attention``, with a row for each sequence."""
+    ``block_table``, ``kv_lens`` and ``q_starts`` as for ``tree_attention``, with a row for each sequence and its new
+    tokens in pages that no other holds (as ``pages_resize`` leaves them)."""
     if not group.apart:
         raise ValueError("arrays of the group's caches share memory, where tokens would move twice")
     dev = group.caches[0].k.device
